@@ -6,10 +6,13 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
-SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("dsa_sparse_attn.cu", "dsa_topk.cu", "dsa_kv_insert.cu")]
+SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("dsa_sparse_attn.cu", "dsa_kv8_attn.cu", "dsa_kv8_insert.cu",
+                                                      "dsa_topk.cu", "dsa_kv_insert.cu", "dsa_page_map.cu")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libdsa_sparse_attn.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
@@ -23,21 +26,29 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build the library")
 
 
-def build(verbose: bool = False, extra_flags=None) -> str:
-    """Build the shared library if any source is newer than it; return its path."""
-    deps = SOURCES + [os.path.join(PKG_DIR, "csrc", "ptx_sm103.cuh"), os.path.join(INCLUDE, "dsa_sparse_attn.h"),
-                      os.path.join(INCLUDE, "dsa_topk.h"), os.path.join(INCLUDE, "dsa_kv_insert.h"),
-            os.path.abspath(__file__)]
-    if os.path.exists(LIB_PATH) and all(os.path.getmtime(LIB_PATH) >= os.path.getmtime(d) for d in deps):
-        return LIB_PATH
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-I", INCLUDE, "-o", tmp, *SOURCES, *(extra_flags or [])]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+
+
+def build(verbose: bool = False, extra_flags=None) -> str:
+    """Build the shared library if any source is newer than it; return its path.  The
+    sources are compiled at the same time, one nvcc each, and then linked."""
+    headers = [os.path.join(INCLUDE, h) for h in sorted(os.listdir(INCLUDE)) if h.endswith(".h")]
+    deps = SOURCES + headers + [os.path.join(PKG_DIR, "csrc", "ptx_sm103.cuh"), os.path.abspath(__file__)]
+    if os.path.exists(LIB_PATH) and all(os.path.getmtime(LIB_PATH) >= os.path.getmtime(d) for d in deps):
+        return LIB_PATH
+    flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, *(extra_flags or [])]
+    nvcc = nvcc_path()
+    tmp = LIB_PATH + f".tmp{os.getpid()}"
+    with tempfile.TemporaryDirectory(prefix="dsa_build_") as objs:
+        jobs = [(src, os.path.join(objs, os.path.basename(src) + ".o")) for src in SOURCES]
+        with ThreadPoolExecutor(len(jobs)) as pool:
+            list(pool.map(lambda job: _run([nvcc, *flags, "-c", "-o", job[1], job[0]], verbose), jobs))
+        _run([nvcc, *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *[obj for _, obj in jobs]], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -1,0 +1,894 @@
+// Attention over the paged 8-bit cache (include/dsa_kv8.h).
+//
+// A call is a one-CTA plan kernel and the attention kernels as its dependents.
+//
+// Rows.  The query rows of one request and KV head are its q_len queries times the
+// h_q / h_kv heads that share the KV head: row = query * group + head of the group, so
+// every cached token is read once for all of them.  Requests with at most 8 * NT rows
+// (decode, drafted tokens) go to rows_kernel below; the others are cut into tiles.
+//
+// Scales.  With S = q . code_k summed in fp32 and x = S * k_scale * softmax_scale * log2 e,
+// the kernels take t = x + log2(v_scale) and w = 2^(t - m), m a running maximum of t.  Then
+// O = sum w * code_v is the weighted sum with every page's value scale in it, and
+// l = sum w / v_scale is the softmax's sum: w is at most 2^8 (the maximum may lag by 8),
+// whatever the scales' magnitudes, so that it fits fp16.
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <mutex>
+#include <stdint.h>
+
+#include "dsa_kv8.h"
+#include "ptx_sm103.cuh"
+
+namespace dsa_kv8 {
+
+constexpr int STEP = 16;          // cached tokens of one step of a warp; every page size is a multiple
+constexpr int MAX_ROWS = 32;      // most query rows of a request in rows_kernel
+constexpr int TILE_ROWS = 32;     // query rows of a tile
+constexpr int ROW_WARPS = 4;      // warps of a rows_kernel CTA
+constexpr int CTAS_PER_SM = 4;    // the plan's CTAs per SM
+constexpr int MIN_STEPS = 8;      // a CTA's least share, in steps: two for each warp
+constexpr int PLAN_THREADS = 1024;
+constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
+constexpr float LAG = 8.0f;
+
+struct Share {   // where a CTA's share of the steps begins
+  int req, head;
+  long long step;
+};
+
+struct Header {
+  uint32_t status;
+  int n_tiles;
+  long long share;   // steps of every CTA
+};
+
+struct Params {
+  const uint16_t* q;
+  const uint8_t *k_pool, *v_pool;
+  const float *k_scale, *v_scale;
+  const int32_t *table, *cu_q, *kv_lens;
+  uint16_t* out;
+  float* lse;
+  long long q_ld, q_hd, out_ld, out_hd, table_ld;
+  Header* header;
+  Share* shares;
+  int* arrived;
+  int2* tiles;
+  float* partial;
+  int n_tokens, n_req, h_q, h_kv, group, n_pages, page_shift, cap, max_q_len, window, fp16;
+  int small_rows;   // requests with at most this many rows go to rows_kernel
+  int n_shares, max_tiles;
+  float scale_log2;   // softmax_scale * log2 e
+};
+
+struct Request {
+  int q0, q_len, kv;
+  __device__ __forceinline__ int rows(const Params& P) const { return q_len * P.group; }
+};
+
+__device__ __forceinline__ Request request(const Params& P, int r) {
+  Request a;
+  a.q0 = min(max(P.cu_q[r], 0), P.n_tokens);
+  a.q_len = min(max(P.cu_q[r + 1], a.q0), P.n_tokens) - a.q0;
+  a.kv = min(max(P.kv_lens[r], 0), P.cap);
+  return a;
+}
+
+// The cached tokens [lo, hi) that the query positions [p0, p1] may see, lo rounded down to
+// a step.  Never empty: a row that sees nothing is still computed, and its result is 0.
+struct Span {
+  int lo, steps;
+};
+__device__ __forceinline__ Span span(const Params& P, const Request& a, int i0, int i1) {
+  const int p0 = a.kv - a.q_len + i0, p1 = a.kv - a.q_len + i1;
+  Span s;
+  s.lo = P.window > 0 ? max(p0 - P.window + 1, 0) & ~(STEP - 1) : 0;
+  s.steps = max((p1 + 1 - s.lo + STEP - 1) / STEP, 1);
+  if (p1 + 1 <= s.lo) s.steps = 1;
+  return s;
+}
+
+// ------------------------------------------------------------------------------ plan
+// The steps of the small requests, all heads of all requests in a row, are cut into equal
+// shares, one for each CTA: a share may begin and end inside a request, and the CTAs are
+// done at the same time whatever the lengths.  The tiles of the other requests are listed.
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params P) {
+  extern __shared__ long long s_step[];   // [n_req + 1] exclusive prefix of the steps
+  long long* s_tile = s_step + P.n_req + 1;   // [n_req + 1] of the tiles
+  __shared__ long long s_step_warp[32], s_tile_warp[32];
+  __shared__ uint32_t s_bad;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = P.n_req;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  for (int r = tid; r < n; r += PLAN_THREADS) {
+    const Request a = request(P, r);
+    const int rows = a.rows(P);
+    long long steps = 0;
+    int tiles = 0;
+    if (a.q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
+    else if (rows > P.small_rows) tiles = (rows + TILE_ROWS - 1) / TILE_ROWS;
+    else if (rows > 0) steps = span(P, a, 0, a.q_len - 1).steps;
+    s_step[r] = steps;
+    s_tile[r] = tiles;
+  }
+  __syncthreads();
+  const int per = ((n + PLAN_THREADS - 1) / PLAN_THREADS) | 1;   // odd: no bank conflicts
+  const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
+  long long st = 0, ti = 0;
+  for (int r = r0; r < r1; ++r) {
+    st += s_step[r];
+    ti += s_tile[r];
+  }
+  long long st_in = st, ti_in = ti;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xFFFFFFFFu, st_in, o), b = __shfl_up_sync(0xFFFFFFFFu, ti_in, o);
+    if (lane >= o) {
+      st_in += a;
+      ti_in += b;
+    }
+  }
+  if (lane == 31) {
+    s_step_warp[w] = st_in;
+    s_tile_warp[w] = ti_in;
+  }
+  __syncthreads();
+  long long st_ex = st_in - st, ti_ex = ti_in - ti, all = 0, all_tiles = 0;
+#pragma unroll
+  for (int u = 0; u < 32; ++u) {
+    if (u < w) {
+      st_ex += s_step_warp[u];
+      ti_ex += s_tile_warp[u];
+    }
+    all += s_step_warp[u];
+    all_tiles += s_tile_warp[u];
+  }
+  for (int r = r0; r < r1; ++r) {
+    const long long a = s_step[r], b = s_tile[r];
+    s_step[r] = st_ex;
+    s_tile[r] = ti_ex;
+    st_ex += a;
+    ti_ex += b;
+  }
+  if (tid == 0) {
+    s_step[n] = all;
+    s_tile[n] = all_tiles;
+  }
+  __syncthreads();
+
+  const long long total = all * P.h_kv;
+  const long long share = max((total + P.n_shares - 1) / P.n_shares, (long long)MIN_STEPS);
+  for (int b = tid; b < P.n_shares; b += PLAN_THREADS) {
+    Share s;
+    s.req = -1;
+    s.head = 0;
+    s.step = 0;
+    const long long f = b * share;
+    if (f < total) {
+      int lo = 0, hi = n;   // the request with s_step[lo] * h_kv <= f < s_step[lo + 1] * h_kv
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_step[mid] * P.h_kv <= f) lo = mid; else hi = mid;
+      }
+      const long long steps = s_step[lo + 1] - s_step[lo], rest = f - s_step[lo] * P.h_kv;
+      s.req = lo;
+      s.head = (int)(rest / steps);
+      s.step = rest - s.head * steps;
+    }
+    P.shares[b] = s;
+    P.arrived[b] = 0;
+  }
+  // ascending cu_q cannot give more tiles than the list has room for
+  const int n_tiles = (int)min(all_tiles, (long long)P.max_tiles);
+  for (int i = tid; i < n_tiles; i += PLAN_THREADS) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_tile[mid] <= i) lo = mid; else hi = mid;
+    }
+    P.tiles[i] = make_int2(lo, (int)(i - s_tile[lo]));
+  }
+  if (tid == 0) {
+    P.header->status = s_bad;
+    P.header->n_tiles = n_tiles;
+    P.header->share = share;
+  }
+}
+
+// ------------------------------------------------------------------------------ rows
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 sums
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 matrix of 16-bit values held two to a lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+__device__ __forceinline__ float2 unpack(uint32_t w, int fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack(float a, float b, int fp16) {
+  if (fp16) return dsa::pack_f16x2(a, b);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// One warp's share of the steps of a unit (one request or tile, one KV head).
+//
+// The two products are taken with the cached tokens as the rows of the matrix instruction:
+// S^T[16 tokens x 8 rows] = K Q^T and O^T[16 dims x 8 rows] += V^T P^T, so that 8 query
+// rows fill an instruction (16 would be needed with the roles exchanged), and codes go
+// from global memory to the operand's registers without shared memory: the contraction's
+// order is free, so a lane's 16 consecutive key bytes are its operands of four
+// instructions, and its 16 consecutive value bytes of four tokens are its operands of
+// eight.  P^T comes from S^T's registers by an 8 x 8 transpose.
+//
+// Lane r * 4 + c (r = lane / 4, c = lane % 4) holds, for tile nt of 8 rows, the scores of
+// tokens r and r + 8 for rows 8 nt + 2c and + 1; and O^T of dims r * (D / 8) + 0 .. D / 8 - 1
+// for the same rows.
+template <int D, int NT>
+struct RowState {
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+};
+
+template <int D>
+struct Codes {
+  uint4 k[2][D / 64];   // token r (0) and r + 8 (1): bytes 64 j + 16 c ..
+  uint4 v[4];           // tokens 2c, 2c + 1, 2c + 8, 2c + 9: bytes r * (D / 8) .. (8 of them for D = 64)
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void rows_steps(const Params& P, int req, int head, int lo, int seen_lo, int hi, int step0,
+                                           int step1, int stride, const uint32_t (&qf)[NT == 1 ? D / 16 : 1][2],
+                                           const uint16_t* s_q, const float (&qs)[NT][2], const int (&pos)[NT][2],
+                                           int pos_min, int pos_max, RowState<D, NT>& R) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int page_mask = (1 << P.page_shift) - 1;
+  const int32_t* table = P.table + req * P.table_ld;
+  // the page of a step, -1 where there is none
+  auto page_of = [&](int s) -> int {
+    const int base = lo + s * STEP;
+    if (s >= step1 || base >= hi) return -1;
+    const int p = __ldg(table + (base >> P.page_shift));
+    return (p < 0 || p >= P.n_pages) ? -1 : p;
+  };
+  auto row_of = [&](int page, int s) -> long long {
+    return (((long long)page * P.h_kv + head) << P.page_shift) + ((lo + s * STEP) & page_mask);
+  };
+  Codes<D> C;
+  auto load_k = [&](int page, int s) {
+    if (page < 0) return;
+    const uint8_t* k = P.k_pool + (row_of(page, s) + r) * D + 16 * c;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      C.k[0][j] = dsa::ldg_nc(k + 64 * j);
+      C.k[1][j] = dsa::ldg_nc(k + 8 * D + 64 * j);
+    }
+  };
+  auto load_v = [&](int page, int s) {
+    if (page < 0) return;
+    const uint8_t* v = P.v_pool + (row_of(page, s) + 2 * c) * D + r * (D / 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* at = v + ((i & 1) + (i >> 1) * 8) * D;
+      if (D == 128) {
+        C.v[i] = dsa::ldg_nc(at);
+      } else {
+        const uint2 x = dsa::ldg_nc_v2(at);
+        C.v[i] = make_uint4(x.x, x.y, 0u, 0u);
+      }
+    }
+  };
+  auto load_scale = [&](const float* scale, int page) -> float {
+    return page < 0 ? 1.0f : __ldg(scale + (long long)page * P.h_kv + head);
+  };
+
+  int page = page_of(step0), page_next = page_of(step0 + stride);
+  load_k(page, step0);
+  load_v(page, step0);
+  float ks = load_scale(P.k_scale, page), vs = load_scale(P.v_scale, page);
+  for (int s = step0; s < step1; s += stride) {
+    const int page_after = page_of(s + 2 * stride);
+    const float ks_next = load_scale(P.k_scale, page_next), vs_next = load_scale(P.v_scale, page_next);
+    if (page < 0) {
+      load_k(page_next, s + stride);
+      load_v(page_next, s + stride);
+    } else {
+      const int base = lo + s * STEP;
+      // scores
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        uint32_t qw[NT][8];
+        if (NT > 1) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint4* at = reinterpret_cast<const uint4*>(s_q + (8 * nt + r) * (D + 8) + 64 * j + 16 * c);
+            const uint4 a = at[0], b = at[1];
+            qw[nt][0] = a.x; qw[nt][1] = a.y; qw[nt][2] = a.z; qw[nt][3] = a.w;
+            qw[nt][4] = b.x; qw[nt][5] = b.y; qw[nt][6] = b.z; qw[nt][7] = b.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w0 = word(C.k[0][j], i), w1 = word(C.k[1][j], i);
+          const uint32_t a0 = dsa::e4m3x2_to_f16x2(w0 & 0xFFFFu), a2 = dsa::e4m3x2_to_f16x2(w0 >> 16);
+          const uint32_t a1 = dsa::e4m3x2_to_f16x2(w1 & 0xFFFFu), a3 = dsa::e4m3x2_to_f16x2(w1 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (NT == 1) mma(x[nt], a0, a1, a2, a3, qf[4 * j + i][0], qf[4 * j + i][1]);
+            else mma(x[nt], a0, a1, a2, a3, qw[nt][2 * i], qw[nt][2 * i + 1]);
+          }
+        }
+      }
+      load_k(page_next, s + stride);
+      // t = x + log2(v_scale), masked
+      const float vsc = fminf(fmaxf(vs, 5.421010862427522e-20f), 1.8446744073709552e19f);   // [2^-64, 2^64]
+      const float bias = log2f(vsc), vinv = 1.0f / vsc;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(x[nt][e], qs[nt][e & 1] * ks, bias);
+      const bool edge = base + STEP - 1 > pos_min || (P.window > 0 && base <= pos_max - P.window);
+      if (edge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = base + r + (e >> 1) * 8, p = pos[nt][e & 1];
+            if (j > p || (P.window > 0 && j <= p - P.window)) x[nt][e] = -INFINITY;
+          }
+        // rows outside what any query sees may hold NaN codes: 0 * NaN is not 0
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = base + 2 * c + (i & 1) + (i >> 1) * 8;
+          if (j < seen_lo || j >= hi) C.v[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      // the running maximum, moved only when a score passes it by 2^LAG
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) up |= fmaxf(x[nt][e], x[nt][e + 2]) > R.m[nt][e] + LAG;
+      if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = fmaxf(fmaxf(x[nt][e], x[nt][e + 2]), R.m[nt][e]);
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+            f[e] = ex2(R.m[nt][e] - t);
+            R.m[nt][e] = t;
+            R.l[nt][e] *= f[e];
+          }
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R.o[nt][mt][e] *= f[e & 1];
+        }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float wt[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wt[e] = ex2(x[nt][e] - R.m[nt][e & 1]);
+        R.l[nt][0] = fmaf(wt[0] + wt[2], vinv, R.l[nt][0]);
+        R.l[nt][1] = fmaf(wt[1] + wt[3], vinv, R.l[nt][1]);
+        pf[nt][0] = transpose8(dsa::pack_f16x2(wt[0], wt[1]));
+        pf[nt][1] = transpose8(dsa::pack_f16x2(wt[2], wt[3]));
+      }
+      // values
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t w0 = word(C.v[0], i), w1 = word(C.v[1], i), w2 = word(C.v[2], i), w3 = word(C.v[3], i);
+        const uint32_t p0 = __byte_perm(w0, w1, 0x5140), p1 = __byte_perm(w0, w1, 0x7362);
+        const uint32_t p2 = __byte_perm(w2, w3, 0x5140), p3 = __byte_perm(w2, w3, 0x7362);
+        const uint32_t a[2][4] = {
+            {dsa::e4m3x2_to_f16x2(p0 & 0xFFFFu), dsa::e4m3x2_to_f16x2(p0 >> 16), dsa::e4m3x2_to_f16x2(p2 & 0xFFFFu),
+             dsa::e4m3x2_to_f16x2(p2 >> 16)},
+            {dsa::e4m3x2_to_f16x2(p1 & 0xFFFFu), dsa::e4m3x2_to_f16x2(p1 >> 16), dsa::e4m3x2_to_f16x2(p3 & 0xFFFFu),
+             dsa::e4m3x2_to_f16x2(p3 >> 16)}};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma(R.o[nt][2 * i + h], a[h][0], a[h][1], a[h][2], a[h][3], pf[nt][0], pf[nt][1]);
+      }
+      load_v(page_next, s + stride);
+    }
+    page = page_next;
+    page_next = page_after;
+    ks = ks_next;
+    vs = vs_next;
+  }
+}
+
+template <int D, int NT, int NW>
+struct RowSmem {
+  static constexpr int PITCH = D + 4;   // floats of a row: the warps' writes meet no bank conflict
+  float o[NW][8 * NT][PITCH];
+  float m[NW][8 * NT], l[NW][8 * NT];
+  uint16_t q[NT == 1 ? 8 : 8 * NT * (D + 8)];
+  int last;
+};
+
+// Steps [step0, step1) of one unit by the whole CTA, joined over its warps.  Rows
+// [row0, row0 + 8 NT) of the request.  Results go to `out` (pieces == 1) or to the CTA's
+// partial buffer, and the last CTA of a unit to arrive joins them in the order of the
+// pieces, so that the result does not depend on which one it was.
+template <int D, int NT, int NW>
+__device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S, int req, const Request& a, int head,
+                                          int row0, const Span& sp, int step0, int step1, int pieces, int first_cta,
+                                          int my_slot) {
+  constexpr int R8 = 8 * NT;
+  constexpr int PSIZE = R8 * D + 2 * R8;   // floats of one partial result
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, r = lane >> 2, c = lane & 3;
+  const int rows = a.rows(P);
+  const int pos0 = a.kv - a.q_len;
+
+  // queries: fp16 after a scaling of each row by a power of two that brings its largest
+  // magnitude to [2^7, 2^8)
+  uint32_t qf[NT == 1 ? D / 16 : 1][2];
+  float qs[NT][2];
+  int pos[NT][2];
+  float scale_row[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = row0 + 8 * nt + r;
+    uint4 v[D / 64][2];
+    float mx = 0.f;
+    const bool in = row < rows;
+    const int i = row / P.group;
+    const uint16_t* src = P.q + (a.q0 + i) * P.q_ld + (head * P.group + row - i * P.group) * P.q_hd + 16 * c;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v[j][h] = in ? dsa::ldg_nc(src + 64 * j + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack(word(v[j][h], e), P.fp16);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    // exponent of the largest magnitude, kept where both 2^e factors are normal numbers
+    const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127 - 7, -100), 120) : 0;
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    scale_row[nt] = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 f = unpack(word(v[j][h], u), P.fp16);
+          p[u] = dsa::pack_f16x2(f.x * down, f.y * down);
+        }
+        if (NT == 1) {
+          qf[NT == 1 ? 4 * j + 2 * h : 0][0] = p[0];
+          qf[NT == 1 ? 4 * j + 2 * h : 0][1] = p[1];
+          qf[NT == 1 ? 4 * j + 2 * h + 1 : 0][0] = p[2];
+          qf[NT == 1 ? 4 * j + 2 * h + 1 : 0][1] = p[3];
+        } else if (w == 0) {
+          *reinterpret_cast<uint4*>(S.q + (8 * nt + r) * (D + 8) + 64 * j + 16 * c + 8 * h) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+  }
+  // this lane's score columns are rows 8 nt + 2c + e; their scales are with lanes of r = 2c + e
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      qs[nt][e] = __shfl_sync(0xFFFFFFFFu, scale_row[nt], (2 * c + e) * 4) * P.scale_log2;
+      pos[nt][e] = pos0 + min(row0 + 8 * nt + 2 * c + e, rows - 1) / P.group;
+    }
+  const int pos_min = pos0 + row0 / P.group, pos_max = pos0 + min(row0 + R8 - 1, rows - 1) / P.group;
+  const int hi = min(pos_max + 1, a.kv);
+  const int seen_lo = P.window > 0 ? max(pos_min - P.window + 1, 0) : 0;
+  if (NT > 1) __syncthreads();
+
+  RowState<D, NT> R;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) R.o[nt][mt][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      R.m[nt][e] = M_INIT;
+      R.l[nt][e] = 0.f;
+    }
+  }
+  rows_steps<D, NT>(P, req, head, sp.lo, seen_lo, hi, step0 + w, step1, NW, qf, S.q, qs, pos, pos_min, pos_max, R);
+
+  // join the warps: dims are kept in the order mt * 16 + r * 2 + (0, 1)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = R.l[nt][e];
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+      const int row = 8 * nt + 2 * c + e;
+      if (r == 0) {
+        S.m[w][row] = R.m[nt][e];
+        S.l[w][row] = l;
+      }
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt)
+        *reinterpret_cast<float2*>(&S.o[w][row][mt * 16 + r * 2]) = make_float2(R.o[nt][mt][e], R.o[nt][mt][e + 2]);
+    }
+  __syncthreads();
+  const int live = min(rows - row0, R8);
+  float* mine = pieces > 1 ? P.partial + (long long)my_slot * PSIZE : nullptr;
+  auto write = [&](int row, int k4, float4 o, float m, float l) {
+    // o: dims k4 .. k4 + 3 in the joined order, which are two pairs of neighbours
+    const int i = (row0 + row) / P.group, h = head * P.group + (row0 + row) - i * P.group;
+    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays one
+    const int mt = k4 >> 4, rr = (k4 & 15) >> 1;
+    uint16_t* at = P.out + (a.q0 + i) * P.out_ld + h * P.out_hd + rr * (D / 8) + 2 * mt;
+    *reinterpret_cast<uint32_t*>(at) = pack(o.x * inv, o.y * inv, P.fp16);
+    *reinterpret_cast<uint32_t*>(at + D / 8) = pack(o.z * inv, o.w * inv, P.fp16);
+    if (k4 == 0 && P.lse)
+      P.lse[(long long)(a.q0 + i) * P.h_q + h] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+  };
+  for (int u = tid; u < live * (D / 4); u += 32 * NW) {
+    const int row = u / (D / 4), k4 = (u % (D / 4)) * 4;
+    float m = S.m[0][row];
+#pragma unroll
+    for (int x = 1; x < NW; ++x) m = fmaxf(m, S.m[x][row]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+      const float f = ex2(S.m[x][row] - m);
+      const float4 v = *reinterpret_cast<const float4*>(&S.o[x][row][k4]);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+      l = fmaf(S.l[x][row], f, l);
+    }
+    if (pieces == 1) {
+      write(row, k4, o, m, l);
+    } else {
+      *reinterpret_cast<float4*>(mine + row * D + k4) = o;
+      if (k4 == 0) {
+        mine[R8 * D + row] = m;
+        mine[R8 * D + R8 + row] = l;
+      }
+    }
+  }
+  if (pieces > 1) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) S.last = atomicAdd(P.arrived + first_cta, 1) == pieces - 1;
+    __syncthreads();
+    if (S.last) {
+      __threadfence();
+      // piece 0 is the second buffer of the unit's first CTA, the others the first buffers
+      // of the CTAs behind it
+      for (int u = tid; u < live * (D / 4); u += 32 * NW) {
+        const int row = u / (D / 4), k4 = (u % (D / 4)) * 4;
+        float m = M_INIT, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = 0; p0 < pieces; p0 += 8) {
+          float pm[8], pl[8];
+          float4 po[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int p = p0 + x;
+            pm[x] = M_INIT;
+            pl[x] = 0.f;
+            po[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p < pieces) {
+              const float* b = P.partial + (long long)(2 * (first_cta + p) + (p == 0 ? 1 : 0)) * PSIZE;
+              po[x] = __ldcg(reinterpret_cast<const float4*>(b + row * D + k4));
+              pm[x] = __ldcg(b + R8 * D + row);
+              pl[x] = __ldcg(b + R8 * D + R8 + row);
+            }
+          }
+          float top = m;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) top = fmaxf(top, pm[x]);
+          const float f0 = ex2(m - top);
+          o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+          l *= f0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float f = ex2(pm[x] - top);
+            o.x = fmaf(po[x].x, f, o.x);
+            o.y = fmaf(po[x].y, f, o.y);
+            o.z = fmaf(po[x].z, f, o.z);
+            o.w = fmaf(po[x].w, f, o.w);
+            l = fmaf(pl[x], f, l);
+          }
+          m = top;
+        }
+        write(row, k4, o, m, l);
+      }
+    }
+  }
+  __syncthreads();   // the shared memory is used again
+}
+
+template <int D, int NT, int NW>
+__global__ void __launch_bounds__(32 * NW) rows_kernel(const __grid_constant__ Params P) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  RowSmem<D, NT, NW>& S = *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x;
+  const long long share = P.header->share;
+  const Share at = P.shares[b];
+  int req = at.req, head = at.head;
+  if (req < 0) return;
+  long long step = at.step, left = share;
+  long long unit = b * share - step;   // where the unit begins among all steps
+  Request a = request(P, req);
+  Span sp = span(P, a, 0, a.q_len - 1);
+  while (true) {
+    const int take = (int)min(left, sp.steps - step);
+    const int first = (int)(unit / share), lastc = (int)((unit + sp.steps - 1) / share);
+    rows_unit<D, NT, NW>(P, S, req, a, head, 0, sp, (int)step, (int)step + take, lastc - first + 1, first,
+                         2 * b + (first == b ? 1 : 0));
+    left -= take;
+    if (left == 0) return;
+    unit += sp.steps;
+    step = 0;
+    if (++head < P.h_kv) continue;
+    head = 0;
+    do {
+      if (++req >= P.n_req) return;
+      a = request(P, req);
+    } while (a.q_len == 0 || a.q_len > P.max_q_len || a.rows(P) > P.small_rows);
+    sp = span(P, a, 0, a.q_len - 1);
+  }
+}
+
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW) tiles_kernel(const __grid_constant__ Params P) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  RowSmem<D, TILE_ROWS / 8, NW>& S = *reinterpret_cast<RowSmem<D, TILE_ROWS / 8, NW>*>(smem_raw);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = P.header->n_tiles;
+  // later tiles of a request see more tokens: they go first
+  for (long long u = blockIdx.x; u < (long long)n * P.h_kv; u += gridDim.x) {
+    const int2 tile = P.tiles[n - 1 - (int)(u / P.h_kv)];
+    const int head = (int)(u % P.h_kv), row0 = tile.y * TILE_ROWS;
+    const Request a = request(P, tile.x);
+    const int row1 = min(row0 + TILE_ROWS, a.rows(P)) - 1;
+    const Span sp = span(P, a, row0 / P.group, row1 / P.group);
+    rows_unit<D, TILE_ROWS / 8, NW>(P, S, tile.x, a, head, row0, sp, 0, sp.steps, 1, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------------------------ host
+static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+static int check(const dsa_kv8_params* p) {
+  if (!p || p->n_tokens < 0 || p->n_tokens > (1 << 30) || p->n_req < 0 || p->h_q < 1 || p->h_kv < 1 ||
+      p->h_q % p->h_kv != 0 || p->n_pages < 0 || p->table_cols < 0 || p->max_q_len < 0 || p->window < 0 ||
+      (p->type != DSA_KV8_BF16 && p->type != DSA_KV8_FP16) || !isfinite(p->softmax_scale) || p->flags != 0)
+    return DSA_ERR_INVALID_ARG;
+  if ((p->d != 64 && p->d != 128) ||
+      (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) ||
+      p->n_req > DSA_KV8_MAX_REQ || p->h_kv > DSA_KV8_MAX_HEADS || p->h_q / p->h_kv > DSA_KV8_MAX_GROUP ||
+      (long long)p->n_tokens * (p->h_q / p->h_kv) >= (1LL << 31))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  return DSA_OK;
+}
+
+// tiles of 8 query rows of a request in rows_kernel: 1, 2 or 4.  Where the batch has
+// requests for the tiles as well, single-query requests set it.
+static int row_tiles(const dsa_kv8_params* p) {
+  const long long group = p->h_q / p->h_kv, most = (long long)p->max_q_len * group;
+  const long long rows = most <= MAX_ROWS ? most : (group <= MAX_ROWS ? group : MAX_ROWS);
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+
+struct Layout {
+  int n_shares, max_tiles;
+  size_t shares, arrived, tiles, partial, bytes;
+};
+
+static size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+static Layout layout(const dsa_kv8_params* p, int sms) {
+  Layout L;
+  const size_t group = p->h_q / p->h_kv, rows = 8 * (size_t)row_tiles(p);
+  L.n_shares = CTAS_PER_SM * sms;
+  size_t at = 256;
+  L.shares = at;
+  at += up(L.n_shares * sizeof(Share));
+  L.arrived = at;
+  at += up(L.n_shares * sizeof(int));
+  L.tiles = at;
+  L.max_tiles = (int)(p->n_tokens * group / TILE_ROWS + p->n_req);
+  at += up((size_t)L.max_tiles * sizeof(int2));
+  L.partial = at;
+  at += up((size_t)L.n_shares * 2 * (rows * p->d + 2 * rows) * sizeof(float));
+  L.bytes = at;
+  return L;
+}
+
+template <typename K>
+static int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st, const Params& P, bool dependent) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+template <int D>
+static int launch_all(const dsa_kv8_params* p, const Params& P, int sms, cudaStream_t st) {
+  int rc;
+  switch (row_tiles(p)) {
+    case 1:
+      rc = launch(rows_kernel<D, 1, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 1, ROW_WARPS>), st, P, true);
+      break;
+    case 2:
+      rc = launch(rows_kernel<D, 2, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 2, ROW_WARPS>), st, P, true);
+      break;
+    default:
+      rc = launch(rows_kernel<D, 4, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 4, ROW_WARPS>), st, P, true);
+  }
+  if (rc != DSA_OK) return rc;
+  if ((long long)p->max_q_len * P.group > P.small_rows)
+    rc = launch(tiles_kernel<D, ROW_WARPS>, 2 * sms, 32 * ROW_WARPS, sizeof(RowSmem<D, TILE_ROWS / 8, ROW_WARPS>), st, P, false);
+  return rc;
+}
+
+}  // namespace dsa_kv8
+
+extern "C" {
+
+int dsa_kv8_params_init(dsa_kv8_params* p, int32_t n_tokens, int32_t n_req, int32_t h_q, int32_t h_kv, int32_t d,
+                        int32_t page_size, int32_t n_pages, int32_t table_cols) {
+  if (!p) return DSA_ERR_INVALID_ARG;
+  p->n_tokens = n_tokens;
+  p->n_req = n_req;
+  p->h_q = h_q;
+  p->h_kv = h_kv;
+  p->d = d;
+  p->page_size = page_size;
+  p->n_pages = n_pages;
+  p->table_cols = table_cols;
+  p->max_q_len = n_tokens;
+  p->window = 0;
+  p->type = DSA_KV8_BF16;
+  p->softmax_scale = d > 0 ? (float)(1.0 / sqrt((double)d)) : 1.0f;
+  p->flags = 0;
+  return dsa_kv8::check(p);
+}
+
+static int current_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+size_t dsa_kv8_attn_workspace_size(const dsa_kv8_params* p, int num_sms) {
+  if (dsa_kv8::check(p) != DSA_OK) return 0;
+  if (num_sms <= 0 && current_sms(&num_sms) != DSA_OK) return 0;
+  return dsa_kv8::layout(p, num_sms).bytes;
+}
+
+int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_pool, const void* v_pool,
+                     const float* k_scale, const float* v_scale, const int32_t* block_table, int64_t table_ld,
+                     const int32_t* cu_q, const int32_t* kv_lens, void* out, int64_t out_ld, int64_t out_hd, float* lse,
+                     const dsa_kv8_params* p, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace dsa_kv8;
+  const int rc = check(p);
+  if (rc != DSA_OK) return rc;
+  if (!workspace || !aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;
+  if (p->n_tokens > 0 && p->n_req > 0) {
+    if (q_ld % 8 != 0 || q_hd % 8 != 0 || out_ld % 8 != 0 || out_hd % 8 != 0 || q_ld < p->d || out_ld < p->d ||
+        (p->h_q > 1 && (q_hd < p->d || out_hd < p->d)) || table_ld < p->table_cols)
+      return DSA_ERR_INVALID_ARG;
+    if (!q || !out || !cu_q || !kv_lens || !aligned(q, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
+        !aligned(kv_lens, 4) || !aligned(lse, 4))
+      return DSA_ERR_INVALID_ARG;
+    if (p->table_cols > 0 && (!block_table || !aligned(block_table, 4))) return DSA_ERR_INVALID_ARG;
+    if (p->n_pages > 0 && (!k_pool || !v_pool || !k_scale || !v_scale || !aligned(k_pool, 16) || !aligned(v_pool, 16) ||
+                           !aligned(k_scale, 4) || !aligned(v_scale, 4)))
+      return DSA_ERR_INVALID_ARG;
+  }
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED_DEVICE;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSA_ERR_CUDA;
+  const Layout L = layout(p, sms);
+  if (workspace_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (p->n_tokens == 0 || p->n_req == 0)
+    return cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  Params P;
+  P.q = static_cast<const uint16_t*>(q);
+  P.k_pool = static_cast<const uint8_t*>(k_pool);
+  P.v_pool = static_cast<const uint8_t*>(v_pool);
+  P.k_scale = k_scale;
+  P.v_scale = v_scale;
+  P.table = block_table;
+  P.cu_q = cu_q;
+  P.kv_lens = kv_lens;
+  P.out = static_cast<uint16_t*>(out);
+  P.lse = lse;
+  P.q_ld = q_ld;
+  P.q_hd = q_hd;
+  P.out_ld = out_ld;
+  P.out_hd = out_hd;
+  P.table_ld = table_ld;
+  P.header = reinterpret_cast<Header*>(ws);
+  P.shares = reinterpret_cast<Share*>(ws + L.shares);
+  P.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  P.tiles = reinterpret_cast<int2*>(ws + L.tiles);
+  P.partial = reinterpret_cast<float*>(ws + L.partial);
+  P.n_tokens = p->n_tokens;
+  P.n_req = p->n_req;
+  P.h_q = p->h_q;
+  P.h_kv = p->h_kv;
+  P.group = p->h_q / p->h_kv;
+  P.n_pages = p->n_pages;
+  P.page_shift = __builtin_ctz(p->page_size);
+  // positions stay below 2^31 with room for a step and a tile behind the last one
+  const long long cap = (long long)p->table_cols * p->page_size, most = (1LL << 31) - 1024;
+  P.cap = (int)(cap < most ? cap : most);
+  P.max_q_len = p->max_q_len;
+  P.window = p->window;
+  P.fp16 = p->type == DSA_KV8_FP16;
+  P.small_rows = 8 * row_tiles(p);
+  P.n_shares = L.n_shares;
+  P.max_tiles = L.max_tiles;
+  P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  const size_t smem = (size_t)(p->n_req + 1) * 2 * sizeof(long long);
+  const int rc1 = launch(plan_kernel, 1, PLAN_THREADS, smem, st, P, false);
+  if (rc1 != DSA_OK) return rc1;
+  return p->d == 128 ? launch_all<128>(p, P, sms, st) : launch_all<64>(p, P, sms, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,261 @@
+// Insert into the paged 8-bit cache (include/dsa_kv8.h): new tokens' keys and values as
+// E4M3 codes under one power-of-two scale per page and KV head.
+//
+// A CTA takes the runs (new tokens of one page) that start in its window of the batch, for
+// one KV head, keys or values; a run that passes the window's end is finished by the CTA
+// where it starts, so no two CTAs touch one page.  D / 8 lanes hold a token (16 bytes
+// each), so that a row is read in one piece:
+//   1. every token of the CTA's runs is read once into registers, and its largest
+//      magnitude goes into its run's maximum (shared memory, an integer maximum of the
+//      bits, which order as the magnitudes do);
+//   2. one thread per run forms the scale from the maximum's exponent, writes it, and
+//      lists the run if the page's older rows have to be rescaled;
+//   3. the registers are scaled, rounded and written; then the listed runs' older rows.
+// Bound by memory: 2 bytes read and 1 written per value; the older rows are read only
+// where a page's scale grows, which a new token does less and less often as a page fills.
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dsa_kv8.h"
+#include "ptx_sm103.cuh"
+
+namespace dsa_kv8 {
+
+constexpr int THREADS = 256;
+constexpr int WINDOW = 64;   // most tokens in which a CTA's runs start
+
+struct Params {
+  const uint16_t *x[2];
+  long long ld[2], hd[2];
+  uint8_t* pool[2];
+  float* scale[2];
+  const int64_t* slots;
+  uint32_t* status;
+  long long n_rows;
+  int n_tokens, h_kv, page_shift, window;
+};
+
+__device__ __forceinline__ float2 to_f32x2(uint32_t w, int fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// least power of two s >= 2^-64 with amax <= 448 s = 1.75 * 2^8 s, at most 2^64
+__device__ __forceinline__ float page_scale(uint32_t amax_bits) {
+  int e = (int)(amax_bits >> 23) - 127 - 8;
+  if ((amax_bits & 0x7FFFFFu) > 0x600000u) ++e;
+  e = min(max(e, -64), 64);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+template <int D, int PASSES>
+__global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__ Params P, int fp16) {
+  constexpr int LANES = D / 8;                    // lanes of one token
+  constexpr int GROUPS = THREADS / LANES;         // tokens per pass
+  constexpr int SPAN = PASSES * GROUPS;           // tokens that the CTA may hold
+  __shared__ long long s_slot[SPAN + 1];          // [i + 1]: slot of token t0 + i
+  __shared__ int s_run[SPAN];                     // where a token's run starts, -1: not this CTA's
+  __shared__ uint32_t s_amax[WINDOW];             // by the run's first token
+  __shared__ float s_scale[WINDOW];
+  __shared__ int s_last[THREADS / 32];
+  __shared__ int s_n_old, s_old_end[WINDOW], s_old_run[WINDOW];
+  __shared__ float s_old_ratio[WINDOW];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int t0 = blockIdx.x * P.window;
+  const int head = blockIdx.y, which = blockIdx.z;
+  const int page_mask = (1 << P.page_shift) - 1;
+  static_assert(SPAN <= THREADS, "one thread per token");
+
+  // slots and runs
+  long long slot = -1;
+  if (tid < SPAN && t0 + tid < P.n_tokens) {
+    slot = P.slots[t0 + tid];
+    if (slot >= P.n_rows) {
+      if (head == 0 && which == 0 && P.status) atomicOr(P.status, DSA_STATUS_SLOT_OUT_OF_RANGE);
+      slot = -1;
+    }
+  }
+  if (tid < SPAN) s_slot[tid + 1] = slot;
+  if (tid == 0) {
+    const long long before = t0 > 0 ? P.slots[t0 - 1] : -1;
+    s_slot[0] = before >= P.n_rows ? -1 : before;
+    s_n_old = 0;
+  }
+  if (tid < WINDOW) s_amax[tid] = 0u;
+  __syncthreads();
+  const bool starts = slot >= 0 && ((slot & page_mask) == 0 || s_slot[tid] != slot - 1);
+  // the last start or gap at or before each token
+  const uint32_t breaks = __ballot_sync(0xFFFFFFFFu, slot < 0 || starts);
+  const uint32_t upto = breaks & (0xFFFFFFFFu >> (31 - lane));
+  int from = upto ? 32 * w + 31 - __clz(upto) : -1;
+  if (lane == 31) s_last[w] = from;
+  __syncthreads();
+  for (int u = w - 1; u >= 0 && from < 0; --u) from = s_last[u];
+  // `from` is the run's start if a run starts there: -1 (the run began before this window)
+  // and starts past the window belong to another CTA
+  if (tid < SPAN) s_run[tid] = (slot >= 0 && from >= 0 && from < P.window) ? from : -1;
+  __syncthreads();
+
+  // 1. values into registers, maxima of the runs
+  const int group = tid / LANES, part = tid % LANES;
+  const uint16_t* src = P.x[which] + head * P.hd[which] + part * 8;
+  uint4 x[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * GROUPS + group;
+    x[p] = make_uint4(0u, 0u, 0u, 0u);
+    if (s_run[i] >= 0) x[p] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + i) * P.ld[which]));
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const uint32_t v[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = to_f32x2(v[k], fp16);
+      m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));   // a NaN is left out by the maximum
+    }
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const int run = s_run[p * GROUPS + group];
+    if (part == 0 && run >= 0) atomicMax(&s_amax[run], __float_as_uint(m));
+  }
+  __syncthreads();
+
+  // 2. scales
+  if (tid < P.window && starts) {
+    const long long page = slot >> P.page_shift;
+    const int o0 = (int)slot & page_mask;
+    float* at = P.scale[which] + page * P.h_kv + head;
+    float s = page_scale(s_amax[tid]);
+    if (o0 > 0) {
+      const float old = *at;
+      if (old >= s) {
+        s = old;
+      } else {
+        const int k = atomicAdd(&s_n_old, 1);   // the order of the list changes no result
+        s_old_run[k] = tid;
+        s_old_ratio[k] = old / s;
+      }
+    }
+    *at = s;
+    s_scale[tid] = 1.0f / s;
+  }
+  __syncthreads();
+
+  // 3. codes
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * GROUPS + group;
+    const int run = s_run[i];
+    if (run < 0) continue;
+    const float inv = s_scale[run];
+    const uint32_t v[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = to_f32x2(v[k], fp16);
+      c[k] = dsa::f32x2_to_e4m3x2(f.x * inv, f.y * inv);
+    }
+    const long long sl = s_slot[i + 1];
+    const long long row = (((sl >> P.page_shift) * P.h_kv + head) << P.page_shift) + (sl & page_mask);
+    *reinterpret_cast<uint2*>(P.pool[which] + row * D + part * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
+
+  // the older rows of pages whose scale grew: (run, row) pairs over the groups
+  const int n_old = s_n_old;
+  if (n_old == 0) return;
+  if (tid == 0) {
+    int sum = 0;
+    for (int k = 0; k < n_old; ++k) {
+      sum += (int)s_slot[s_old_run[k] + 1] & page_mask;
+      s_old_end[k] = sum;
+    }
+  }
+  __syncthreads();
+  const int rows = s_old_end[n_old - 1];
+  for (int f = group; f < rows; f += GROUPS) {
+    int k = 0;
+    while (s_old_end[k] <= f) ++k;
+    const int run = s_old_run[k];
+    const int r = f - (k > 0 ? s_old_end[k - 1] : 0);
+    const float ratio = s_old_ratio[k];
+    const long long page = s_slot[run + 1] >> P.page_shift;
+    uint2* at = reinterpret_cast<uint2*>(P.pool[which] + (((page * P.h_kv + head) << P.page_shift) + r) * D + part * 8);
+    const uint2 c = *at;
+    const uint32_t in[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t h2 = dsa::e4m3x2_to_f16x2(in[e]);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      o[e] = dsa::f32x2_to_e4m3x2(v.x * ratio, v.y * ratio);
+    }
+    *at = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+  }
+}
+
+static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+static bool bad_pitch(int64_t ld, int64_t hd, int heads, int d) {
+  return ld < d || ld % 8 != 0 || hd % 8 != 0 || (heads > 1 && hd < d);
+}
+
+}  // namespace dsa_kv8
+
+extern "C" int dsa_kv8_insert(const void* k, int64_t k_ld, int64_t k_hd, const void* v, int64_t v_ld, int64_t v_hd,
+                              const int64_t* slots, int32_t n_tokens, int32_t type, void* k_pool, void* v_pool,
+                              float* k_scale, float* v_scale, int32_t n_pages, int32_t h_kv, int32_t page_size,
+                              int32_t d, uint32_t* status, void* stream) {
+  using namespace dsa_kv8;
+  if (n_tokens < 0 || n_tokens > (1 << 30) || n_pages < 0 || h_kv < 1 || (type != DSA_KV8_BF16 && type != DSA_KV8_FP16))
+    return DSA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
+      h_kv > DSA_KV8_MAX_HEADS)
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_tokens == 0) return DSA_OK;
+  if (bad_pitch(k_ld, k_hd, h_kv, d) || bad_pitch(v_ld, v_hd, h_kv, d)) return DSA_ERR_INVALID_ARG;
+  if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || (status && !aligned(status, 4)))
+    return DSA_ERR_INVALID_ARG;
+  if (n_pages > 0 && (!k_pool || !v_pool || !k_scale || !v_scale)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return DSA_ERR_INVALID_ARG;
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED_DEVICE;
+  Params P;
+  P.x[0] = static_cast<const uint16_t*>(k);
+  P.x[1] = static_cast<const uint16_t*>(v);
+  P.ld[0] = k_ld;
+  P.ld[1] = v_ld;
+  P.hd[0] = k_hd;
+  P.hd[1] = v_hd;
+  P.pool[0] = static_cast<uint8_t*>(k_pool);
+  P.pool[1] = static_cast<uint8_t*>(v_pool);
+  P.scale[0] = k_scale;
+  P.scale[1] = v_scale;
+  P.slots = slots;
+  P.status = status;
+  P.n_rows = (long long)n_pages * page_size;
+  P.n_tokens = n_tokens;
+  P.h_kv = h_kv;
+  P.page_shift = __builtin_ctz(page_size);
+  P.window = WINDOW;
+  const dim3 grid((unsigned)((n_tokens + P.window - 1) / P.window), (unsigned)h_kv, 2);
+  const int fp16 = type == DSA_KV8_FP16;
+  cudaStream_t st = (cudaStream_t)stream;
+  // WINDOW + page_size - 1 tokens fit the CTA's registers: 128 for pages of up to 64 tokens, 192 for 128
+  if (d == 128) {
+    if (page_size <= 64) insert_kernel<128, 8><<<grid, THREADS, 0, st>>>(P, fp16);
+    else insert_kernel<128, 12><<<grid, THREADS, 0, st>>>(P, fp16);
+  } else {
+    if (page_size <= 64) insert_kernel<64, 4><<<grid, THREADS, 0, st>>>(P, fp16);
+    else insert_kernel<64, 6><<<grid, THREADS, 0, st>>>(P, fp16);
+  }
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}

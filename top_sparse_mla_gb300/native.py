@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/dsa_sparse_attn.h (argument marshalling only).
+"""ctypes binding of the C ABI in include/*.h (argument marshalling only).
 
 Every entry point keeps the C name.  Tensors are passed as raw device pointers
 (``tensor.data_ptr()``); the stream is the caller's current CUDA stream.  All of the
@@ -42,6 +42,16 @@ DSA_NVFP4_QK_DIMS = 512
 DSA_NVFP4_SWA_ROW_BYTES = 528
 DSA_NVFP4_CMP_ROW_BYTES = 288
 DSA_STATUS_SLOT_OUT_OF_RANGE = 4
+DSA_PAGE_MAP_MAX_REQ = 8192
+DSA_STATUS_OUT_OF_PAGES = 8
+DSA_STATUS_TABLE_FULL = 16
+DSA_STATUS_TOKENS_FULL = 32
+DSA_KV8_BF16 = 0
+DSA_KV8_FP16 = 1
+DSA_KV8_MAX_HEADS = 1024
+DSA_KV8_MAX_GROUP = 128
+DSA_KV8_MAX_REQ = 8192
+DSA_STATUS_QUERY_TOO_LONG = 64
 
 EXPORTED = (
     "dsa_params_init",
@@ -54,6 +64,11 @@ EXPORTED = (
     "dsa_error_string",
     "dsa_topk_select",
     "dsa_kv_insert",
+    "dsa_page_map",
+    "dsa_kv8_insert",
+    "dsa_kv8_params_init",
+    "dsa_kv8_attn_workspace_size",
+    "dsa_kv8_attn_fwd",
 )
 
 
@@ -71,6 +86,24 @@ class DsaParams(ctypes.Structure):
         ("flags", ctypes.c_uint32),
         ("kv_format", ctypes.c_int32),
         ("cmp_scale", ctypes.c_float),
+    ]
+
+
+class DsaKv8Params(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32),
+        ("n_req", ctypes.c_int32),
+        ("h_q", ctypes.c_int32),
+        ("h_kv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("table_cols", ctypes.c_int32),
+        ("max_q_len", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("type", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
     ]
 
 
@@ -115,6 +148,18 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_kv_insert.argtypes = [vp, ctypes.c_int64, vp, vp, ctypes.c_int32, vp, ctypes.c_float, ctypes.c_float, vp,
                                   ctypes.c_int64, ctypes.c_uint32, vp, vp]
     lib.dsa_kv_insert.restype = ctypes.c_int
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    lib.dsa_page_map.argtypes = [vp, vp, i32, vp, i64, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.dsa_page_map.restype = ctypes.c_int
+    lib.dsa_kv8_insert.argtypes = [vp, i64, i64, vp, i64, i64, vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.dsa_kv8_insert.restype = ctypes.c_int
+    p8 = ctypes.POINTER(DsaKv8Params)
+    lib.dsa_kv8_params_init.argtypes = [p8, i32, i32, i32, i32, i32, i32, i32, i32]
+    lib.dsa_kv8_params_init.restype = ctypes.c_int
+    lib.dsa_kv8_attn_workspace_size.argtypes = [p8, ctypes.c_int]
+    lib.dsa_kv8_attn_workspace_size.restype = sz
+    lib.dsa_kv8_attn_fwd.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp, i64, i64, vp, p8, vp, sz, vp]
+    lib.dsa_kv8_attn_fwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -222,6 +267,158 @@ def dsa_kv_insert(kv, positions, slots, kv_norm_w, pool, rms_eps: float = 1e-6, 
                                  DSA_KV_FLAG_CHECK_SLOTS if check_slots else 0, _ptr(status), _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, "dsa_kv_insert")
+
+
+def _require(ok: bool, where: str, what: str) -> None:
+    if not ok:
+        raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+def _rows(x, dtype: str, where: str, name: str, *shape) -> None:
+    """x is a dense device tensor of this dtype and shape (None: any extent)."""
+    if str(x.dtype) != dtype or x.dim() != len(shape) or not x.is_contiguous() or any(
+            n is not None and int(m) != n for m, n in zip(x.shape, shape)):
+        raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {name} must be a contiguous {dtype} tensor of shape "
+                       f"{tuple('any' if n is None else n for n in shape)}, got {x.dtype} {tuple(x.shape)}")
+
+
+def _one_device(where: str, *tensors) -> None:
+    """All tensors on the current CUDA device (the library launches there)."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for x in tensors:
+        if x is not None and (not x.is_cuda or x.device.index != dev):
+            raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: every tensor must be on the current CUDA device")
+
+
+def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu_new, kv_lens, positions, slots,
+                 token_req, info, stream=None) -> None:
+    """Page map of one serving step (include/dsa_page_map.h). ctx_lens, new_lens, kv_lens:
+    int32 [n_req]; block_table: int32 [n_req, cols] (in and out; a row pitch is allowed);
+    free_pages: int32 [n_free]; cu_new: int32 [n_req + 1]; positions, token_req (or None):
+    int32 [n_tokens]; slots: int64 [n_tokens]; info: int32 [2] (pages taken, status bits)."""
+    where = "dsa_page_map"
+    n_req, n_tokens = int(ctx_lens.shape[0]), int(slots.shape[0])
+    i32 = "torch.int32"
+    _rows(ctx_lens, i32, where, "ctx_lens", n_req)
+    _rows(new_lens, i32, where, "new_lens", n_req)
+    _rows(free_pages, i32, where, "free_pages", None)
+    _rows(cu_new, i32, where, "cu_new", n_req + 1)
+    _rows(kv_lens, i32, where, "kv_lens", n_req)
+    _rows(positions, i32, where, "positions", n_tokens)
+    _rows(slots, "torch.int64", where, "slots", n_tokens)
+    if token_req is not None:
+        _rows(token_req, i32, where, "token_req", n_tokens)
+    _rows(info, i32, where, "info", 2)
+    cols = int(block_table.shape[1]) if block_table.dim() == 2 else 0
+    _require(str(block_table.dtype) == i32 and block_table.dim() == 2 and int(block_table.shape[0]) == n_req
+             and (cols <= 1 or int(block_table.stride(1)) == 1), where, "block_table must be int32 [n_req, cols] rows")
+    _one_device(where, ctx_lens, new_lens, block_table, free_pages, cu_new, kv_lens, positions, slots, token_req, info)
+    ld = max(int(block_table.stride(0)), cols) if n_req > 1 else cols
+    rc = library().dsa_page_map(_ptr(ctx_lens), _ptr(new_lens), n_req, _ptr(block_table), ld, cols, _ptr(free_pages),
+                                int(free_pages.shape[0]), int(page_size), n_tokens, _ptr(cu_new), _ptr(kv_lens),
+                                _ptr(positions), _ptr(slots), _ptr(token_req), _ptr(info), _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+
+
+_KV8_TYPES = {"torch.bfloat16": DSA_KV8_BF16, "torch.float16": DSA_KV8_FP16}
+
+
+def _kv8_pools(where, k_pool, v_pool, k_scale, v_scale):
+    _rows(k_pool, "torch.uint8", where, "k_pool", None, None, None, None)
+    n_pages, h_kv, page, d = (int(x) for x in k_pool.shape)
+    _rows(v_pool, "torch.uint8", where, "v_pool", n_pages, h_kv, page, d)
+    _rows(k_scale, "torch.float32", where, "k_scale", n_pages, h_kv)
+    _rows(v_scale, "torch.float32", where, "v_scale", n_pages, h_kv)
+    return n_pages, h_kv, page, d
+
+
+def _heads(where, x, name, n, h, d, dtype=None):
+    """(token pitch, head pitch) of a [n, h, d] tensor whose last dimension is dense."""
+    _require(x.dim() == 3 and tuple(int(m) for m in x.shape) == (n, h, d) and (x.numel() == 0 or int(x.stride(2)) == 1)
+             and (dtype is None or x.dtype == dtype), where, f"{name} must be [{n}, {h}, {d}] with a dense last dimension")
+    # a pitch that no second row uses may be anything: give the dense one
+    return (int(x.stride(0)) if n > 1 else max(h * d, 8)), (int(x.stride(1)) if h > 1 else d)
+
+
+def dsa_kv8_insert(k, v, slots, k_pool, v_pool, k_scale, v_scale, status=None, stream=None) -> None:
+    """Insert into the paged 8-bit cache (include/dsa_kv8.h). k, v: bf16 or fp16
+    [n_tokens, h_kv, d] device tensors (token and head pitches allowed); slots: int64
+    [n_tokens] (< 0 = skip); k_pool, v_pool: uint8 [n_pages, h_kv, page_size, d]; k_scale,
+    v_scale: fp32 [n_pages, h_kv]; status: uint32 or int32 [1] device tensor or None."""
+    where = "dsa_kv8_insert"
+    n_pages, h_kv, page, d = _kv8_pools(where, k_pool, v_pool, k_scale, v_scale)
+    n = int(slots.shape[0])
+    _rows(slots, "torch.int64", where, "slots", n)
+    _require(str(k.dtype) in _KV8_TYPES, where, "k must be bfloat16 or float16")
+    k_ld, k_hd = _heads(where, k, "k", n, h_kv, d)
+    v_ld, v_hd = _heads(where, v, "v", n, h_kv, d, k.dtype)
+    _one_device(where, k, v, slots, k_pool, v_pool, k_scale, v_scale, status)
+    rc = library().dsa_kv8_insert(_ptr(k), k_ld, k_hd, _ptr(v), v_ld, v_hd, _ptr(slots), n, _KV8_TYPES[str(k.dtype)],
+                                  _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), n_pages, h_kv, page, d,
+                                  _ptr(status), _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+
+
+def dsa_kv8_params_init(q, k_pool, block_table, max_q_len=None, **overrides) -> DsaKv8Params:
+    """Parameters of dsa_kv8_attn_fwd for these tensors' shapes and type: q bf16 or fp16
+    [n_tokens, h_q, d], k_pool uint8 [n_pages, h_kv, page_size, d], block_table
+    [n_req, cols]. max_q_len: most query rows of a request (default: n_tokens);
+    overrides: window, softmax_scale."""
+    where = "dsa_kv8_params_init"
+    _require(q.dim() == 3 and k_pool.dim() == 4 and block_table.dim() == 2 and str(q.dtype) in _KV8_TYPES
+             and int(q.shape[2]) == int(k_pool.shape[3]), where, "q, k_pool and block_table do not belong together")
+    p = DsaKv8Params()
+    n_pages, h_kv, page, d = (int(x) for x in k_pool.shape)
+    rc = library().dsa_kv8_params_init(ctypes.byref(p), int(q.shape[0]), int(block_table.shape[0]), int(q.shape[1]),
+                                       h_kv, d, page, n_pages, int(block_table.shape[1]))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+    p.type = _KV8_TYPES[str(q.dtype)]
+    if max_q_len is not None:
+        p.max_q_len = int(max_q_len)
+    for name, value in overrides.items():
+        _require(name in ("window", "softmax_scale", "flags"), where, f"unknown parameter {name}")
+        setattr(p, name, value)
+    return p
+
+
+def dsa_kv8_attn_workspace_size(p: DsaKv8Params, num_sms: int = 0) -> int:
+    n = int(library().dsa_kv8_attn_workspace_size(ctypes.byref(p), int(num_sms)))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, "dsa_kv8_attn_workspace_size")
+    return n
+
+
+def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, p: DsaKv8Params, workspace,
+                     lse=None, stream=None) -> None:
+    """Attention over the paged 8-bit cache (include/dsa_kv8.h). q, out: bf16 or fp16
+    [n_tokens, h_q, d] (token and head pitches allowed); pools and scales as
+    dsa_kv8_insert; block_table: int32 [n_req, cols]; cu_q: int32 [n_req + 1]; kv_lens:
+    int32 [n_req]; lse: fp32 [n_tokens, h_q] or None; workspace: uint8, 256-byte aligned
+    (dsa_kv8_attn_workspace_size(p) bytes)."""
+    where = "dsa_kv8_attn_fwd"
+    n_pages, h_kv, page, d = _kv8_pools(where, k_pool, v_pool, k_scale, v_scale)
+    _require((n_pages, h_kv, page, d) == (p.n_pages, p.h_kv, p.page_size, p.d), where, "the pools are not p's")
+    _require(_KV8_TYPES.get(str(q.dtype)) == p.type, where, "q's type is not p's")
+    q_ld, q_hd = _heads(where, q, "q", p.n_tokens, p.h_q, d)
+    out_ld, out_hd = _heads(where, out, "out", p.n_tokens, p.h_q, d, q.dtype)
+    _rows(cu_q, "torch.int32", where, "cu_q", p.n_req + 1)
+    _rows(kv_lens, "torch.int32", where, "kv_lens", p.n_req)
+    _require(str(block_table.dtype) == "torch.int32" and tuple(block_table.shape) == (p.n_req, p.table_cols)
+             and (p.table_cols <= 1 or int(block_table.stride(1)) == 1), where, "block_table must be int32 [n_req, cols] rows")
+    if lse is not None:
+        _rows(lse, "torch.float32", where, "lse", p.n_tokens, p.h_q)
+    _one_device(where, q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, workspace, lse)
+    table_ld = max(int(block_table.stride(0)), p.table_cols) if p.n_req > 1 else p.table_cols
+    rc = library().dsa_kv8_attn_fwd(_ptr(q), q_ld, q_hd, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                                    _ptr(block_table), table_ld, _ptr(cu_q), _ptr(kv_lens), _ptr(out), out_ld, out_hd,
+                                    _ptr(lse), ctypes.byref(p), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
 
 
 def dsa_sparse_attn_read_status(workspace, stream=None) -> int:
