@@ -127,7 +127,8 @@ def test_extreme_magnitudes():
     k[5] *= 2.0 ** 60
     k[6] = -448.0 * 2.0 ** 64
     slots = np.array([0, 16, 32, 48, 64, 80 + 3, 80 + 4, 80 + 5, 1, 17, 33, 49])
-    cache.insert(k, k.flip(0), slots)
+    for a, b in ((0, 8), (8, 12)):   # the second call continues pages of the first
+        cache.insert(k[a:b], k.flip(0)[a:b], slots[a:b])
 
 
 def test_non_finite_values_stay_in_their_page():
@@ -140,7 +141,7 @@ def test_non_finite_values_stay_in_their_page():
     kp, ks, vp, vs = cache.dev
     native.dsa_kv8_insert(k, k, torch.tensor([3, 32, 33], device="cuda"), kp, vp, ks, vs)
     assert kp[0, 0, 3, 5].item() == 0x7E            # an infinity saturates
-    assert (kp[2, 0, 1, 7].item() & 0x7F) == 0x7F   # the NaN code
+    assert (kp[2, 0, 0, 7].item() & 0x7F) == 0x7F   # the NaN code
     assert ks[2, 0].item() == 2.0 ** -8             # the NaN does not change the scale of 1.0s
     for i in (0, 2):
         assert np.array_equal(cache.dev[i][1].cpu().numpy(), before[i][1])

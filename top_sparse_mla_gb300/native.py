@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 from .build import LIB_PATH
 
 DSA_OK = 0
@@ -201,7 +203,6 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
-        import torch
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -269,26 +270,41 @@ def dsa_kv_insert(kv, positions, slots, kv_norm_w, pool, rms_eps: float = 1e-6, 
         raise DsaError(rc, "dsa_kv_insert")
 
 
-def _require(ok: bool, where: str, what: str) -> None:
-    if not ok:
-        raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {what}")
+def _refuse(where: str, what: str) -> None:
+    raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {what}")
 
 
-def _rows(x, dtype: str, where: str, name: str, *shape) -> None:
-    """x is a dense device tensor of this dtype and shape (None: any extent)."""
-    if str(x.dtype) != dtype or x.dim() != len(shape) or not x.is_contiguous() or any(
-            n is not None and int(m) != n for m, n in zip(x.shape, shape)):
-        raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {name} must be a contiguous {dtype} tensor of shape "
-                       f"{tuple('any' if n is None else n for n in shape)}, got {x.dtype} {tuple(x.shape)}")
+def _device(where: str, x) -> int:
+    """The current CUDA device, where the library launches; x has to be on it."""
+    dev = x.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _refuse(where, "every tensor must be on the current CUDA device")
+    return dev
 
 
-def _one_device(where: str, *tensors) -> None:
-    """All tensors on the current CUDA device (the library launches there)."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for x in tensors:
-        if x is not None and (not x.is_cuda or x.device.index != dev):
-            raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: every tensor must be on the current CUDA device")
+def _dense(where: str, dev: int, *specs) -> None:
+    """Each (tensor, name, dtype, shape) is a contiguous tensor of that dtype and shape on device dev."""
+    for x, name, dtype, shape in specs:
+        if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
+            _refuse(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current CUDA "
+                    f"device, got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _table_pitch(where: str, dev: int, x, n_req: int, cols: int) -> int:
+    """Row pitch of a block table: int32 [n_req, cols] with dense rows."""
+    if (x.dtype is not torch.int32 or x.shape != (n_req, cols) or (cols > 1 and x.stride(1) != 1)
+            or x.get_device() != dev):
+        _refuse(where, "block_table must be an int32 [n_req, cols] tensor with dense rows on the current CUDA device")
+    return max(x.stride(0), cols) if n_req > 1 else cols
+
+
+def _heads(where: str, dev: int, x, name: str, dtype, n: int, h: int, d: int):
+    """(token pitch, head pitch) of a [n, h, d] tensor whose last dimension is dense."""
+    if x.dtype is not dtype or x.shape != (n, h, d) or (n > 0 and x.stride(2) != 1) or x.get_device() != dev:
+        _refuse(where, f"{name} must be a {dtype} tensor of shape {(n, h, d)} with a dense last dimension on the "
+                f"current CUDA device, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    # a pitch that no second row uses may be anything: give the dense one
+    return (x.stride(0) if n > 1 else h * d), (x.stride(1) if h > 1 else d)
 
 
 def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu_new, kv_lens, positions, slots,
@@ -298,48 +314,35 @@ def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu
     free_pages: int32 [n_free]; cu_new: int32 [n_req + 1]; positions, token_req (or None):
     int32 [n_tokens]; slots: int64 [n_tokens]; info: int32 [2] (pages taken, status bits)."""
     where = "dsa_page_map"
-    n_req, n_tokens = int(ctx_lens.shape[0]), int(slots.shape[0])
-    i32 = "torch.int32"
-    _rows(ctx_lens, i32, where, "ctx_lens", n_req)
-    _rows(new_lens, i32, where, "new_lens", n_req)
-    _rows(free_pages, i32, where, "free_pages", None)
-    _rows(cu_new, i32, where, "cu_new", n_req + 1)
-    _rows(kv_lens, i32, where, "kv_lens", n_req)
-    _rows(positions, i32, where, "positions", n_tokens)
-    _rows(slots, "torch.int64", where, "slots", n_tokens)
+    n_req, n_tokens, cols = ctx_lens.shape[0], slots.shape[0], block_table.shape[-1]
+    dev = _device(where, ctx_lens)
+    i32 = torch.int32
+    by_token, by_req = (n_tokens,), (n_req,)
+    _dense(where, dev, (ctx_lens, "ctx_lens", i32, by_req), (new_lens, "new_lens", i32, by_req),
+           (free_pages, "free_pages", i32, (free_pages.shape[0],)), (cu_new, "cu_new", i32, (n_req + 1,)),
+           (kv_lens, "kv_lens", i32, by_req), (positions, "positions", i32, by_token),
+           (slots, "slots", torch.int64, by_token), (info, "info", i32, (2,)))
     if token_req is not None:
-        _rows(token_req, i32, where, "token_req", n_tokens)
-    _rows(info, i32, where, "info", 2)
-    cols = int(block_table.shape[1]) if block_table.dim() == 2 else 0
-    _require(str(block_table.dtype) == i32 and block_table.dim() == 2 and int(block_table.shape[0]) == n_req
-             and (cols <= 1 or int(block_table.stride(1)) == 1), where, "block_table must be int32 [n_req, cols] rows")
-    _one_device(where, ctx_lens, new_lens, block_table, free_pages, cu_new, kv_lens, positions, slots, token_req, info)
-    ld = max(int(block_table.stride(0)), cols) if n_req > 1 else cols
-    rc = library().dsa_page_map(_ptr(ctx_lens), _ptr(new_lens), n_req, _ptr(block_table), ld, cols, _ptr(free_pages),
-                                int(free_pages.shape[0]), int(page_size), n_tokens, _ptr(cu_new), _ptr(kv_lens),
-                                _ptr(positions), _ptr(slots), _ptr(token_req), _ptr(info), _stream(stream))
+        _dense(where, dev, (token_req, "token_req", i32, by_token))
+    ld = _table_pitch(where, dev, block_table, n_req, cols)
+    rc = library().dsa_page_map(ctx_lens.data_ptr(), new_lens.data_ptr(), n_req, block_table.data_ptr(), ld, cols,
+                                free_pages.data_ptr(), free_pages.shape[0], page_size, n_tokens, cu_new.data_ptr(),
+                                kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), _ptr(token_req),
+                                info.data_ptr(), _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
 
-_KV8_TYPES = {"torch.bfloat16": DSA_KV8_BF16, "torch.float16": DSA_KV8_FP16}
+_KV8_TYPES = {torch.bfloat16: DSA_KV8_BF16, torch.float16: DSA_KV8_FP16}
 
 
-def _kv8_pools(where, k_pool, v_pool, k_scale, v_scale):
-    _rows(k_pool, "torch.uint8", where, "k_pool", None, None, None, None)
-    n_pages, h_kv, page, d = (int(x) for x in k_pool.shape)
-    _rows(v_pool, "torch.uint8", where, "v_pool", n_pages, h_kv, page, d)
-    _rows(k_scale, "torch.float32", where, "k_scale", n_pages, h_kv)
-    _rows(v_scale, "torch.float32", where, "v_scale", n_pages, h_kv)
-    return n_pages, h_kv, page, d
-
-
-def _heads(where, x, name, n, h, d, dtype=None):
-    """(token pitch, head pitch) of a [n, h, d] tensor whose last dimension is dense."""
-    _require(x.dim() == 3 and tuple(int(m) for m in x.shape) == (n, h, d) and (x.numel() == 0 or int(x.stride(2)) == 1)
-             and (dtype is None or x.dtype == dtype), where, f"{name} must be [{n}, {h}, {d}] with a dense last dimension")
-    # a pitch that no second row uses may be anything: give the dense one
-    return (int(x.stride(0)) if n > 1 else max(h * d, 8)), (int(x.stride(1)) if h > 1 else d)
+def _kv8_pools(where, dev, k_pool, v_pool, k_scale, v_scale):
+    shape = k_pool.shape
+    if len(shape) != 4:
+        _refuse(where, "k_pool must be [n_pages, h_kv, page_size, d]")
+    _dense(where, dev, (k_pool, "k_pool", torch.uint8, shape), (v_pool, "v_pool", torch.uint8, shape),
+           (k_scale, "k_scale", torch.float32, shape[:2]), (v_scale, "v_scale", torch.float32, shape[:2]))
+    return shape
 
 
 def dsa_kv8_insert(k, v, slots, k_pool, v_pool, k_scale, v_scale, status=None, stream=None) -> None:
@@ -348,16 +351,19 @@ def dsa_kv8_insert(k, v, slots, k_pool, v_pool, k_scale, v_scale, status=None, s
     [n_tokens] (< 0 = skip); k_pool, v_pool: uint8 [n_pages, h_kv, page_size, d]; k_scale,
     v_scale: fp32 [n_pages, h_kv]; status: uint32 or int32 [1] device tensor or None."""
     where = "dsa_kv8_insert"
-    n_pages, h_kv, page, d = _kv8_pools(where, k_pool, v_pool, k_scale, v_scale)
-    n = int(slots.shape[0])
-    _rows(slots, "torch.int64", where, "slots", n)
-    _require(str(k.dtype) in _KV8_TYPES, where, "k must be bfloat16 or float16")
-    k_ld, k_hd = _heads(where, k, "k", n, h_kv, d)
-    v_ld, v_hd = _heads(where, v, "v", n, h_kv, d, k.dtype)
-    _one_device(where, k, v, slots, k_pool, v_pool, k_scale, v_scale, status)
-    rc = library().dsa_kv8_insert(_ptr(k), k_ld, k_hd, _ptr(v), v_ld, v_hd, _ptr(slots), n, _KV8_TYPES[str(k.dtype)],
-                                  _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), n_pages, h_kv, page, d,
-                                  _ptr(status), _stream(stream))
+    dev = _device(where, k)
+    n_pages, h_kv, page, d = _kv8_pools(where, dev, k_pool, v_pool, k_scale, v_scale)
+    n, dtype = slots.shape[0], k.dtype
+    if dtype not in _KV8_TYPES:
+        _refuse(where, "k must be bfloat16 or float16")
+    _dense(where, dev, (slots, "slots", torch.int64, (n,)))
+    k_ld, k_hd = _heads(where, dev, k, "k", dtype, n, h_kv, d)
+    v_ld, v_hd = _heads(where, dev, v, "v", dtype, n, h_kv, d)
+    if status is not None and (status.element_size() != 4 or status.get_device() != dev):
+        _refuse(where, "status must be a 32-bit word on the current CUDA device")
+    rc = library().dsa_kv8_insert(k.data_ptr(), k_ld, k_hd, v.data_ptr(), v_ld, v_hd, slots.data_ptr(), n,
+                                  _KV8_TYPES[dtype], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+                                  v_scale.data_ptr(), n_pages, h_kv, page, d, _ptr(status), _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
@@ -368,19 +374,21 @@ def dsa_kv8_params_init(q, k_pool, block_table, max_q_len=None, **overrides) -> 
     [n_req, cols]. max_q_len: most query rows of a request (default: n_tokens);
     overrides: window, softmax_scale."""
     where = "dsa_kv8_params_init"
-    _require(q.dim() == 3 and k_pool.dim() == 4 and block_table.dim() == 2 and str(q.dtype) in _KV8_TYPES
-             and int(q.shape[2]) == int(k_pool.shape[3]), where, "q, k_pool and block_table do not belong together")
+    if (q.dim() != 3 or k_pool.dim() != 4 or block_table.dim() != 2 or q.dtype not in _KV8_TYPES
+            or q.shape[2] != k_pool.shape[3]):
+        _refuse(where, "q, k_pool and block_table do not belong together")
     p = DsaKv8Params()
     n_pages, h_kv, page, d = (int(x) for x in k_pool.shape)
     rc = library().dsa_kv8_params_init(ctypes.byref(p), int(q.shape[0]), int(block_table.shape[0]), int(q.shape[1]),
                                        h_kv, d, page, n_pages, int(block_table.shape[1]))
     if rc != DSA_OK:
         raise DsaError(rc, where)
-    p.type = _KV8_TYPES[str(q.dtype)]
+    p.type = _KV8_TYPES[q.dtype]
     if max_q_len is not None:
         p.max_q_len = int(max_q_len)
     for name, value in overrides.items():
-        _require(name in ("window", "softmax_scale", "flags"), where, f"unknown parameter {name}")
+        if name not in ("window", "softmax_scale", "flags"):
+            _refuse(where, f"unknown parameter {name}")
         setattr(p, name, value)
     return p
 
@@ -400,23 +408,24 @@ def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_
     int32 [n_req]; lse: fp32 [n_tokens, h_q] or None; workspace: uint8, 256-byte aligned
     (dsa_kv8_attn_workspace_size(p) bytes)."""
     where = "dsa_kv8_attn_fwd"
-    n_pages, h_kv, page, d = _kv8_pools(where, k_pool, v_pool, k_scale, v_scale)
-    _require((n_pages, h_kv, page, d) == (p.n_pages, p.h_kv, p.page_size, p.d), where, "the pools are not p's")
-    _require(_KV8_TYPES.get(str(q.dtype)) == p.type, where, "q's type is not p's")
-    q_ld, q_hd = _heads(where, q, "q", p.n_tokens, p.h_q, d)
-    out_ld, out_hd = _heads(where, out, "out", p.n_tokens, p.h_q, d, q.dtype)
-    _rows(cu_q, "torch.int32", where, "cu_q", p.n_req + 1)
-    _rows(kv_lens, "torch.int32", where, "kv_lens", p.n_req)
-    _require(str(block_table.dtype) == "torch.int32" and tuple(block_table.shape) == (p.n_req, p.table_cols)
-             and (p.table_cols <= 1 or int(block_table.stride(1)) == 1), where, "block_table must be int32 [n_req, cols] rows")
+    dev = _device(where, q)
+    if _kv8_pools(where, dev, k_pool, v_pool, k_scale, v_scale) != (p.n_pages, p.h_kv, p.page_size, p.d):
+        _refuse(where, "the pools are not those of p")
+    n, h_q, n_req, dtype = p.n_tokens, p.h_q, p.n_req, q.dtype
+    if _KV8_TYPES.get(dtype) != p.type:
+        _refuse(where, "q's type is not that of p")
+    q_ld, q_hd = _heads(where, dev, q, "q", dtype, n, h_q, p.d)
+    out_ld, out_hd = _heads(where, dev, out, "out", dtype, n, h_q, p.d)
+    _dense(where, dev, (cu_q, "cu_q", torch.int32, (n_req + 1,)), (kv_lens, "kv_lens", torch.int32, (n_req,)))
     if lse is not None:
-        _rows(lse, "torch.float32", where, "lse", p.n_tokens, p.h_q)
-    _one_device(where, q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, workspace, lse)
-    table_ld = max(int(block_table.stride(0)), p.table_cols) if p.n_req > 1 else p.table_cols
-    rc = library().dsa_kv8_attn_fwd(_ptr(q), q_ld, q_hd, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                                    _ptr(block_table), table_ld, _ptr(cu_q), _ptr(kv_lens), _ptr(out), out_ld, out_hd,
-                                    _ptr(lse), ctypes.byref(p), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
+        _dense(where, dev, (lse, "lse", torch.float32, (n, h_q)))
+    table_ld = _table_pitch(where, dev, block_table, n_req, p.table_cols)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(where, "the workspace must be contiguous and on the current CUDA device")
+    rc = library().dsa_kv8_attn_fwd(q.data_ptr(), q_ld, q_hd, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), block_table.data_ptr(), table_ld, cu_q.data_ptr(),
+                                    kv_lens.data_ptr(), out.data_ptr(), out_ld, out_hd, _ptr(lse), ctypes.byref(p),
+                                    workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
