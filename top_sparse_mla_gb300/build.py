@@ -11,8 +11,8 @@ from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
-SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("dsa_sparse_attn.cu", "dsa_kv8_attn.cu", "dsa_kv8_insert.cu",
-                                                      "dsa_topk.cu", "dsa_kv_insert.cu", "dsa_page_map.cu")]
+SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("dsa_sparse_attn.cu", "dsa_kv8_attn.cu", "dsa_kv8_tiles.cu",
+                                                      "dsa_kv8_insert.cu", "dsa_topk.cu", "dsa_kv_insert.cu", "dsa_page_map.cu")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libdsa_sparse_attn.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
@@ -37,8 +37,9 @@ def _run(cmd, verbose: bool) -> None:
 def build(verbose: bool = False, extra_flags=None) -> str:
     """Build the shared library if any source is newer than it; return its path.  The
     sources are compiled at the same time, one nvcc each, and then linked."""
-    headers = [os.path.join(INCLUDE, h) for h in sorted(os.listdir(INCLUDE)) if h.endswith(".h")]
-    deps = SOURCES + headers + [os.path.join(PKG_DIR, "csrc", "ptx_sm103.cuh"), os.path.abspath(__file__)]
+    csrc = os.path.join(PKG_DIR, "csrc")
+    headers = [os.path.join(where, h) for where in (INCLUDE, csrc) for h in sorted(os.listdir(where)) if h.endswith((".h", ".cuh"))]
+    deps = SOURCES + headers + [os.path.abspath(__file__)]
     if os.path.exists(LIB_PATH) and all(os.path.getmtime(LIB_PATH) >= os.path.getmtime(d) for d in deps):
         return LIB_PATH
     flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, *(extra_flags or [])]

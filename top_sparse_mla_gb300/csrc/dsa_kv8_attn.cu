@@ -13,83 +13,16 @@
 // l = sum w / v_scale is the softmax's sum: w is at most 2^8 (the maximum may lag by 8),
 // whatever the scales' magnitudes, so that it fits fp16.
 
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <math.h>
-#include <mutex>
-#include <stdint.h>
-
-#include "dsa_kv8.h"
-#include "ptx_sm103.cuh"
+#include "dsa_kv8.cuh"
 
 namespace dsa_kv8 {
 
-constexpr int STEP = 16;          // cached tokens of one step of a warp; every page size is a multiple
 constexpr int MAX_ROWS = 32;      // most query rows of a request in rows_kernel
-constexpr int TILE_ROWS = 32;     // query rows of a tile
 constexpr int ROW_WARPS = 4;      // warps of a rows_kernel CTA
 constexpr int CTAS_PER_SM = 4;    // the plan's CTAs per SM
 constexpr int MIN_STEPS = 8;      // a CTA's least share, in steps: two for each warp
 constexpr int PLAN_THREADS = 1024;
 constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
-constexpr float LAG = 8.0f;
-
-struct Share {   // where a CTA's share of the steps begins
-  int req, head;
-  long long step;
-};
-
-struct Header {
-  uint32_t status;
-  int n_tiles;
-  long long share;   // steps of every CTA
-};
-
-struct Params {
-  const uint16_t* q;
-  const uint8_t *k_pool, *v_pool;
-  const float *k_scale, *v_scale;
-  const int32_t *table, *cu_q, *kv_lens;
-  uint16_t* out;
-  float* lse;
-  long long q_ld, q_hd, out_ld, out_hd, table_ld;
-  Header* header;
-  Share* shares;
-  int* arrived;
-  int2* tiles;
-  float* partial;
-  int n_tokens, n_req, h_q, h_kv, group, n_pages, page_shift, cap, max_q_len, window, fp16;
-  int small_rows;   // requests with at most this many rows go to rows_kernel
-  int n_shares, max_tiles;
-  float scale_log2;   // softmax_scale * log2 e
-};
-
-struct Request {
-  int q0, q_len, kv;
-  __device__ __forceinline__ int rows(const Params& P) const { return q_len * P.group; }
-};
-
-__device__ __forceinline__ Request request(const Params& P, int r) {
-  Request a;
-  a.q0 = min(max(P.cu_q[r], 0), P.n_tokens);
-  a.q_len = min(max(P.cu_q[r + 1], a.q0), P.n_tokens) - a.q0;
-  a.kv = min(max(P.kv_lens[r], 0), P.cap);
-  return a;
-}
-
-// The cached tokens [lo, hi) that the query positions [p0, p1] may see, lo rounded down to
-// a step.  Never empty: a row that sees nothing is still computed, and its result is 0.
-struct Span {
-  int lo, steps;
-};
-__device__ __forceinline__ Span span(const Params& P, const Request& a, int i0, int i1) {
-  const int p0 = a.kv - a.q_len + i0, p1 = a.kv - a.q_len + i1;
-  Span s;
-  s.lo = P.window > 0 ? max(p0 - P.window + 1, 0) & ~(STEP - 1) : 0;
-  s.steps = max((p1 + 1 - s.lo + STEP - 1) / STEP, 1);
-  if (p1 + 1 <= s.lo) s.steps = 1;
-  return s;
-}
 
 // ------------------------------------------------------------------------------ plan
 // The steps of the small requests, all heads of all requests in a row, are cut into equal
@@ -190,7 +123,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       const int mid = (lo + hi) >> 1;
       if (s_tile[mid] <= i) lo = mid; else hi = mid;
     }
-    P.tiles[i] = make_int2(lo, (int)(i - s_tile[lo]));
+    const Request a = request(P, lo);
+    const int row0 = (int)(i - s_tile[lo]) * TILE_ROWS, row1 = min(row0 + TILE_ROWS, a.rows(P)) - 1;
+    Tile t;
+    t.req = lo;
+    t.row0 = row0;
+    t.q0 = a.q0;
+    t.rows = a.rows(P);
+    t.pos0 = a.kv - a.q_len;
+    t.lo = span(P, a, row0 / P.group, row1 / P.group).lo;
+    t.hi = max(t.pos0 + row1 / P.group + 1, 0);
+    t.pad = 0;
+    P.tiles[n_tiles - 1 - i] = t;   // later tiles of a request see more tokens: they go first
   }
   if (tid == 0) {
     P.header->status = s_bad;
@@ -200,11 +144,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 }
 
 // ------------------------------------------------------------------------------ rows
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 sums
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -220,18 +159,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-__device__ __forceinline__ float2 unpack(uint32_t w, int fp16) {
-  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t pack(float a, float b, int fp16) {
-  if (fp16) return dsa::pack_f16x2(a, b);
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
 
 // One warp's share of the steps of a unit (one request or tile, one KV head).
 //
@@ -348,7 +275,7 @@ __device__ __forceinline__ void rows_steps(const Params& P, int req, int head, i
       }
       load_k(page_next, s + stride);
       // t = x + log2(v_scale), masked
-      const float vsc = fminf(fmaxf(vs, 5.421010862427522e-20f), 1.8446744073709552e19f);   // [2^-64, 2^64]
+      const float vsc = bounded_scale(vs);
       const float bias = log2f(vsc), vinv = 1.0f / vsc;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -482,10 +409,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
       }
     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-    // exponent of the largest magnitude, kept where both 2^e factors are normal numbers
-    const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127 - 7, -100), 120) : 0;
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    scale_row[nt] = __uint_as_float((uint32_t)(127 + e) << 23);
+    const float down = row_scaling(mx, scale_row[nt]);
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -678,23 +602,6 @@ __global__ void __launch_bounds__(32 * NW) rows_kernel(const __grid_constant__ P
   }
 }
 
-template <int D, int NW>
-__global__ void __launch_bounds__(32 * NW) tiles_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  RowSmem<D, TILE_ROWS / 8, NW>& S = *reinterpret_cast<RowSmem<D, TILE_ROWS / 8, NW>*>(smem_raw);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = P.header->n_tiles;
-  // later tiles of a request see more tokens: they go first
-  for (long long u = blockIdx.x; u < (long long)n * P.h_kv; u += gridDim.x) {
-    const int2 tile = P.tiles[n - 1 - (int)(u / P.h_kv)];
-    const int head = (int)(u % P.h_kv), row0 = tile.y * TILE_ROWS;
-    const Request a = request(P, tile.x);
-    const int row1 = min(row0 + TILE_ROWS, a.rows(P)) - 1;
-    const Span sp = span(P, a, row0 / P.group, row1 / P.group);
-    rows_unit<D, TILE_ROWS / 8, NW>(P, S, tile.x, a, head, row0, sp, 0, sp.steps, 1, 0, 0);
-  }
-}
-
 // ------------------------------------------------------------------------------ host
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -737,7 +644,7 @@ static Layout layout(const dsa_kv8_params* p, int sms) {
   at += up(L.n_shares * sizeof(int));
   L.tiles = at;
   L.max_tiles = (int)(p->n_tokens * group / TILE_ROWS + p->n_req);
-  at += up((size_t)L.max_tiles * sizeof(int2));
+  at += up((size_t)L.max_tiles * sizeof(Tile));
   L.partial = at;
   at += up((size_t)L.n_shares * 2 * (rows * p->d + 2 * rows) * sizeof(float));
   L.bytes = at;
@@ -775,8 +682,10 @@ static int launch_all(const dsa_kv8_params* p, const Params& P, int sms, cudaStr
       rc = launch(rows_kernel<D, 4, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 4, ROW_WARPS>), st, P, true);
   }
   if (rc != DSA_OK) return rc;
-  if ((long long)p->max_q_len * P.group > P.small_rows)
-    rc = launch(tiles_kernel<D, ROW_WARPS>, 2 * sms, 32 * ROW_WARPS, sizeof(RowSmem<D, TILE_ROWS / 8, ROW_WARPS>), st, P, false);
+  if ((long long)p->max_q_len * P.group > P.small_rows) {
+    const long long units = (long long)P.max_tiles * P.h_kv;
+    rc = launch_tiles(D, (int)(units < sms ? units : sms), P, st);
+  }
   return rc;
 }
 
@@ -866,7 +775,7 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   P.header = reinterpret_cast<Header*>(ws);
   P.shares = reinterpret_cast<Share*>(ws + L.shares);
   P.arrived = reinterpret_cast<int*>(ws + L.arrived);
-  P.tiles = reinterpret_cast<int2*>(ws + L.tiles);
+  P.tiles = reinterpret_cast<Tile*>(ws + L.tiles);
   P.partial = reinterpret_cast<float*>(ws + L.partial);
   P.n_tokens = p->n_tokens;
   P.n_req = p->n_req;

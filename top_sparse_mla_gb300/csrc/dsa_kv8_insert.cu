@@ -21,7 +21,7 @@
 #include "dsa_kv8.h"
 #include "ptx_sm103.cuh"
 
-namespace dsa_kv8 {
+namespace dsa_kv8_insert_impl {
 
 constexpr int THREADS = 256;
 constexpr int WINDOW = 64;   // most tokens in which a CTA's runs start
@@ -204,13 +204,13 @@ static bool bad_pitch(int64_t ld, int64_t hd, int heads, int d) {
   return ld < d || ld % 8 != 0 || hd % 8 != 0 || (heads > 1 && hd < d);
 }
 
-}  // namespace dsa_kv8
+}  // namespace dsa_kv8_insert_impl
 
 extern "C" int dsa_kv8_insert(const void* k, int64_t k_ld, int64_t k_hd, const void* v, int64_t v_ld, int64_t v_hd,
                               const int64_t* slots, int32_t n_tokens, int32_t type, void* k_pool, void* v_pool,
                               float* k_scale, float* v_scale, int32_t n_pages, int32_t h_kv, int32_t page_size,
                               int32_t d, uint32_t* status, void* stream) {
-  using namespace dsa_kv8;
+  using namespace dsa_kv8_insert_impl;
   if (n_tokens < 0 || n_tokens > (1 << 30) || n_pages < 0 || h_kv < 1 || (type != DSA_KV8_BF16 && type != DSA_KV8_FP16))
     return DSA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||

@@ -1,0 +1,523 @@
+// Attention over the paged 8-bit cache for requests with many query rows (prefill): tiles
+// of 256 rows on the tensor cores (tcgen05), as dsa_kv8_attn.cu's plan lists them.
+//
+// One persistent CTA per SM takes units (tile, KV head).  Roles:
+//   - warps 0-3 and 4-7, a softmax group for each half of the tile (128 rows): a thread
+//     owns a query row.  It scales its row to fp16 into shared memory, and for each block
+//     of 128 cached tokens reads its scores from tensor memory, forms the weights and
+//     writes them back as fp16 over the scores; in the end it divides its row of O by the
+//     softmax's sum and stores it.
+//   - warps 8-11: the block's codes from the pages into fp16 tiles in shared memory (K and
+//     V, two buffers each), loaded one block ahead into registers.  A token's row is 128
+//     bytes wide in the 128-byte swizzle, in panels of 64 dims, which serves K as a
+//     K-major and V as an MN-major operand.
+//   - warp 12 issues the products: S = Q K^T (128 x 128 x D) and O += P V (128 x D x 128,
+//     P in tensor memory).  The two halves alternate, so that one half's softmax runs
+//     under the other half's products.
+// Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
+// and the CTA's roles stop, drain the tensor core and free its memory.
+//
+// Scores become u = S * (k_scale * softmax_scale * log2 e * row scaling) + (log2 v_scale - m)
+// with m an integer that may lag behind the row's maximum by 2^LAG: O is rescaled only
+// when a score passes it by more (by a power of two, exactly), which is rare after the
+// first block.
+
+#include "dsa_kv8.cuh"
+
+namespace dsa_kv8 {
+
+using namespace dsa;
+
+constexpr int BLOCK = 128;       // cached tokens of a block
+constexpr int W_DQ = 8, W_MMA = 12, TILE_THREADS = 13 * 32;
+constexpr unsigned long long WAIT_LIMIT_CYCLES = 4000000000ull;   // ~2 s at 2 GHz
+
+// barriers
+enum { B_KFULL = 0, B_KFREE = 2, B_VFULL = 4, B_VFREE = 6, B_SFULL = 8, B_PFULL = 10, B_QFULL = 12, B_OFULL = 14, B_SCALES = 16, B_DRAIN = 20, N_BAR };
+constexpr int N_SCALES = 4;      // blocks whose scales are kept: see dequant()
+
+template <int D>
+struct TileSmem {
+  static constexpr int OPERAND = BLOCK * D * 2;   // a K, V or half-Q tile in fp16
+  static constexpr int PANEL = BLOCK * 128;       // 64 dims of it
+  static constexpr int Q = 0, K = 2 * OPERAND, V = 4 * OPERAND, SCALES = 6 * OPERAND;
+  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * N_BAR + 8, BYTES = MISC + 16;
+};
+template <int D>
+struct Tmem {   // columns
+  static constexpr int S = 0, O = 256, COLS = 512;   // S and O of half t at S + 128 t, O + D t
+};
+
+struct Ctx {
+  uint8_t* sm;
+  uint32_t sb, bars;
+  volatile int* misc;   // [0]: tensor memory address, [1]: abort
+  uint32_t* status;
+};
+
+DSA_DEV uint32_t bar(const Ctx& c, int i) { return c.bars + 8u * (uint32_t)i; }
+DSA_DEV void arrive_w(const Ctx& c, int b) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar(c, b));
+}
+// The waiting part of a bounded wait, out of line.  False when the limit passes or when
+// another thread of the CTA has given up.
+__device__ __noinline__ bool wait_slow(uint32_t addr, uint32_t parity, volatile int* misc, uint32_t* status) {
+  const unsigned long long start = clock64();
+  while (true) {
+    if (mbar_wait_susp(addr, parity)) return true;
+    if (misc[1]) return false;
+    if (clock64() - start > WAIT_LIMIT_CYCLES) {
+      atomicOr(status, DSA_STATUS_WAIT_TIMEOUT);
+      misc[1] = 1;
+      return false;
+    }
+  }
+}
+// The whole warp waits and agrees on the outcome.
+DSA_DEV bool wait_w(const Ctx& c, int b, uint32_t parity) {
+  const uint32_t addr = bar(c, b);
+  const bool ok = mbar_try(addr, parity) || wait_slow(addr, parity, c.misc, c.status);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+DSA_DEV bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+DSA_DEV void commit(uint32_t bar_addr) {
+  if (elect_one()) tc_commit(bar_addr);
+  __syncwarp();
+}
+
+// A unit as every role sees it.
+struct Unit {
+  Tile t;
+  int head;
+  int blocks[2];   // blocks of each half; 0 for a half without rows
+};
+DSA_DEV bool unit(const Params& P, long long u, int n_tiles, Unit& x) {
+  if (u >= (long long)n_tiles * P.h_kv) return false;
+  const int i = (int)(u / P.h_kv);
+  x.head = (int)(u - (long long)i * P.h_kv);
+  const int4* at = reinterpret_cast<const int4*>(P.tiles + i);
+  const int4 a = __ldg(at), b = __ldg(at + 1);
+  x.t.req = a.x; x.t.row0 = a.y; x.t.q0 = a.z; x.t.rows = a.w;
+  x.t.pos0 = b.x; x.t.lo = b.y; x.t.hi = b.z;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r0 = x.t.row0 + 128 * h, r1 = min(r0 + 128, x.t.rows) - 1;
+    const int hi = x.t.pos0 + r1 / P.group + 1;   // past the last token that the half sees
+    x.blocks[h] = r0 < x.t.rows ? max((hi - x.t.lo + BLOCK - 1) / BLOCK, 1) : 0;
+    if (r0 < x.t.rows && hi <= x.t.lo) x.blocks[h] = 1;
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------------------ codes
+// Block i of the CTA (over all units) uses buffer i % 2 of K and V.  Its scales are in
+// slot i % 4: K's buffer is written two blocks ahead of the softmax, which reads the
+// scales of the block it is at.  When the buffer of block i is free (the products of
+// block i - 2 are done, for which the weights of block i - 3 were needed), the softmax has
+// left block i - 3: slots i - 2, i - 1 and i are in use.  (The scales have barriers of
+// their own: K's could complete a phase more before the softmax looks at it.)
+template <int D>
+DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
+  using SM = TileSmem<D>;
+  constexpr int CHUNKS = D / 16;            // 16-byte chunks of a row
+  constexpr int ROWS = 128 / CHUNKS;        // rows of one pass of the 128 threads
+  constexpr int PASSES = BLOCK / ROWS;      // 8, or 4 for D = 64
+  const int tid = threadIdx.x - 32 * W_DQ;
+  const int chunk = tid % CHUNKS, sub = tid / CHUNKS;
+  const int page_mask = (1 << P.page_shift) - 1;
+  // the two 16-byte units of fp16 that a chunk of codes becomes; panels alternate the
+  // order in which they are stored, so that a quarter warp meets no bank conflict
+  const int panel = chunk >> 2, u0 = 2 * (chunk & 3), flip = panel & 1;
+  uint32_t g = 0;
+  Unit x;
+  for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
+    const int blocks = max(x.blocks[0], x.blocks[1]);
+    const int32_t* table = P.table + x.t.req * P.table_ld;
+    const int p_first = x.t.pos0 + x.t.row0 / P.group;
+    const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
+    // pages of the thread's rows in a block (rows sub + ROWS * p); -1 where there is nothing
+    int page[PASSES];
+    auto find_pages = [&](int i) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int j = x.t.lo + i * BLOCK + p * ROWS + sub;
+        int id = -1;
+        if (i < blocks && j < x.t.hi) id = __ldg(table + (j >> P.page_shift));
+        page[p] = (id < 0 || id >= P.n_pages) ? -1 : id;
+      }
+    };
+    uint4 kr[PASSES], vr[PASSES];
+    auto load = [&](const uint8_t* pool, uint4 (&r)[PASSES], int i, bool only_seen) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int j = x.t.lo + i * BLOCK + p * ROWS + sub;
+        r[p] = make_uint4(0u, 0u, 0u, 0u);
+        // values outside what any row sees may be NaN codes, and 0 * NaN is not 0
+        if (page[p] >= 0 && (!only_seen || j >= seen_lo))
+          r[p] = ldg_nc(pool + ((((long long)page[p] * P.h_kv + x.head) << P.page_shift) + (j & page_mask)) * D + 16 * chunk);
+      }
+    };
+    auto store = [&](int at, const uint4 (&r)[PASSES]) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int row = p * ROWS + sub;
+        uint32_t h[8];
+        codes16_to_f16(r[p], h);
+        const uint32_t base = c.sb + at + panel * SM::PANEL + row * 128;
+        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+        sts128(base + (((u0 + flip) ^ (row & 7)) << 4), flip ? b : a);
+        sts128(base + (((u0 + 1 - flip) ^ (row & 7)) << 4), flip ? a : b);
+      }
+    };
+    // the scales of group `tid` of 16 tokens, by the first eight threads
+    float ks = 1.f, vs = 1.f;
+    bool there = false;
+    auto load_scales = [&](int i) {
+      if (tid < 8) {
+        const int j = x.t.lo + i * BLOCK + 16 * tid;
+        int id = -1;
+        if (i < blocks && j < x.t.hi) id = __ldg(table + (j >> P.page_shift));
+        there = id >= 0 && id < P.n_pages;
+        if (there) {
+          ks = __ldg(P.k_scale + (long long)id * P.h_kv + x.head);
+          vs = bounded_scale(__ldg(P.v_scale + (long long)id * P.h_kv + x.head));
+        }
+      }
+    };
+    find_pages(0);
+    load(P.k_pool, kr, 0, false);
+    load(P.v_pool, vr, 0, true);
+    load_scales(0);
+    for (int i = 0; i < blocks; ++i, ++g) {
+      const int buf = g & 1;
+      const uint32_t free_parity = ((g >> 1) & 1) ^ 1;
+      find_pages(i + 1);
+      if (!wait_w(c, B_KFREE + buf, free_parity)) return;
+      store(SM::K + buf * SM::OPERAND, kr);
+      if (tid < 8) {
+        float4* s = reinterpret_cast<float4*>(c.sm + SM::SCALES) + (g % N_SCALES) * 8 + tid;
+        *s = make_float4(ks * P.scale_log2, there ? log2f(vs) : -INFINITY, 1.0f / vs, 0.f);
+        if (!there) *s = make_float4(0.f, -INFINITY, 1.f, 0.f);
+      }
+      if (tid < 32) arrive_w(c, B_SCALES + g % N_SCALES);
+      fence_async_smem();
+      arrive_w(c, B_KFULL + buf);
+      load(P.k_pool, kr, i + 1, false);
+      load_scales(i + 1);
+      if (!wait_w(c, B_VFREE + buf, free_parity)) return;
+      store(SM::V + buf * SM::OPERAND, vr);
+      fence_async_smem();
+      arrive_w(c, B_VFULL + buf);
+      load(P.v_pool, vr, i + 1, true);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ products
+template <int D>
+DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles) {
+  using SM = TileSmem<D>;
+  using TM = Tmem<D>;
+  constexpr uint32_t ID_QK = idesc_f16(128, BLOCK, 0, 0);
+  constexpr uint32_t ID_PV = idesc_f16(128, D, 0, 1);
+  const uint64_t d_q = sdesc(c.sb + SM::Q, 16, 1024);
+  const uint64_t d_k = sdesc(c.sb + SM::K, 16, 1024);
+  const uint64_t d_v = sdesc(c.sb + SM::V, SM::PANEL, 1024);
+  uint32_t g = 0;                 // blocks
+  uint32_t np[2] = {0, 0};        // blocks of each half
+  uint32_t nq[2] = {0, 0};        // units of each half
+  Unit x;
+  for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
+    const int blocks = max(x.blocks[0], x.blocks[1]);
+    for (int i = 0; i <= blocks; ++i) {
+      const int kb = (g + i) & 1, vb = (g + i - 1) & 1;
+      if (i < blocks && !wait_w(c, B_KFULL + kb, ((g + i) >> 1) & 1)) return;
+      if (i > 0 && !wait_w(c, B_VFULL + vb, ((g + i - 1) >> 1) & 1)) return;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (i > 0 && i - 1 < x.blocks[h]) {
+          if (!wait_w(c, B_PFULL + h, np[h] & 1)) return;
+          ++np[h];
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < BLOCK / 16; ++k) {
+            if (elect_one())
+              mma_ts(tmem + TM::O + D * h, tmem + TM::S + 128 * h + 8 * k,
+                     d_v + ((uint32_t)(vb * SM::OPERAND + k * 2048) >> 4), ID_PV, (i > 1 || k > 0) ? 1u : 0u);
+            __syncwarp();
+          }
+          if (i == x.blocks[h]) commit(bar(c, B_OFULL + h));
+        }
+        if (i < x.blocks[h]) {
+          if (i == 0) {
+            if (!wait_w(c, B_QFULL + h, nq[h] & 1)) return;
+            ++nq[h];
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * SM::PANEL + (k & 3) * 32;
+            if (elect_one())
+              mma_ss(tmem + TM::S + 128 * h, d_q + ((h * SM::OPERAND + off) >> 4), d_k + ((kb * SM::OPERAND + off) >> 4),
+                     ID_QK, k ? 1u : 0u);
+            __syncwarp();
+          }
+          commit(bar(c, B_SFULL + h));
+        }
+      }
+      if (i < blocks) commit(bar(c, B_KFREE + kb));
+      if (i > 0) commit(bar(c, B_VFREE + vb));
+    }
+    g += blocks;
+  }
+}
+
+// ------------------------------------------------------------------------------ softmax
+template <int D>
+DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, int h) {
+  using SM = TileSmem<D>;
+  using TM = Tmem<D>;
+  const int row_in = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;   // the warp's 32 lanes of tensor memory
+  const uint32_t ts = tmem + lanes + TM::S + 128 * h, to = tmem + lanes + TM::O + D * h;
+  uint32_t g = 0, ns = 0, no = 0;
+  Unit x;
+  for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
+    const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
+    if (mine == 0) {
+      g += blocks;
+      continue;
+    }
+    const int first = x.t.row0 + 128 * h, row = first + row_in;
+    const bool live = row < x.t.rows;
+    const int qi = min(row, x.t.rows - 1) / P.group;
+    const int pos = x.t.pos0 + qi;
+    const int pos_min = x.t.pos0 + first / P.group, pos_max = x.t.pos0 + min(first + 127, x.t.rows - 1) / P.group;
+    const int head = x.head * P.group + row - qi * P.group;
+    // ---- the query row (its buffer was last read for this half's last scores)
+    float row_scale;
+    {
+      const uint16_t* src = P.q + (x.t.q0 + qi) * P.q_ld + head * P.q_hd;
+      uint4 v[D / 8];
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) v[k] = live ? ldg_nc(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack(word(v[k], e), P.fp16);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      const float down = row_scaling(mx, row_scale);
+      const uint32_t base = c.sb + SM::Q + h * SM::OPERAND + row_in * 128;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack(word(v[k], e), P.fp16);
+          p[e] = pack_f16x2(f.x * down, f.y * down);
+        }
+        sts128(base + (k >> 3) * SM::PANEL + (((k & 7) ^ (row_in & 7)) << 4), make_uint4(p[0], p[1], p[2], p[3]));
+      }
+      fence_async_smem();
+      tc_fence_before();   // this half's O was read before
+      arrive_w(c, B_QFULL + h);
+    }
+    float m = 0.f, l = 0.f;
+    bool fresh = true;   // m is not set: every score so far was masked
+    for (int i = 0; i < mine; ++i) {
+      const uint32_t gi = g + i;
+      if (!wait_w(c, B_SCALES + gi % N_SCALES, (gi / N_SCALES) & 1)) return;
+      if (!wait_w(c, B_SFULL + h, ns & 1)) return;
+      ++ns;
+      tc_fence_after();
+      const float4* sc = reinterpret_cast<const float4*>(c.sm + SM::SCALES) + (gi % N_SCALES) * 8;
+      const int base = x.t.lo + i * BLOCK;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t a[32], b[32];
+        tmem_ld32(ts + 64 * s, a);
+        tmem_ld32(ts + 64 * s + 32, b);
+        tc_wait_ld();
+        float x2[64];
+        float vinv[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 f = sc[4 * s + q];
+          const float mul = f.x * row_scale, add = f.y - m;
+          vinv[q] = f.z;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x2[16 * q + e] = fmaf(__uint_as_float(q < 2 ? a[16 * (q & 1) + e] : b[16 * (q & 1) + e]), mul, add);
+        }
+        const int j0 = base + 64 * s;
+        if (j0 + 63 > pos_min || (P.window > 0 && j0 <= pos_max - P.window)) {
+          const int last = pos - j0, before = P.window > 0 ? last - P.window : -1;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e > last || e <= before) x2[e] = -INFINITY;
+        }
+        float top = x2[0];
+#pragma unroll
+        for (int e = 1; e < 64; ++e) top = fmaxf(top, x2[e]);
+        const bool up = top > (fresh ? -INFINITY : LAG);
+        if (__any_sync(0xFFFFFFFFu, up)) {
+          const float to_m = up ? floorf(m + top) : m;   // the largest weight is in [1, 2)
+          const float delta = to_m - m, f = (up && !fresh) ? ex2(-delta) : 1.0f;
+          if (up) fresh = false;
+          m = to_m;
+          l *= f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) x2[e] -= delta;
+          if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+            if (i > 0) {
+              // the product of the block before is done: these scores were issued after it
+#pragma unroll 1
+              for (int k = 0; k < D; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + k, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(to + k, o);
+              }
+            }
+            if (s == 1) {   // the weights of the block's first half
+              const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+              for (int k = 0; k < 32; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(ts + k, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f2);
+                  o[e] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+                tmem_st16(ts + k, o);
+              }
+            }
+          }
+        }
+        uint32_t p[32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w0 = ex2(x2[16 * q + 2 * e]), w1 = ex2(x2[16 * q + 2 * e + 1]);
+            sum += w0 + w1;
+            p[8 * q + e] = pack_f16x2(w0, w1);
+          }
+          l = fmaf(sum, vinv[q], l);
+        }
+        tmem_st32(ts + 32 * s, p);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      arrive_w(c, B_PFULL + h);
+    }
+    // ---- result
+    if (!wait_w(c, B_OFULL + h, no & 1)) return;
+    ++no;
+    tc_fence_after();
+    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays one
+    uint16_t* dst = P.out + (x.t.q0 + qi) * P.out_ld + head * P.out_hd;
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+      uint32_t o[32];
+      tmem_ld32(to + k, o);
+      tc_wait_ld();
+      if (live) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 v;
+          v.x = pack(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv, P.fp16);
+          v.y = pack(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv, P.fp16);
+          v.z = pack(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv, P.fp16);
+          v.w = pack(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv, P.fp16);
+          *reinterpret_cast<uint4*>(dst + k + 8 * e) = v;
+        }
+      }
+    }
+    if (live && P.lse)
+      P.lse[(long long)(x.t.q0 + qi) * P.h_q + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+    g += blocks;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_constant__ Params P) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using SM = TileSmem<D>;
+  Ctx c;
+  c.sm = smem;
+  c.sb = smem_u32(smem);
+  c.bars = c.sb + SM::BAR;
+  c.misc = reinterpret_cast<volatile int*>(smem + SM::MISC);
+  c.status = &P.header->status;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(c, B_KFULL + i), 4);
+      mbar_init(bar(c, B_KFREE + i), 1);
+      mbar_init(bar(c, B_VFULL + i), 4);
+      mbar_init(bar(c, B_VFREE + i), 1);
+      mbar_init(bar(c, B_SFULL + i), 1);
+      mbar_init(bar(c, B_PFULL + i), 4);
+      mbar_init(bar(c, B_QFULL + i), 4);
+      mbar_init(bar(c, B_OFULL + i), 1);
+    }
+    for (int i = 0; i < N_SCALES; ++i) mbar_init(bar(c, B_SCALES + i), 1);
+    mbar_init(bar(c, B_DRAIN), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    c.misc[1] = 0;
+  }
+  if (warp == W_MMA) tmem_alloc(c.sb + SM::MISC, Tmem<D>::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)c.misc[0];
+  const int n_tiles = P.header->n_tiles;
+  if (warp < W_DQ) softmax<D>(P, c, tmem, n_tiles, warp >> 2);
+  else if (warp < W_MMA) dequant<D>(P, c, n_tiles);
+  else products<D>(P, c, tmem, n_tiles);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA && (threadIdx.x & 31) == 0) {
+    // every product has completed before tensor memory is released
+    tc_commit(bar(c, B_DRAIN));
+    const unsigned long long start = clock64();
+    while (!mbar_wait_susp(bar(c, B_DRAIN), 0) && clock64() - start < WAIT_LIMIT_CYCLES) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Tmem<D>::COLS);
+  }
+}
+
+template <int D>
+static int launch_one(int grid, const Params& P, cudaStream_t st) {
+  constexpr int smem = TileSmem<D>::BYTES;
+  if (cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  tiles_kernel<D><<<grid, TILE_THREADS, smem, st>>>(P);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+int launch_tiles(int d, int grid, const Params& P, cudaStream_t st) {
+  return d == 128 ? launch_one<128>(grid, P, st) : launch_one<64>(grid, P, st);
+}
+
+}  // namespace dsa_kv8
