@@ -613,7 +613,8 @@ static int check(const dsa_kv8_params* p) {
   if ((p->d != 64 && p->d != 128) ||
       (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) ||
       p->n_req > DSA_KV8_MAX_REQ || p->h_kv > DSA_KV8_MAX_HEADS || p->h_q / p->h_kv > DSA_KV8_MAX_GROUP ||
-      (long long)p->n_tokens * (p->h_q / p->h_kv) >= (1LL << 31))
+      (long long)p->n_tokens * (p->h_q / p->h_kv) >= (1LL << 31) ||
+      (long long)p->n_pages * p->h_kv * p->page_size >= (1LL << 32) - 1)   // rows of a pool are numbered in 32 bits
     return DSA_ERR_UNSUPPORTED_SHAPE;
   return DSA_OK;
 }

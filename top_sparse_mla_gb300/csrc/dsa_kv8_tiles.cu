@@ -122,18 +122,23 @@ DSA_DEV bool unit(const Params& P, long long u, int n_tiles, Unit& x) {
 // block i - 2 are done, for which the weights of block i - 3 were needed), the softmax has
 // left block i - 3: slots i - 2, i - 1 and i are in use.  (The scales have barriers of
 // their own: K's could complete a phase more before the softmax looks at it.)
+// A warp stops at the first use of a value that it is still loading, so a block's table
+// entries are loaded two blocks ahead, its scales and codes one block ahead.
 template <int D>
 DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   using SM = TileSmem<D>;
   constexpr int CHUNKS = D / 16;            // 16-byte chunks of a row
-  constexpr int ROWS = 128 / CHUNKS;        // rows of one pass of the 128 threads
+  constexpr int ROWS = 128 / CHUNKS;        // rows of one pass of the four warps: 16 or 32
   constexpr int PASSES = BLOCK / ROWS;      // 8, or 4 for D = 64
-  const int tid = threadIdx.x - 32 * W_DQ;
-  const int chunk = tid % CHUNKS, sub = tid / CHUNKS;
+  const int w = (threadIdx.x >> 5) - W_DQ, lane = threadIdx.x & 31;
+  // A chunk of codes becomes two 16-byte units of a swizzled row; a quarter warp holds
+  // four chunks of one panel in an even and the odd row behind it, whose units never meet
+  // in a bank.
+  const int chunk = (lane & 3) + (D == 128 ? (lane >> 4) * 4 : 0);
+  const int sub = w * (ROWS / 4) + (D == 128 ? (lane >> 2) & 3 : lane >> 2);   // row of a pass
   const int page_mask = (1 << P.page_shift) - 1;
-  // the two 16-byte units of fp16 that a chunk of codes becomes; panels alternate the
-  // order in which they are stored, so that a quarter warp meets no bank conflict
-  const int panel = chunk >> 2, u0 = 2 * (chunk & 3), flip = panel & 1;
+  const uint32_t store_at = c.sb + (chunk >> 2) * SM::PANEL + sub * 128;
+  const uint32_t s0 = ((2 * (chunk & 3)) ^ (sub & 7)) << 4, s1 = ((2 * (chunk & 3) + 1) ^ (sub & 7)) << 4;
   uint32_t g = 0;
   Unit x;
   for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
@@ -141,85 +146,97 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
     const int32_t* table = P.table + x.t.req * P.table_ld;
     const int p_first = x.t.pos0 + x.t.row0 / P.group;
     const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
-    // pages of the thread's rows in a block (rows sub + ROWS * p); -1 where there is nothing
-    int page[PASSES];
-    auto find_pages = [&](int i) {
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int j = x.t.lo + i * BLOCK + p * ROWS + sub;
-        int id = -1;
-        if (i < blocks && j < x.t.hi) id = __ldg(table + (j >> P.page_shift));
-        page[p] = (id < 0 || id >= P.n_pages) ? -1 : id;
-      }
+    // lane l of every warp looks after group l of the block's eight groups of 16 tokens,
+    // each of which lies in one page
+    auto entry = [&](int i) -> int {
+      const int j = x.t.lo + i * BLOCK + 16 * (lane & 7);
+      return (i < blocks && j < x.t.hi) ? __ldg(table + (j >> P.page_shift)) : -1;
+    };
+    // first row of the group in the pools, NONE where there is no page
+    constexpr uint32_t NONE = 0xFFFFFFFFu;
+    auto rows_of = [&](int raw, int i) -> uint32_t {
+      const int j = x.t.lo + i * BLOCK + 16 * (lane & 7);
+      if (raw < 0 || raw >= P.n_pages) return NONE;
+      return (((uint32_t)raw * P.h_kv + x.head) << P.page_shift) + (j & page_mask);
     };
     uint4 kr[PASSES], vr[PASSES];
-    auto load = [&](const uint8_t* pool, uint4 (&r)[PASSES], int i, bool only_seen) {
+    auto load = [&](const uint8_t* pool, uint4 (&r)[PASSES], uint32_t rows, int i, bool values) {
+      const bool all = __all_sync(0xFFFFFFFFu, rows != NONE);
+      const int j0 = x.t.lo + i * BLOCK;
+      const uint8_t* at = pool + 16 * chunk;
+      if (all && (!values || (j0 >= seen_lo && j0 + BLOCK <= x.t.hi))) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int j = x.t.lo + i * BLOCK + p * ROWS + sub;
-        r[p] = make_uint4(0u, 0u, 0u, 0u);
+        for (int p = 0; p < PASSES; ++p) {
+          const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows, (p * ROWS + sub) >> 4) + (sub & 15);
+          r[p] = ldg_nc(at + (uint64_t)row * D);
+        }
+      } else {
         // values outside what any row sees may be NaN codes, and 0 * NaN is not 0
-        if (page[p] >= 0 && (!only_seen || j >= seen_lo))
-          r[p] = ldg_nc(pool + ((((long long)page[p] * P.h_kv + x.head) << P.page_shift) + (j & page_mask)) * D + 16 * chunk);
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows, (p * ROWS + sub) >> 4);
+          const int j = j0 + p * ROWS + sub;
+          r[p] = make_uint4(0u, 0u, 0u, 0u);
+          if (row != NONE && (!values || (j >= seen_lo && j < x.t.hi))) r[p] = ldg_nc(at + (uint64_t)(row + (sub & 15)) * D);
+        }
       }
     };
     auto store = [&](int at, const uint4 (&r)[PASSES]) {
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
-        const int row = p * ROWS + sub;
         uint32_t h[8];
         codes16_to_f16(r[p], h);
-        const uint32_t base = c.sb + at + panel * SM::PANEL + row * 128;
-        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-        sts128(base + (((u0 + flip) ^ (row & 7)) << 4), flip ? b : a);
-        sts128(base + (((u0 + 1 - flip) ^ (row & 7)) << 4), flip ? a : b);
+        const uint32_t base = store_at + at + p * ROWS * 128;
+        sts128(base + s0, make_uint4(h[0], h[1], h[2], h[3]));
+        sts128(base + s1, make_uint4(h[4], h[5], h[6], h[7]));
       }
     };
-    // the scales of group `tid` of 16 tokens, by the first eight threads
     float ks = 1.f, vs = 1.f;
-    bool there = false;
-    auto load_scales = [&](int i) {
-      if (tid < 8) {
-        const int j = x.t.lo + i * BLOCK + 16 * tid;
-        int id = -1;
-        if (i < blocks && j < x.t.hi) id = __ldg(table + (j >> P.page_shift));
-        there = id >= 0 && id < P.n_pages;
-        if (there) {
-          ks = __ldg(P.k_scale + (long long)id * P.h_kv + x.head);
-          vs = bounded_scale(__ldg(P.v_scale + (long long)id * P.h_kv + x.head));
-        }
+    auto load_scales = [&](int raw) {
+      if (w == 0 && lane < 8 && raw >= 0 && raw < P.n_pages) {
+        ks = __ldg(P.k_scale + (long long)raw * P.h_kv + x.head);
+        vs = __ldg(P.v_scale + (long long)raw * P.h_kv + x.head);
       }
     };
-    find_pages(0);
-    load(P.k_pool, kr, 0, false);
-    load(P.v_pool, vr, 0, true);
-    load_scales(0);
+    int raw = entry(0);
+    uint32_t rows = rows_of(raw, 0);   // of the block whose codes are in the registers
+    load(P.k_pool, kr, rows, 0, false);
+    load(P.v_pool, vr, rows, 0, true);
+    load_scales(raw);
+    raw = entry(1);
     for (int i = 0; i < blocks; ++i, ++g) {
       const int buf = g & 1;
       const uint32_t free_parity = ((g >> 1) & 1) ^ 1;
-      find_pages(i + 1);
+      const int raw_next = entry(i + 2);
+      const uint32_t rows_next = rows_of(raw, i + 1);
       if (!wait_w(c, B_KFREE + buf, free_parity)) return;
       store(SM::K + buf * SM::OPERAND, kr);
-      if (tid < 8) {
-        float4* s = reinterpret_cast<float4*>(c.sm + SM::SCALES) + (g % N_SCALES) * 8 + tid;
-        *s = make_float4(ks * P.scale_log2, there ? log2f(vs) : -INFINITY, 1.0f / vs, 0.f);
-        if (!there) *s = make_float4(0.f, -INFINITY, 1.f, 0.f);
-      }
-      if (tid < 32) arrive_w(c, B_SCALES + g % N_SCALES);
       fence_async_smem();
       arrive_w(c, B_KFULL + buf);
-      load(P.k_pool, kr, i + 1, false);
-      load_scales(i + 1);
+      load(P.k_pool, kr, rows_next, i + 1, false);
+      if (w == 0) {
+        if (lane < 8) {
+          const float v = bounded_scale(vs);
+          reinterpret_cast<float4*>(c.sm + SM::SCALES)[(g % N_SCALES) * 8 + lane] =
+              rows != NONE ? make_float4(ks * P.scale_log2, log2f(v), 1.0f / v, 0.f) : make_float4(0.f, -INFINITY, 1.f, 0.f);
+        }
+        arrive_w(c, B_SCALES + g % N_SCALES);
+        load_scales(raw);
+      }
       if (!wait_w(c, B_VFREE + buf, free_parity)) return;
       store(SM::V + buf * SM::OPERAND, vr);
       fence_async_smem();
       arrive_w(c, B_VFULL + buf);
-      load(P.v_pool, vr, i + 1, true);
+      load(P.v_pool, vr, rows_next, i + 1, true);
+      raw = raw_next;
+      rows = rows_next;
     }
   }
 }
 
 // ------------------------------------------------------------------------------ products
+// The whole warp runs this role and one elected lane issues each product: with
+// warp-uniform control flow the descriptors stay in uniform registers.
 template <int D>
 DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles) {
   using SM = TileSmem<D>;
@@ -236,7 +253,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
   for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     for (int i = 0; i <= blocks; ++i) {
-      const int kb = (g + i) & 1, vb = (g + i - 1) & 1;
+      const int kb = (g + i) & 1, vb = kb ^ 1;
       if (i < blocks && !wait_w(c, B_KFULL + kb, ((g + i) >> 1) & 1)) return;
       if (i > 0 && !wait_w(c, B_VFULL + vb, ((g + i - 1) >> 1) & 1)) return;
 #pragma unroll
@@ -279,6 +296,29 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
 }
 
 // ------------------------------------------------------------------------------ softmax
+DSA_DEV uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+// two fp32 operations in one instruction
+DSA_DEV void fma2(uint32_t& x0, uint32_t& x1, uint64_t mul, uint64_t add) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x0), "r"(x1));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(mul), "l"(add));
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x0), "=r"(x1) : "l"(v));
+}
+DSA_DEV void add2(float& s0, float& s1, float a, float b) {
+  uint64_t v = pair(s0, s1);
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(pair(a, b)));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(v));
+}
+DSA_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int D>
 DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, int h) {
   using SM = TileSmem<D>;
@@ -341,33 +381,41 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       tc_fence_after();
       const float4* sc = reinterpret_cast<const float4*>(c.sm + SM::SCALES) + (gi % N_SCALES) * 8;
       const int base = x.t.lo + i * BLOCK;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t a[32], b[32];
-        tmem_ld32(ts + 64 * s, a);
-        tmem_ld32(ts + 64 * s + 32, b);
-        tc_wait_ld();
-        float x2[64];
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {   // 64 tokens at a time: two copies of this code cost more than they gain
+        uint32_t x2[64];
+        tmem_ld32(ts + 64 * s, *reinterpret_cast<uint32_t(*)[32]>(x2));
+        tmem_ld32(ts + 64 * s + 32, *reinterpret_cast<uint32_t(*)[32]>(x2 + 32));
+        float2 mul_add[4];
         float vinv[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 f = sc[4 * s + q];
-          const float mul = f.x * row_scale, add = f.y - m;
+          mul_add[q] = make_float2(f.x * row_scale, f.y - m);
           vinv[q] = f.z;
+        }
+        tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            x2[16 * q + e] = fmaf(__uint_as_float(q < 2 ? a[16 * (q & 1) + e] : b[16 * (q & 1) + e]), mul, add);
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t mul = pair(mul_add[q].x, mul_add[q].x), add = pair(mul_add[q].y, mul_add[q].y);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) fma2(x2[16 * q + e], x2[16 * q + e + 1], mul, add);
         }
         const int j0 = base + 64 * s;
         if (j0 + 63 > pos_min || (P.window > 0 && j0 <= pos_max - P.window)) {
           const int last = pos - j0, before = P.window > 0 ? last - P.window : -1;
 #pragma unroll
           for (int e = 0; e < 64; ++e)
-            if (e > last || e <= before) x2[e] = -INFINITY;
+            if (e > last || e <= before) x2[e] = 0xFF800000u;   // -inf
         }
-        float top = x2[0];
+        float t4[4];
 #pragma unroll
-        for (int e = 1; e < 64; ++e) top = fmaxf(top, x2[e]);
+        for (int q = 0; q < 4; ++q) {
+          t4[q] = fmaxf(__uint_as_float(x2[q]), __uint_as_float(x2[q + 4]));
+#pragma unroll
+          for (int e = 8; e < 64; e += 8) t4[q] = max3(t4[q], __uint_as_float(x2[e + q]), __uint_as_float(x2[e + 4 + q]));
+        }
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         const bool up = top > (fresh ? -INFINITY : LAG);
         if (__any_sync(0xFFFFFFFFu, up)) {
           const float to_m = up ? floorf(m + top) : m;   // the largest weight is in [1, 2)
@@ -376,7 +424,7 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
           m = to_m;
           l *= f;
 #pragma unroll
-          for (int e = 0; e < 64; ++e) x2[e] -= delta;
+          for (int e = 0; e < 64; ++e) x2[e] = __float_as_uint(__uint_as_float(x2[e]) - delta);
           if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
             if (i > 0) {
               // the product of the block before is done: these scores were issued after it
@@ -410,14 +458,14 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
         uint32_t p[32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float sum = 0.f;
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float w0 = ex2(x2[16 * q + 2 * e]), w1 = ex2(x2[16 * q + 2 * e + 1]);
-            sum += w0 + w1;
+            const float w0 = ex2(__uint_as_float(x2[16 * q + 2 * e])), w1 = ex2(__uint_as_float(x2[16 * q + 2 * e + 1]));
+            add2(s0, s1, w0, w1);
             p[8 * q + e] = pack_f16x2(w0, w1);
           }
-          l = fmaf(sum, vinv[q], l);
+          l = fmaf(s0 + s1, vinv[q], l);
         }
         tmem_st32(ts + 32 * s, p);
       }
