@@ -7,9 +7,10 @@
 //     of 128 cached tokens reads its scores from tensor memory, forms the weights and
 //     writes them back as fp16 over the scores; in the end it divides its row of O by the
 //     softmax's sum and stores it.
-//   - warps 8-11: the block's codes from the pages into fp16 tiles in shared memory (K and
-//     V, two buffers each), loaded one block ahead into registers.  A token's row is 128
-//     bytes wide in the 128-byte swizzle, in panels of 64 dims, which serves K as a
+//   - warp 13 copies the codes of each block from the pages into shared memory (bulk copies
+//     of 16 tokens, which lie in one page), and the pages' scales;
+//   - warps 8-11 turn them into fp16 tiles (K and V, two buffers each).  A token's row is
+//     128 bytes wide in the 128-byte swizzle, in panels of 64 dims, which serves K as a
 //     K-major and V as an MN-major operand.
 //   - warp 12 issues the products: S = Q K^T (128 x 128 x D) and O += P V (128 x D x 128,
 //     P in tensor memory).  The two halves alternate, so that one half's softmax runs
@@ -29,19 +30,26 @@ namespace dsa_kv8 {
 using namespace dsa;
 
 constexpr int BLOCK = 128;       // cached tokens of a block
-constexpr int W_DQ = 8, W_MMA = 12, TILE_THREADS = 13 * 32;
+constexpr int W_DQ = 8, W_MMA = 12, W_COPY = 13, TILE_THREADS = 14 * 32;
 constexpr unsigned long long WAIT_LIMIT_CYCLES = 4000000000ull;   // ~2 s at 2 GHz
 
 // barriers
-enum { B_KFULL = 0, B_KFREE = 2, B_VFULL = 4, B_VFREE = 6, B_SFULL = 8, B_PFULL = 10, B_QFULL = 12, B_OFULL = 14, B_SCALES = 16, B_DRAIN = 20, N_BAR };
-constexpr int N_SCALES = 4;      // blocks whose scales are kept: see dequant()
+enum {
+  B_KFULL = 0, B_KFREE = 2, B_VFULL = 4, B_VFREE = 6,   // fp16 tiles, by buffer
+  B_SFULL = 8, B_PFULL = 10, B_QFULL = 12, B_OFULL = 14,   // scores, weights, queries, result, by half
+  B_RAWFULL = 16, B_RAWFREE = 18,   // codes of keys (0) and values (1)
+  B_SCALES = 20, B_DRAIN = 24, N_BAR
+};
+constexpr int N_SCALES = 4;      // blocks whose scales are kept: see copies()
 
 template <int D>
 struct TileSmem {
   static constexpr int OPERAND = BLOCK * D * 2;   // a K, V or half-Q tile in fp16
   static constexpr int PANEL = BLOCK * 128;       // 64 dims of it
-  static constexpr int Q = 0, K = 2 * OPERAND, V = 4 * OPERAND, SCALES = 6 * OPERAND;
-  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * N_BAR + 8, BYTES = MISC + 16;
+  static constexpr int RAWTILE = BLOCK * D;       // codes of a K or V block
+  static constexpr int Q = 0, K = 2 * OPERAND, V = 4 * OPERAND, RAW = 6 * OPERAND, SCALES = RAW + 2 * RAWTILE;
+  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * ((N_BAR + 1) & ~1), BYTES = MISC + 16;
+  static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 template <int D>
 struct Tmem {   // columns
@@ -51,7 +59,7 @@ struct Tmem {   // columns
 struct Ctx {
   uint8_t* sm;
   uint32_t sb, bars;
-  volatile int* misc;   // [0]: tensor memory address, [1]: abort
+  volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2], [3]: groups of the K and V codes that have a page
   uint32_t* status;
 };
 
@@ -116,14 +124,94 @@ DSA_DEV bool unit(const Params& P, long long u, int n_tiles, Unit& x) {
 }
 
 // ------------------------------------------------------------------------------ codes
-// Block i of the CTA (over all units) uses buffer i % 2 of K and V.  Its scales are in
-// slot i % 4: K's buffer is written two blocks ahead of the softmax, which reads the
-// scales of the block it is at.  When the buffer of block i is free (the products of
-// block i - 2 are done, for which the weights of block i - 3 were needed), the softmax has
-// left block i - 3: slots i - 2, i - 1 and i are in use.  (The scales have barriers of
-// their own: K's could complete a phase more before the softmax looks at it.)
-// A warp stops at the first use of a value that it is still loading, so a block's table
-// entries are loaded two blocks ahead, its scales and codes one block ahead.
+// Lane l looks after group l of a block's eight groups of 16 tokens, each of which lies in
+// one page.  A warp stops at the first use of a value that it is still loading, so a
+// block's table entries are loaded two blocks ahead and its scales one block ahead.
+//
+// The scales of block g (counted over all units) are in slot g % 4.  They are written when
+// the codes' buffer is free of block g - 1, so its K tile was written, so the products of
+// block g - 3 were issued, and those needed the weights of block g - 4: the softmax has
+// left the slot.
+template <int D>
+DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
+  using SM = TileSmem<D>;
+  constexpr uint32_t GROUP_BYTES = 16 * D;
+  const int lane = threadIdx.x & 31, grp = lane & 7;
+  const int page_mask = (1 << P.page_shift) - 1;
+  uint32_t g = 0;
+  bool ok = true;
+  Unit x;
+  for (long long u = blockIdx.x; ok && unit(P, u, n_tiles, x); u += gridDim.x) {
+    const int blocks = max(x.blocks[0], x.blocks[1]);
+    const int32_t* table = P.table + x.t.req * P.table_ld;
+    auto entry = [&](int i) -> int {
+      const int j = x.t.lo + i * BLOCK + 16 * grp;
+      return (i < blocks && j < x.t.hi) ? __ldg(table + (j >> P.page_shift)) : -1;
+    };
+    float ks = 1.f, vs = 1.f;
+    auto load_scales = [&](int raw) {
+      if (lane < 8 && raw >= 0 && raw < P.n_pages) {
+        ks = __ldg(P.k_scale + (long long)raw * P.h_kv + x.head);
+        vs = __ldg(P.v_scale + (long long)raw * P.h_kv + x.head);
+      }
+    };
+    int raw = entry(0), raw_next = entry(1);
+    load_scales(raw);
+    for (int i = 0; i < blocks; ++i, ++g) {
+      const int raw_after = entry(i + 2);
+      const bool there = raw >= 0 && raw < P.n_pages;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there && lane < 8);
+      // first row of the group in the pools
+      const uint32_t row = (((uint32_t)raw * P.h_kv + x.head) << P.page_shift) +
+                           ((x.t.lo + i * BLOCK + 16 * grp) & page_mask);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!(ok = wait_w(c, B_RAWFREE + kv, (g & 1) ^ 1))) break;
+        if (kv == 0) {
+          if (lane < 8) {
+            const float v = bounded_scale(vs);
+            reinterpret_cast<float4*>(c.sm + SM::SCALES)[(g % N_SCALES) * 8 + lane] =
+                there ? make_float4(ks * P.scale_log2, log2f(v), 1.0f / v, 0.f) : make_float4(0.f, -INFINITY, 1.f, 0.f);
+          }
+          arrive_w(c, B_SCALES + g % N_SCALES);
+          load_scales(raw_next);
+        }
+        const uint32_t full = bar(c, B_RAWFULL + kv);
+        if (lane == 0) {
+          c.misc[2 + kv] = (int)mask;
+          asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                       "r"((uint32_t)__popc(mask) * GROUP_BYTES)
+                       : "memory");
+        }
+        __syncwarp();
+        if (there && lane < 8) {
+          const uint8_t* src = (kv == 0 ? P.k_pool : P.v_pool) + (uint64_t)row * D;
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           c.sb + SM::RAW + kv * SM::RAWTILE + grp * GROUP_BYTES),
+                       "l"(src), "r"(GROUP_BYTES), "r"(full)
+                       : "memory");
+        }
+      }
+      if (!ok) break;
+      raw = raw_next;
+      raw_next = raw_after;
+    }
+  }
+  if (!ok) {
+    // gave up: wait, with a limit, for the copies in flight.  Block g's keys were issued if
+    // the values' wait ran out; both buffers' last copies belong to block g or g - 1.
+    const unsigned long long start = clock64();
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      for (uint32_t b = g > 0 ? g - 1 : 0; b <= g; ++b)
+        while (!mbar_wait_susp(bar(c, B_RAWFULL + kv), b & 1) && clock64() - start < WAIT_LIMIT_CYCLES / 4) {
+        }
+  }
+}
+
+// Block g uses buffer g % 2 of K and V.  A lane turns 16 codes into two 16-byte units of a
+// swizzled row.  A quarter warp holds four chunks of an even row and the other four of the
+// odd row behind it, which meet in no bank, neither here nor there.
 template <int D>
 DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   using SM = TileSmem<D>;
@@ -131,105 +219,52 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   constexpr int ROWS = 128 / CHUNKS;        // rows of one pass of the four warps: 16 or 32
   constexpr int PASSES = BLOCK / ROWS;      // 8, or 4 for D = 64
   const int w = (threadIdx.x >> 5) - W_DQ, lane = threadIdx.x & 31;
-  // A chunk of codes becomes two 16-byte units of a swizzled row; a quarter warp holds
-  // four chunks of one panel in an even and the odd row behind it, whose units never meet
-  // in a bank.
-  const int chunk = (lane & 3) + (D == 128 ? (lane >> 4) * 4 : 0);
   const int sub = w * (ROWS / 4) + (D == 128 ? (lane >> 2) & 3 : lane >> 2);   // row of a pass
-  const int page_mask = (1 << P.page_shift) - 1;
+  const int chunk = (lane & 3) + (D == 128 ? ((lane >> 4) ^ (sub & 1)) * 4 : 0);
+  const uint32_t load_at = c.sb + SM::RAW + sub * D + 16 * chunk;
   const uint32_t store_at = c.sb + (chunk >> 2) * SM::PANEL + sub * 128;
   const uint32_t s0 = ((2 * (chunk & 3)) ^ (sub & 7)) << 4, s1 = ((2 * (chunk & 3) + 1) ^ (sub & 7)) << 4;
   uint32_t g = 0;
   Unit x;
   for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
-    const int32_t* table = P.table + x.t.req * P.table_ld;
     const int p_first = x.t.pos0 + x.t.row0 / P.group;
     const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
-    // lane l of every warp looks after group l of the block's eight groups of 16 tokens,
-    // each of which lies in one page
-    auto entry = [&](int i) -> int {
-      const int j = x.t.lo + i * BLOCK + 16 * (lane & 7);
-      return (i < blocks && j < x.t.hi) ? __ldg(table + (j >> P.page_shift)) : -1;
-    };
-    // first row of the group in the pools, NONE where there is no page
-    constexpr uint32_t NONE = 0xFFFFFFFFu;
-    auto rows_of = [&](int raw, int i) -> uint32_t {
-      const int j = x.t.lo + i * BLOCK + 16 * (lane & 7);
-      if (raw < 0 || raw >= P.n_pages) return NONE;
-      return (((uint32_t)raw * P.h_kv + x.head) << P.page_shift) + (j & page_mask);
-    };
-    uint4 kr[PASSES], vr[PASSES];
-    auto load = [&](const uint8_t* pool, uint4 (&r)[PASSES], uint32_t rows, int i, bool values) {
-      const bool all = __all_sync(0xFFFFFFFFu, rows != NONE);
-      const int j0 = x.t.lo + i * BLOCK;
-      const uint8_t* at = pool + 16 * chunk;
-      if (all && (!values || (j0 >= seen_lo && j0 + BLOCK <= x.t.hi))) {
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-          const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows, (p * ROWS + sub) >> 4) + (sub & 15);
-          r[p] = ldg_nc(at + (uint64_t)row * D);
-        }
-      } else {
-        // values outside what any row sees may be NaN codes, and 0 * NaN is not 0
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-          const uint32_t row = __shfl_sync(0xFFFFFFFFu, rows, (p * ROWS + sub) >> 4);
-          const int j = j0 + p * ROWS + sub;
-          r[p] = make_uint4(0u, 0u, 0u, 0u);
-          if (row != NONE && (!values || (j >= seen_lo && j < x.t.hi))) r[p] = ldg_nc(at + (uint64_t)(row + (sub & 15)) * D);
-        }
-      }
-    };
-    auto store = [&](int at, const uint4 (&r)[PASSES]) {
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        uint32_t h[8];
-        codes16_to_f16(r[p], h);
-        const uint32_t base = store_at + at + p * ROWS * 128;
-        sts128(base + s0, make_uint4(h[0], h[1], h[2], h[3]));
-        sts128(base + s1, make_uint4(h[4], h[5], h[6], h[7]));
-      }
-    };
-    float ks = 1.f, vs = 1.f;
-    auto load_scales = [&](int raw) {
-      if (w == 0 && lane < 8 && raw >= 0 && raw < P.n_pages) {
-        ks = __ldg(P.k_scale + (long long)raw * P.h_kv + x.head);
-        vs = __ldg(P.v_scale + (long long)raw * P.h_kv + x.head);
-      }
-    };
-    int raw = entry(0);
-    uint32_t rows = rows_of(raw, 0);   // of the block whose codes are in the registers
-    load(P.k_pool, kr, rows, 0, false);
-    load(P.v_pool, vr, rows, 0, true);
-    load_scales(raw);
-    raw = entry(1);
     for (int i = 0; i < blocks; ++i, ++g) {
-      const int buf = g & 1;
-      const uint32_t free_parity = ((g >> 1) & 1) ^ 1;
-      const int raw_next = entry(i + 2);
-      const uint32_t rows_next = rows_of(raw, i + 1);
-      if (!wait_w(c, B_KFREE + buf, free_parity)) return;
-      store(SM::K + buf * SM::OPERAND, kr);
-      fence_async_smem();
-      arrive_w(c, B_KFULL + buf);
-      load(P.k_pool, kr, rows_next, i + 1, false);
-      if (w == 0) {
-        if (lane < 8) {
-          const float v = bounded_scale(vs);
-          reinterpret_cast<float4*>(c.sm + SM::SCALES)[(g % N_SCALES) * 8 + lane] =
-              rows != NONE ? make_float4(ks * P.scale_log2, log2f(v), 1.0f / v, 0.f) : make_float4(0.f, -INFINITY, 1.f, 0.f);
+      const int buf = g & 1, j0 = x.t.lo + i * BLOCK;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!wait_w(c, B_RAWFULL + kv, g & 1)) return;
+        const uint32_t mask = (uint32_t)c.misc[2 + kv];
+        uint4 r[PASSES];
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(r[p].x), "=r"(r[p].y), "=r"(r[p].z), "=r"(r[p].w)
+                       : "r"(load_at + kv * SM::RAWTILE + p * ROWS * D)
+                       : "memory");
+        if (mask != 0xFFu || (kv == 1 && (j0 < seen_lo || j0 + BLOCK > x.t.hi))) {
+          // no page, or values outside what any row sees: they may be NaN codes, and
+          // 0 * NaN is not 0
+#pragma unroll
+          for (int p = 0; p < PASSES; ++p) {
+            const int row = p * ROWS + sub, j = j0 + row;
+            if (!((mask >> (row >> 4)) & 1u) || (kv == 1 && (j < seen_lo || j >= x.t.hi))) r[p] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
-        arrive_w(c, B_SCALES + g % N_SCALES);
-        load_scales(raw);
+        if (!wait_w(c, (kv ? B_VFREE : B_KFREE) + buf, ((g >> 1) & 1) ^ 1)) return;
+        const uint32_t to = store_at + (kv ? SM::V : SM::K) + buf * SM::OPERAND;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          uint32_t h[8];
+          codes16_to_f16(r[p], h);
+          sts128(to + p * ROWS * 128 + s0, make_uint4(h[0], h[1], h[2], h[3]));
+          sts128(to + p * ROWS * 128 + s1, make_uint4(h[4], h[5], h[6], h[7]));
+        }
+        fence_async_smem();
+        arrive_w(c, (kv ? B_VFULL : B_KFULL) + buf);
+        if (lane == 0) mbar_arrive(bar(c, B_RAWFREE + kv));
       }
-      if (!wait_w(c, B_VFREE + buf, free_parity)) return;
-      store(SM::V + buf * SM::OPERAND, vr);
-      fence_async_smem();
-      arrive_w(c, B_VFULL + buf);
-      load(P.v_pool, vr, rows_next, i + 1, true);
-      raw = raw_next;
-      rows = rows_next;
     }
   }
 }
@@ -523,6 +558,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
       mbar_init(bar(c, B_PFULL + i), 4);
       mbar_init(bar(c, B_QFULL + i), 4);
       mbar_init(bar(c, B_OFULL + i), 1);
+      mbar_init(bar(c, B_RAWFULL + i), 1);
+      mbar_init(bar(c, B_RAWFREE + i), 4);
     }
     for (int i = 0; i < N_SCALES; ++i) mbar_init(bar(c, B_SCALES + i), 1);
     mbar_init(bar(c, B_DRAIN), 1);
@@ -537,7 +574,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   const int n_tiles = P.header->n_tiles;
   if (warp < W_DQ) softmax<D>(P, c, tmem, n_tiles, warp >> 2);
   else if (warp < W_MMA) dequant<D>(P, c, n_tiles);
-  else products<D>(P, c, tmem, n_tiles);
+  else if (warp == W_MMA) products<D>(P, c, tmem, n_tiles);
+  else if (warp == W_COPY) copies<D>(P, c, n_tiles);
   tc_fence_before();
   __syncthreads();
   if (warp == W_MMA && (threadIdx.x & 31) == 0) {
