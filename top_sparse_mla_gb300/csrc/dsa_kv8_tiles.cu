@@ -19,9 +19,10 @@
 // and the CTA's roles stop, drain the tensor core and free its memory.
 //
 // Scores become u = S * (k_scale * softmax_scale * log2 e * row scaling) + (log2 v_scale - m)
-// with m an integer that may lag behind the row's maximum by 2^LAG: O is rescaled only
-// when a score passes it by more (by a power of two, exactly), which is rare after the
-// first block.
+// and weights 2^u, with m an integer that was the row's maximum, rounded down, when it was
+// last set.  Maxima are not looked for again while the weights of 64 tokens add up to less
+// than 2^15, so that each fits fp16; when they do not, m is set anew and O rescaled by a
+// power of two, exactly.  That is rare behind the first block.
 
 #include "dsa_kv8.cuh"
 
@@ -30,7 +31,12 @@ namespace dsa_kv8 {
 using namespace dsa;
 
 constexpr int BLOCK = 128;       // cached tokens of a block
-constexpr int W_DQ = 8, W_MMA = 12, W_COPY = 13, TILE_THREADS = 14 * 32;
+constexpr float MOST = 32768.0f;   // largest sum of 64 weights by an m that is kept
+constexpr int W_DQ = 8, W_MMA = 12, W_COPY = 13, TILE_THREADS = 16 * 32;   // warps 14 and 15 only give registers
+// Registers of a thread of the softmax groups and of the others: eight warps of each, which
+// is what 16 warps of 128 were launched with.
+constexpr int LAUNCH_REGS = 128, SOFTMAX_REGS = 152, OTHER_REGS = 104;
+static_assert(SOFTMAX_REGS + OTHER_REGS == 2 * LAUNCH_REGS, "more registers than the CTA has would be waited for");
 constexpr unsigned long long WAIT_LIMIT_CYCLES = 4000000000ull;   // ~2 s at 2 GHz
 
 // barriers
@@ -38,7 +44,7 @@ enum {
   B_KFULL = 0, B_KFREE = 2, B_VFULL = 4, B_VFREE = 6,   // fp16 tiles, by buffer
   B_SFULL = 8, B_PFULL = 10, B_QFULL = 12, B_OFULL = 14,   // scores, weights, queries, result, by half
   B_RAWFULL = 16, B_RAWFREE = 18,   // codes of keys (0) and values (1)
-  B_SCALES = 20, B_DRAIN = 24, N_BAR
+  B_SCALES = 20, B_DRAIN = 24, N_BAR = 26
 };
 constexpr int N_SCALES = 4;      // blocks whose scales are kept: see copies()
 
@@ -48,7 +54,7 @@ struct TileSmem {
   static constexpr int PANEL = BLOCK * 128;       // 64 dims of it
   static constexpr int RAWTILE = BLOCK * D;       // codes of a K or V block
   static constexpr int Q = 0, K = 2 * OPERAND, V = 4 * OPERAND, RAW = 6 * OPERAND, SCALES = RAW + 2 * RAWTILE;
-  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * ((N_BAR + 1) & ~1), BYTES = MISC + 16;
+  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * N_BAR, BYTES = MISC + 16;
   static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 template <int D>
@@ -68,9 +74,10 @@ DSA_DEV void arrive_w(const Ctx& c, int b) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar(c, b));
 }
-// The waiting part of a bounded wait, out of line.  False when the limit passes or when
-// another thread of the CTA has given up.
-__device__ __noinline__ bool wait_slow(uint32_t addr, uint32_t parity, volatile int* misc, uint32_t* status) {
+// The waiting part of a bounded wait (in line: register counts that differ by role leave
+// no room for a call).  False when the limit passes or when another thread of the CTA has
+// given up.
+DSA_DEV bool wait_slow(uint32_t addr, uint32_t parity, volatile int* misc, uint32_t* status) {
   const unsigned long long start = clock64();
   while (true) {
     if (mbar_wait_susp(addr, parity)) return true;
@@ -105,7 +112,12 @@ struct Unit {
   int head;
   int blocks[2];   // blocks of each half; 0 for a half without rows
 };
-DSA_DEV bool unit(const Params& P, long long u, int n_tiles, Unit& x) {
+// The units are in the order of the tiles, longest first as far as one request goes; the
+// CTAs take them forwards and backwards in turn, so that no CTA has the longer one of every
+// round (forwards only, the first CTA of a 2123-token prefill had 40 blocks where the mean
+// is 31).
+DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
+  const long long u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   if (u >= (long long)n_tiles * P.h_kv) return false;
   const int i = (int)(u / P.h_kv);
   x.head = (int)(u - (long long)i * P.h_kv);
@@ -129,9 +141,8 @@ DSA_DEV bool unit(const Params& P, long long u, int n_tiles, Unit& x) {
 // block's table entries are loaded two blocks ahead and its scales one block ahead.
 //
 // The scales of block g (counted over all units) are in slot g % 4.  They are written when
-// the codes' buffer is free of block g - 1, so its K tile was written, so the products of
-// block g - 3 were issued, and those needed the weights of block g - 4: the softmax has
-// left the slot.
+// the codes of block g - 1 have left their buffer, so the V tile of block g - 2 was written,
+// so the products of block g - 4 are done: the softmax has left the slot.
 template <int D>
 DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   using SM = TileSmem<D>;
@@ -141,7 +152,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   uint32_t g = 0;
   bool ok = true;
   Unit x;
-  for (long long u = blockIdx.x; ok && unit(P, u, n_tiles, x); u += gridDim.x) {
+  for (long long u = 0; ok && unit(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int32_t* table = P.table + x.t.req * P.table_ld;
     auto entry = [&](int i) -> int {
@@ -226,7 +237,7 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   const uint32_t s0 = ((2 * (chunk & 3)) ^ (sub & 7)) << 4, s1 = ((2 * (chunk & 3) + 1) ^ (sub & 7)) << 4;
   uint32_t g = 0;
   Unit x;
-  for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
+  for (long long u = 0; unit(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int p_first = x.t.pos0 + x.t.row0 / P.group;
     const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
@@ -252,6 +263,7 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
             if (!((mask >> (row >> 4)) & 1u) || (kv == 1 && (j < seen_lo || j >= x.t.hi))) r[p] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
+        arrive_w(c, B_RAWFREE + kv);   // the codes are in registers
         if (!wait_w(c, (kv ? B_VFREE : B_KFREE) + buf, ((g >> 1) & 1) ^ 1)) return;
         const uint32_t to = store_at + (kv ? SM::V : SM::K) + buf * SM::OPERAND;
 #pragma unroll
@@ -263,7 +275,6 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
         }
         fence_async_smem();
         arrive_w(c, (kv ? B_VFULL : B_KFULL) + buf);
-        if (lane == 0) mbar_arrive(bar(c, B_RAWFREE + kv));
       }
     }
   }
@@ -285,7 +296,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
   uint32_t np[2] = {0, 0};        // blocks of each half
   uint32_t nq[2] = {0, 0};        // units of each half
   Unit x;
-  for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
+  for (long long u = 0; unit(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     for (int i = 0; i <= blocks; ++i) {
       const int kb = (g + i) & 1, vb = kb ^ 1;
@@ -297,13 +308,13 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
           if (!wait_w(c, B_PFULL + h, np[h] & 1)) return;
           ++np[h];
           tc_fence_after();
+          if (elect_one())
 #pragma unroll
           for (int k = 0; k < BLOCK / 16; ++k) {
-            if (elect_one())
               mma_ts(tmem + TM::O + D * h, tmem + TM::S + 128 * h + 8 * k,
                      d_v + ((uint32_t)(vb * SM::OPERAND + k * 2048) >> 4), ID_PV, (i > 1 || k > 0) ? 1u : 0u);
-            __syncwarp();
           }
+          __syncwarp();
           if (i == x.blocks[h]) commit(bar(c, B_OFULL + h));
         }
         if (i < x.blocks[h]) {
@@ -312,14 +323,14 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
             ++nq[h];
           }
           tc_fence_after();
+          if (elect_one())
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = (k >> 2) * SM::PANEL + (k & 3) * 32;
-            if (elect_one())
               mma_ss(tmem + TM::S + 128 * h, d_q + ((h * SM::OPERAND + off) >> 4), d_k + ((kb * SM::OPERAND + off) >> 4),
                      ID_QK, k ? 1u : 0u);
-            __syncwarp();
           }
+          __syncwarp();
           commit(bar(c, B_SFULL + h));
         }
       }
@@ -363,7 +374,7 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
   const uint32_t ts = tmem + lanes + TM::S + 128 * h, to = tmem + lanes + TM::O + D * h;
   uint32_t g = 0, ns = 0, no = 0;
   Unit x;
-  for (long long u = blockIdx.x; unit(P, u, n_tiles, x); u += gridDim.x) {
+  for (long long u = 0; unit(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
     if (mine == 0) {
       g += blocks;
@@ -418,90 +429,103 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       const int base = x.t.lo + i * BLOCK;
 #pragma unroll 1
       for (int s = 0; s < 2; ++s) {   // 64 tokens at a time: two copies of this code cost more than they gain
-        uint32_t x2[64];
-        tmem_ld32(ts + 64 * s, *reinterpret_cast<uint32_t(*)[32]>(x2));
-        tmem_ld32(ts + 64 * s + 32, *reinterpret_cast<uint32_t(*)[32]>(x2 + 32));
-        float2 mul_add[4];
-        float vinv[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 f = sc[4 * s + q];
-          mul_add[q] = make_float2(f.x * row_scale, f.y - m);
-          vinv[q] = f.z;
-        }
-        tc_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint64_t mul = pair(mul_add[q].x, mul_add[q].x), add = pair(mul_add[q].y, mul_add[q].y);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) fma2(x2[16 * q + e], x2[16 * q + e + 1], mul, add);
-        }
-        const int j0 = base + 64 * s;
-        if (j0 + 63 > pos_min || (P.window > 0 && j0 <= pos_max - P.window)) {
-          const int last = pos - j0, before = P.window > 0 ? last - P.window : -1;
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e > last || e <= before) x2[e] = 0xFF800000u;   // -inf
-        }
-        float t4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          t4[q] = fmaxf(__uint_as_float(x2[q]), __uint_as_float(x2[q + 4]));
-#pragma unroll
-          for (int e = 8; e < 64; e += 8) t4[q] = max3(t4[q], __uint_as_float(x2[e + q]), __uint_as_float(x2[e + 4 + q]));
-        }
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        const bool up = top > (fresh ? -INFINITY : LAG);
-        if (__any_sync(0xFFFFFFFFu, up)) {
-          const float to_m = up ? floorf(m + top) : m;   // the largest weight is in [1, 2)
-          const float delta = to_m - m, f = (up && !fresh) ? ex2(-delta) : 1.0f;
-          if (up) fresh = false;
-          m = to_m;
-          l *= f;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x2[e] = __float_as_uint(__uint_as_float(x2[e]) - delta);
-          if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
-            if (i > 0) {
-              // the product of the block before is done: these scores were issued after it
-#pragma unroll 1
-              for (int k = 0; k < D; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(to + k, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(to + k, o);
-              }
-            }
-            if (s == 1) {   // the weights of the block's first half
-              const __half2 f2 = __float2half2_rn(f);
-#pragma unroll 1
-              for (int k = 0; k < 32; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(ts + k, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f2);
-                  o[e] = *reinterpret_cast<const uint32_t*>(&p);
-                }
-                tmem_st16(ts + k, o);
-              }
-            }
-          }
-        }
         uint32_t p[32];
+        float part;   // this part's sum of w / v_scale
+        // Weights by the row's m as it is.  Where a row has no m yet, or where its weights
+        // turn out too large for fp16, once more after m was moved: the scores are still
+        // in tensor memory.
+        bool move = __any_sync(0xFFFFFFFFu, fresh);
+        while (true) {
+          uint32_t x2[64];
+          tmem_ld32(ts + 64 * s, *reinterpret_cast<uint32_t(*)[32]>(x2));
+          tmem_ld32(ts + 64 * s + 32, *reinterpret_cast<uint32_t(*)[32]>(x2 + 32));
+          float2 mul_add[4];
+          float vinv[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float w0 = ex2(__uint_as_float(x2[16 * q + 2 * e])), w1 = ex2(__uint_as_float(x2[16 * q + 2 * e + 1]));
-            add2(s0, s1, w0, w1);
-            p[8 * q + e] = pack_f16x2(w0, w1);
+          for (int q = 0; q < 4; ++q) {
+            const float4 f = sc[4 * s + q];
+            mul_add[q] = make_float2(f.x * row_scale, f.y - m);
+            vinv[q] = f.z;
           }
-          l = fmaf(s0 + s1, vinv[q], l);
+          tc_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t mul = pair(mul_add[q].x, mul_add[q].x), add = pair(mul_add[q].y, mul_add[q].y);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) fma2(x2[16 * q + e], x2[16 * q + e + 1], mul, add);
+          }
+          const int j0 = base + 64 * s;
+          if (j0 + 63 > pos_min || (P.window > 0 && j0 <= pos_max - P.window)) {
+            const int last = pos - j0, before = P.window > 0 ? last - P.window : -1;
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (e > last || e <= before) x2[e] = 0xFF800000u;   // -inf
+          }
+          if (move) {
+            float t4[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              t4[q] = fmaxf(__uint_as_float(x2[q]), __uint_as_float(x2[q + 4]));
+#pragma unroll
+              for (int e = 8; e < 64; e += 8) t4[q] = max3(t4[q], __uint_as_float(x2[e + q]), __uint_as_float(x2[e + 4 + q]));
+            }
+            const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            const bool up = top > (fresh ? -INFINITY : LAG);
+            const float to_m = up ? floorf(m + top) : m;   // the largest weight is in [1, 2)
+            const float delta = to_m - m, f = (up && !fresh) ? ex2(-delta) : 1.0f;
+            if (up) fresh = false;
+            m = to_m;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x2[e] = __float_as_uint(__uint_as_float(x2[e]) - delta);
+            if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+              if (i > 0) {
+                // the product of the block before is done: these scores were issued after it
+#pragma unroll 1
+                for (int k = 0; k < D; k += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(to + k, o);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(to + k, o);
+                }
+              }
+              if (s == 1) {   // the weights of the block's first part
+                const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+                for (int k = 0; k < 32; k += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(ts + k, o);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f2);
+                    o[e] = *reinterpret_cast<const uint32_t*>(&y);
+                  }
+                  tmem_st16(ts + k, o);
+                }
+              }
+            }
+          }
+          part = 0.f;
+          float all = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float w0 = ex2(__uint_as_float(x2[16 * q + 2 * e])), w1 = ex2(__uint_as_float(x2[16 * q + 2 * e + 1]));
+              add2(s0, s1, w0, w1);
+              p[8 * q + e] = pack_f16x2(w0, w1);
+            }
+            all += s0 + s1;
+            part = fmaf(s0 + s1, vinv[q], part);
+          }
+          if (move || !__any_sync(0xFFFFFFFFu, all > MOST)) break;
+          move = true;
         }
+        l += part;
         tmem_st32(ts + 32 * s, p);
       }
       tc_wait_st();
@@ -572,15 +596,20 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = (uint32_t)c.misc[0];
   const int n_tiles = P.header->n_tiles;
-  if (warp < W_DQ) softmax<D>(P, c, tmem, n_tiles, warp >> 2);
-  else if (warp < W_MMA) dequant<D>(P, c, n_tiles);
-  else if (warp == W_MMA) products<D>(P, c, tmem, n_tiles);
-  else if (warp == W_COPY) copies<D>(P, c, n_tiles);
+  if (warp < W_DQ) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    softmax<D>(P, c, tmem, n_tiles, warp >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    if (warp < W_MMA) dequant<D>(P, c, n_tiles);
+    else if (warp == W_MMA) products<D>(P, c, tmem, n_tiles);
+    else if (warp == W_COPY) copies<D>(P, c, n_tiles);
+  }
+  if (warp == W_MMA) commit(bar(c, B_DRAIN));
   tc_fence_before();
   __syncthreads();
   if (warp == W_MMA && (threadIdx.x & 31) == 0) {
     // every product has completed before tensor memory is released
-    tc_commit(bar(c, B_DRAIN));
     const unsigned long long start = clock64();
     while (!mbar_wait_susp(bar(c, B_DRAIN), 0) && clock64() - start < WAIT_LIMIT_CYCLES) {
     }
@@ -596,6 +625,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
 template <int D>
 static int launch_one(int grid, const Params& P, cudaStream_t st) {
   constexpr int smem = TileSmem<D>::BYTES;
+  // the kernel's groups trade the registers that its launch gave them
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, tiles_kernel<D>) != cudaSuccess || a.numRegs != LAUNCH_REGS) return DSA_ERR_CUDA;
   if (cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
   tiles_kernel<D><<<grid, TILE_THREADS, smem, st>>>(P);
