@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   extern __shared__ long long s_step[];   // [n_req + 1] exclusive prefix of the steps
   long long* s_tile = s_step + P.n_req + 1;   // [n_req + 1] of the tiles
   __shared__ long long s_step_warp[32], s_tile_warp[32];
+  __shared__ int s_place[PLAN_THREADS];
   __shared__ uint32_t s_bad;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = P.n_req;
@@ -117,24 +118,51 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   }
   // ascending cu_q cannot give more tiles than the list has room for
   const int n_tiles = (int)min(all_tiles, (long long)P.max_tiles);
-  for (int i = tid; i < n_tiles; i += PLAN_THREADS) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_tile[mid] <= i) lo = mid; else hi = mid;
+  if (n_tiles > 0) {
+    // the longest first (by cached tokens in blocks of 128, all above 1023 alike): a count
+    // of each length, the places behind the longer ones, then the tiles.  The order among
+    // equal ones changes no result.
+    auto tile = [&](int i) {
+      int lo = 0, hi = n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tile[mid] <= i) lo = mid; else hi = mid;
+      }
+      const Request a = request(P, lo);
+      const int row0 = (int)(i - s_tile[lo]) * TILE_ROWS, row1 = min(row0 + TILE_ROWS, a.rows(P)) - 1;
+      Tile t;
+      t.req = lo;
+      t.row0 = row0;
+      t.q0 = a.q0;
+      t.rows = a.rows(P);
+      t.pos0 = a.kv - a.q_len;
+      t.lo = span(P, a, row0 / P.group, row1 / P.group).lo;
+      t.hi = max(t.pos0 + row1 / P.group + 1, 0);
+      t.pad = 0;
+      return t;
+    };
+    auto length = [](const Tile& t) { return PLAN_THREADS - 1 - min(max(t.hi - t.lo, 0) / 128, PLAN_THREADS - 1); };
+    s_place[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += PLAN_THREADS) atomicAdd(&s_place[length(tile(i))], 1);
+    __syncthreads();
+    const int count = s_place[tid];
+    int before = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+      if (lane >= o) before += v;
     }
-    const Request a = request(P, lo);
-    const int row0 = (int)(i - s_tile[lo]) * TILE_ROWS, row1 = min(row0 + TILE_ROWS, a.rows(P)) - 1;
-    Tile t;
-    t.req = lo;
-    t.row0 = row0;
-    t.q0 = a.q0;
-    t.rows = a.rows(P);
-    t.pos0 = a.kv - a.q_len;
-    t.lo = span(P, a, row0 / P.group, row1 / P.group).lo;
-    t.hi = max(t.pos0 + row1 / P.group + 1, 0);
-    t.pad = 0;
-    P.tiles[n_tiles - 1 - i] = t;   // later tiles of a request see more tokens: they go first
+    if (lane == 31) s_step_warp[w] = before;
+    __syncthreads();
+    before -= count;
+    for (int v = 0; v < w; ++v) before += (int)s_step_warp[v];
+    s_place[tid] = before;
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += PLAN_THREADS) {
+      const Tile t = tile(i);
+      P.tiles[atomicAdd(&s_place[length(t)], 1)] = t;
+    }
   }
   if (tid == 0) {
     P.header->status = s_bad;

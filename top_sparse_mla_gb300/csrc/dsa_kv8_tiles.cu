@@ -112,8 +112,7 @@ struct Unit {
   int head;
   int blocks[2];   // blocks of each half; 0 for a half without rows
 };
-// The units are in the order of the tiles, longest first as far as one request goes; the
-// CTAs take them forwards and backwards in turn, so that no CTA has the longer one of every
+// The units are in the order of the tiles, longest first; the CTAs take them forwards and backwards in turn, so that no CTA has the longer one of every
 // round (forwards only, the first CTA of a 2123-token prefill had 40 blocks where the mean
 // is 31).
 DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
