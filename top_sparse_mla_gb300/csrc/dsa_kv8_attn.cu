@@ -19,9 +19,11 @@ namespace dsa_kv8 {
 
 constexpr int MAX_ROWS = 32;      // most query rows of a request in rows_kernel
 constexpr int ROW_WARPS = 4;      // warps of a rows_kernel CTA
-constexpr int CTAS_PER_SM = 4;    // the plan's CTAs per SM
 constexpr int MIN_STEPS = 8;      // a CTA's least share, in steps: two for each warp
 constexpr int PLAN_THREADS = 1024;
+// rows_kernel's CTAs per SM, by tiles of 8 query rows: what its registers leave room for.
+// Every CTA has to be resident at once, since the plan gives each an equal share.
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
 
 // ------------------------------------------------------------------------------ plan
@@ -598,7 +600,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
 }
 
 template <int D, int NT, int NW>
-__global__ void __launch_bounds__(32 * NW) rows_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) rows_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   RowSmem<D, NT, NW>& S = *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -665,7 +667,7 @@ static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 static Layout layout(const dsa_kv8_params* p, int sms) {
   Layout L;
   const size_t group = p->h_q / p->h_kv, rows = 8 * (size_t)row_tiles(p);
-  L.n_shares = CTAS_PER_SM * sms;
+  L.n_shares = ctas_per_sm(row_tiles(p)) * sms;
   size_t at = 256;
   L.shares = at;
   at += up(L.n_shares * sizeof(Share));
