@@ -59,12 +59,15 @@ struct Request {
   __device__ __forceinline__ int rows(const Params& P) const { return q_len * P.group; }
 };
 
-__device__ __forceinline__ Request request(const Params& P, int r) {
+__device__ __forceinline__ Request request(const Params& P, int from, int to, int kv_len) {
   Request a;
-  a.q0 = min(max(P.cu_q[r], 0), P.n_tokens);
-  a.q_len = min(max(P.cu_q[r + 1], a.q0), P.n_tokens) - a.q0;
-  a.kv = min(max(P.kv_lens[r], 0), P.cap);
+  a.q0 = min(max(from, 0), P.n_tokens);
+  a.q_len = min(max(to, a.q0), P.n_tokens) - a.q0;
+  a.kv = min(max(kv_len, 0), P.cap);
   return a;
+}
+__device__ __forceinline__ Request request(const Params& P, int r) {
+  return request(P, P.cu_q[r], P.cu_q[r + 1], P.kv_lens[r]);
 }
 
 // The cached tokens [lo, hi) that the query positions [p0, p1] may see, lo rounded down to

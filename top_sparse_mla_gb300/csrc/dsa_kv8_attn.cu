@@ -19,7 +19,9 @@ namespace dsa_kv8 {
 
 constexpr int MAX_ROWS = 32;      // most query rows of a request in rows_kernel
 constexpr int ROW_WARPS = 4;      // warps of a rows_kernel CTA
-constexpr int MIN_STEPS = 8;      // a CTA's least share, in steps: two for each warp
+constexpr int UNIT_STEPS = 8;     // what a unit (request, KV head) costs a CTA beside its steps, in steps
+constexpr int MIN_SHARE = UNIT_STEPS + 8;   // a CTA's least share: a unit's beginning and two steps a warp
+constexpr int JOIN = 16;          // partial results that one CTA joins at a time
 constexpr int PLAN_THREADS = 1024;
 // rows_kernel's CTAs per SM, by tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
@@ -27,9 +29,10 @@ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
 
 // ------------------------------------------------------------------------------ plan
-// The steps of the small requests, all heads of all requests in a row, are cut into equal
-// shares, one for each CTA: a share may begin and end inside a request, and the CTAs are
-// done at the same time whatever the lengths.  The tiles of the other requests are listed.
+// The steps of the small requests, all heads of all requests in a row and UNIT_STEPS more
+// in front of each unit's for its beginning and end, are cut into equal shares, one for
+// each CTA: a share may begin and end inside a unit, and the CTAs are done at the same time
+// whatever the lengths.  The tiles of the other requests are listed.
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params P) {
   extern __shared__ long long s_step[];   // [n_req + 1] exclusive prefix of the steps
   long long* s_tile = s_step + P.n_req + 1;   // [n_req + 1] of the tiles
@@ -47,7 +50,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     int tiles = 0;
     if (a.q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
     else if (rows > P.small_rows) tiles = (rows + TILE_ROWS - 1) / TILE_ROWS;
-    else if (rows > 0) steps = span(P, a, 0, a.q_len - 1).steps;
+    else if (rows > 0) steps = UNIT_STEPS + span(P, a, 0, a.q_len - 1).steps;
     s_step[r] = steps;
     s_tile[r] = tiles;
   }
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   __syncthreads();
 
   const long long total = all * P.h_kv;
-  const long long share = max((total + P.n_shares - 1) / P.n_shares, (long long)MIN_STEPS);
+  const long long share = max((total + P.n_shares - 1) / P.n_shares, (long long)MIN_SHARE);
   for (int b = tid; b < P.n_shares; b += PLAN_THREADS) {
     Share s;
     s.req = -1;
@@ -113,10 +116,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       const long long steps = s_step[lo + 1] - s_step[lo], rest = f - s_step[lo] * P.h_kv;
       s.req = lo;
       s.head = (int)(rest / steps);
-      s.step = rest - s.head * steps;
+      s.step = rest - s.head * steps - UNIT_STEPS;
     }
     P.shares[b] = s;
-    P.arrived[b] = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) P.arrived[3 * b + i] = 0;
   }
   // ascending cu_q cannot give more tiles than the list has room for
   const int n_tiles = (int)min(all_tiles, (long long)P.max_tiles);
@@ -215,37 +219,40 @@ struct Codes {
   uint4 v[4];           // tokens 2c, 2c + 1, 2c + 8, 2c + 9: bytes r * (D / 8) .. (8 of them for D = 64)
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void rows_steps(const Params& P, int req, int head, int lo, int seen_lo, int hi, int step0,
-                                           int step1, int stride, const uint32_t (&qf)[NT == 1 ? D / 16 : 1][2],
-                                           const uint16_t* s_q, const float (&qs)[NT][2], const int (&pos)[NT][2],
-                                           int pos_min, int pos_max, RowState<D, NT>& R) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int page_mask = (1 << P.page_shift) - 1;
-  const int32_t* table = P.table + req * P.table_ld;
-  // the page of a step, -1 where there is none
-  auto page_of = [&](int s) -> int {
-    const int base = lo + s * STEP;
-    if (s >= step1 || base >= hi) return -1;
-    const int p = __ldg(table + (base >> P.page_shift));
-    return (p < 0 || p >= P.n_pages) ? -1 : p;
-  };
-  auto row_of = [&](int page, int s) -> long long {
-    return (((long long)page * P.h_kv + head) << P.page_shift) + ((lo + s * STEP) & page_mask);
-  };
+// The steps of one warp: every `stride`-th one of [first, end).  A warp stops at the first
+// use of a value that it is still loading, so a step's table entry is loaded two steps
+// ahead and looked at one step later, its codes and scales one step ahead.
+template <int D>
+struct Steps {
+  const Params& P;
+  const int32_t* table;
+  int head, lo, hi, first, end, stride;
   Codes<D> C;
-  auto load_k = [&](int page, int s) {
-    if (page < 0) return;
-    const uint8_t* k = P.k_pool + (row_of(page, s) + r) * D + 16 * c;
+  int page, raw_next;   // the first step's page, the entry of the one behind it
+  float ks, vs;
+
+  __device__ __forceinline__ int entry(int s) const {
+    const int base = lo + s * STEP;
+    return (s < end && base < hi) ? __ldg(table + (base >> P.page_shift)) : -1;
+  }
+  __device__ __forceinline__ int valid(int raw) const { return (raw < 0 || raw >= P.n_pages) ? -1 : raw; }
+  __device__ __forceinline__ long long row_of(int page_, int s) const {
+    return (((long long)page_ * P.h_kv + head) << P.page_shift) + ((lo + s * STEP) & ((1 << P.page_shift) - 1));
+  }
+  __device__ __forceinline__ void load_k(int page_, int s) {
+    if (page_ < 0) return;
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const uint8_t* k = P.k_pool + (row_of(page_, s) + r) * D + 16 * c;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       C.k[0][j] = dsa::ldg_nc(k + 64 * j);
       C.k[1][j] = dsa::ldg_nc(k + 8 * D + 64 * j);
     }
-  };
-  auto load_v = [&](int page, int s) {
-    if (page < 0) return;
-    const uint8_t* v = P.v_pool + (row_of(page, s) + 2 * c) * D + r * (D / 8);
+  }
+  __device__ __forceinline__ void load_v(int page_, int s) {
+    if (page_ < 0) return;
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const uint8_t* v = P.v_pool + (row_of(page_, s) + 2 * c) * D + r * (D / 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint8_t* at = v + ((i & 1) + (i >> 1) * 8) * D;
@@ -256,21 +263,41 @@ __device__ __forceinline__ void rows_steps(const Params& P, int req, int head, i
         C.v[i] = make_uint4(x.x, x.y, 0u, 0u);
       }
     }
-  };
-  auto load_scale = [&](const float* scale, int page) -> float {
-    return page < 0 ? 1.0f : __ldg(scale + (long long)page * P.h_kv + head);
-  };
+  }
+  __device__ __forceinline__ float load_scale(const float* scale, int page_) const {
+    return page_ < 0 ? 1.0f : __ldg(scale + (long long)page_ * P.h_kv + head);
+  }
+  // two parts, so that the queries can be fetched between them
+  __device__ __forceinline__ void begin() {
+    page = entry(first);
+    raw_next = entry(first + stride);
+  }
+  __device__ __forceinline__ void load_first() {
+    page = valid(page);
+    load_k(page, first);
+    load_v(page, first);
+    ks = load_scale(P.k_scale, page);
+    vs = load_scale(P.v_scale, page);
+  }
+};
 
-  int page = page_of(step0), page_next = page_of(step0 + stride);
-  load_k(page, step0);
-  load_v(page, step0);
-  float ks = load_scale(P.k_scale, page), vs = load_scale(P.v_scale, page);
-  for (int s = step0; s < step1; s += stride) {
-    const int page_after = page_of(s + 2 * stride);
-    const float ks_next = load_scale(P.k_scale, page_next), vs_next = load_scale(P.v_scale, page_next);
+template <int D, int NT>
+__device__ __forceinline__ void rows_steps(const Params& P, Steps<D>& W, int seen_lo,
+                                           const uint32_t (&qf)[NT == 1 ? D / 16 : 1][2], const uint16_t* s_q,
+                                           const float (&qs)[NT][2], const int (&pos)[NT][2], int pos_min, int pos_max,
+                                           RowState<D, NT>& R) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int lo = W.lo, hi = W.hi, stride = W.stride;
+  Codes<D>& C = W.C;
+  int page = W.page, raw_next = W.raw_next;
+  float ks = W.ks, vs = W.vs;
+  for (int s = W.first; s < W.end; s += stride) {
+    const int page_next = W.valid(raw_next);
+    raw_next = W.entry(s + 2 * stride);
+    const float ks_next = W.load_scale(P.k_scale, page_next), vs_next = W.load_scale(P.v_scale, page_next);
     if (page < 0) {
-      load_k(page_next, s + stride);
-      load_v(page_next, s + stride);
+      W.load_k(page_next, s + stride);
+      W.load_v(page_next, s + stride);
     } else {
       const int base = lo + s * STEP;
       // scores
@@ -303,7 +330,7 @@ __device__ __forceinline__ void rows_steps(const Params& P, int req, int head, i
           }
         }
       }
-      load_k(page_next, s + stride);
+      W.load_k(page_next, s + stride);
       // t = x + log2(v_scale), masked
       const float vsc = bounded_scale(vs);
       const float bias = log2f(vsc), vinv = 1.0f / vsc;
@@ -380,10 +407,9 @@ __device__ __forceinline__ void rows_steps(const Params& P, int req, int head, i
           for (int nt = 0; nt < NT; ++nt)
             mma(R.o[nt][2 * i + h], a[h][0], a[h][1], a[h][2], a[h][3], pf[nt][0], pf[nt][1]);
       }
-      load_v(page_next, s + stride);
+      W.load_v(page_next, s + stride);
     }
     page = page_next;
-    page_next = page_after;
     ks = ks_next;
     vs = vs_next;
   }
@@ -395,31 +421,45 @@ struct RowSmem {
   float o[NW][8 * NT][PITCH];
   float m[NW][8 * NT], l[NW][8 * NT];
   uint16_t q[NT == 1 ? 8 : 8 * NT * (D + 8)];
+  float q_scale[8 * NT];
   int last;
 };
 
 // Steps [step0, step1) of one unit by the whole CTA, joined over its warps.  Rows
-// [row0, row0 + 8 NT) of the request.  Results go to `out` (pieces == 1) or to the CTA's
-// partial buffer, and the last CTA of a unit to arrive joins them in the order of the
+// [row0, row0 + 8 NT) of the request.  The unit is in `pieces`, which CTAs first_cta,
+// first_cta + 1, ... have; this CTA has piece `piece`.  A unit in one piece goes to `out`.
+// Else the pieces go to partial buffers, and the last CTA to arrive in each group of JOIN
+// pieces joins the group, and the last of those the groups: always in the order of the
 // pieces, so that the result does not depend on which one it was.
+//
+// A CTA has four partial buffers: for the piece of a unit that it began (1) or continued
+// (0), and for the group of pieces that it is the first of (3, 2).
 template <int D, int NT, int NW>
 __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S, int req, const Request& a, int head,
                                           int row0, const Span& sp, int step0, int step1, int pieces, int first_cta,
-                                          int my_slot) {
+                                          int piece) {
   constexpr int R8 = 8 * NT;
   constexpr int PSIZE = R8 * D + 2 * R8;   // floats of one partial result
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, r = lane >> 2, c = lane & 3;
   const int rows = a.rows(P);
   const int pos0 = a.kv - a.q_len;
 
+  const int pos_min = pos0 + row0 / P.group, pos_max = pos0 + min(row0 + R8 - 1, rows - 1) / P.group;
+  const int hi = min(pos_max + 1, a.kv);
+  const int seen_lo = P.window > 0 ? max(pos_min - P.window + 1, 0) : 0;
+  Steps<D> W{P, P.table + req * P.table_ld, head, sp.lo, hi, step0 + w, step1, NW};
+  W.begin();
+
   // queries: fp16 after a scaling of each row by a power of two that brings its largest
-  // magnitude to [2^7, 2^8)
+  // magnitude to [2^7, 2^8).  Every warp keeps a single tile of rows in registers; of
+  // several, a warp prepares one for all.
   uint32_t qf[NT == 1 ? D / 16 : 1][2];
   float qs[NT][2];
   int pos[NT][2];
-  float scale_row[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  float scale_row = 1.0f;
+  static_assert(NW >= NT, "a warp for each tile of rows");
+  if (NT == 1 || w < NT) {
+    const int nt = NT == 1 ? 0 : w;
     const int row = row0 + 8 * nt + r;
     uint4 v[D / 64][2];
     float mx = 0.f;
@@ -429,17 +469,20 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v[j][h] = in ? dsa::ldg_nc(src + 64 * j + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+      for (int h = 0; h < 2; ++h) v[j][h] = in ? dsa::ldg_nc(src + 64 * j + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+    W.load_first();
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = unpack(word(v[j][h], e), P.fp16);
           mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
-      }
     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-    const float down = row_scaling(mx, scale_row[nt]);
+    const float down = row_scaling(mx, scale_row);
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -455,23 +498,24 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
           qf[NT == 1 ? 4 * j + 2 * h : 0][1] = p[1];
           qf[NT == 1 ? 4 * j + 2 * h + 1 : 0][0] = p[2];
           qf[NT == 1 ? 4 * j + 2 * h + 1 : 0][1] = p[3];
-        } else if (w == 0) {
+        } else {
           *reinterpret_cast<uint4*>(S.q + (8 * nt + r) * (D + 8) + 64 * j + 16 * c + 8 * h) = make_uint4(p[0], p[1], p[2], p[3]);
         }
       }
+    if (NT > 1 && c == 0) S.q_scale[8 * nt + r] = scale_row;
+  } else {
+    W.load_first();
   }
-  // this lane's score columns are rows 8 nt + 2c + e; their scales are with lanes of r = 2c + e
+  if (NT > 1) __syncthreads();
+  // this lane's score columns are rows 8 nt + 2c + e
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      qs[nt][e] = __shfl_sync(0xFFFFFFFFu, scale_row[nt], (2 * c + e) * 4) * P.scale_log2;
+      const float back = NT == 1 ? __shfl_sync(0xFFFFFFFFu, scale_row, (2 * c + e) * 4) : S.q_scale[8 * nt + 2 * c + e];
+      qs[nt][e] = back * P.scale_log2;
       pos[nt][e] = pos0 + min(row0 + 8 * nt + 2 * c + e, rows - 1) / P.group;
     }
-  const int pos_min = pos0 + row0 / P.group, pos_max = pos0 + min(row0 + R8 - 1, rows - 1) / P.group;
-  const int hi = min(pos_max + 1, a.kv);
-  const int seen_lo = P.window > 0 ? max(pos_min - P.window + 1, 0) : 0;
-  if (NT > 1) __syncthreads();
 
   RowState<D, NT> R;
 #pragma unroll
@@ -486,7 +530,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
       R.l[nt][e] = 0.f;
     }
   }
-  rows_steps<D, NT>(P, req, head, sp.lo, seen_lo, hi, step0 + w, step1, NW, qf, S.q, qs, pos, pos_min, pos_max, R);
+  rows_steps<D, NT>(P, W, seen_lo, qf, S.q, qs, pos, pos_min, pos_max, R);
 
   // join the warps: dims are kept in the order mt * 16 + r * 2 + (0, 1)
 #pragma unroll
@@ -507,7 +551,10 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
     }
   __syncthreads();
   const int live = min(rows - row0, R8);
-  float* mine = pieces > 1 ? P.partial + (long long)my_slot * PSIZE : nullptr;
+  auto buffer = [&](int p, int group) -> float* {
+    return P.partial + (4LL * (first_cta + p) + 2 * group + (p == 0 ? 1 : 0)) * PSIZE;
+  };
+  float* mine = pieces > 1 ? buffer(piece, 0) : nullptr;
   auto write = [&](int row, int k4, float4 o, float m, float l) {
     // o: dims k4 .. k4 + 3 in the joined order, which are two pairs of neighbours
     const int i = (row0 + row) / P.group, h = head * P.group + (row0 + row) - i * P.group;
@@ -547,29 +594,22 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
     }
   }
   if (pieces > 1) {
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) S.last = atomicAdd(P.arrived + first_cta, 1) == pieces - 1;
-    __syncthreads();
-    if (S.last) {
-      __threadfence();
-      // piece 0 is the second buffer of the unit's first CTA, the others the first buffers
-      // of the CTAs behind it
+    // join pieces p0, p0 + by, ... (n of them, of this kind of buffer) into `to`, or into the result
+    auto join = [&](int p0, int by, int n, int group, float* to) {
       for (int u = tid; u < live * (D / 4); u += 32 * NW) {
         const int row = u / (D / 4), k4 = (u % (D / 4)) * 4;
         float m = M_INIT, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = 0; p0 < pieces; p0 += 8) {
+        for (int x0 = 0; x0 < n; x0 += 8) {
           float pm[8], pl[8];
           float4 po[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
-            const int p = p0 + x;
             pm[x] = M_INIT;
             pl[x] = 0.f;
             po[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p < pieces) {
-              const float* b = P.partial + (long long)(2 * (first_cta + p) + (p == 0 ? 1 : 0)) * PSIZE;
+            if (x0 + x < n) {
+              const float* b = buffer(p0 + (x0 + x) * by, group);
               po[x] = __ldcg(reinterpret_cast<const float4*>(b + row * D + k4));
               pm[x] = __ldcg(b + R8 * D + row);
               pl[x] = __ldcg(b + R8 * D + R8 + row);
@@ -592,8 +632,31 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
           }
           m = top;
         }
-        write(row, k4, o, m, l);
+        if (!to) {
+          write(row, k4, o, m, l);
+        } else {
+          *reinterpret_cast<float4*>(to + row * D + k4) = o;
+          if (k4 == 0) {
+            to[R8 * D + row] = m;
+            to[R8 * D + R8 + row] = l;
+          }
+        }
       }
+    };
+    // whether this CTA is the last of n to come to a counter
+    auto arrive = [&](int* counter, int n) -> bool {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) S.last = atomicAdd(counter, 1) == n - 1;
+      __syncthreads();
+      const bool last = S.last != 0;
+      if (last) __threadfence();
+      return last;
+    };
+    const int groups = (pieces + JOIN - 1) / JOIN, lead = piece / JOIN * JOIN;
+    if (arrive(P.arrived + 3 * (first_cta + lead) + (lead == 0 ? 1 : 0), min(JOIN, pieces - lead))) {
+      join(lead, 1, min(JOIN, pieces - lead), 0, groups > 1 ? buffer(lead, 1) : nullptr);
+      if (groups > 1 && arrive(P.arrived + 3 * first_cta + 2, groups)) join(0, JOIN, groups, 1, nullptr);
     }
   }
   __syncthreads();   // the shared memory is used again
@@ -609,25 +672,35 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) rows_kernel(const __
   const Share at = P.shares[b];
   int req = at.req, head = at.head;
   if (req < 0) return;
-  long long step = at.step, left = share;
-  long long unit = b * share - step;   // where the unit begins among all steps
+  long long step = at.step, left = share;   // step: of the unit, below 0 in its beginning
+  long long unit = b * share - step;        // where the unit's steps begin among all
   Request a = request(P, req);
   Span sp = span(P, a, 0, a.q_len - 1);
   while (true) {
-    const int take = (int)min(left, sp.steps - step);
-    const int first = (int)(unit / share), lastc = (int)((unit + sp.steps - 1) / share);
-    rows_unit<D, NT, NW>(P, S, req, a, head, 0, sp, (int)step, (int)step + take, lastc - first + 1, first,
-                         2 * b + (first == b ? 1 : 0));
-    left -= take;
+    // the next request's lengths, while this unit is computed
+    int next[3] = {0, 0, 0};
+    if (head + 1 == P.h_kv && req + 1 < P.n_req) {
+      next[0] = __ldg(P.cu_q + req + 1);
+      next[1] = __ldg(P.cu_q + req + 2);
+      next[2] = __ldg(P.kv_lens + req + 1);
+    }
+    const int s0 = (int)max(step, 0LL), s1 = (int)min((long long)sp.steps, step + left);
+    if (s0 < s1) {
+      const int first = (int)(unit / share), last = (int)((unit + sp.steps - 1) / share);
+      rows_unit<D, NT, NW>(P, S, req, a, head, 0, sp, s0, s1, last - first + 1, first, b - first);
+    }
+    left -= min(left, sp.steps - step);
     if (left == 0) return;
-    unit += sp.steps;
-    step = 0;
+    unit += sp.steps + UNIT_STEPS;
+    step = -UNIT_STEPS;
     if (++head < P.h_kv) continue;
     head = 0;
-    do {
+    if (++req >= P.n_req) return;
+    a = request(P, next[0], next[1], next[2]);
+    while (a.q_len == 0 || a.q_len > P.max_q_len || a.rows(P) > P.small_rows) {
       if (++req >= P.n_req) return;
       a = request(P, req);
-    } while (a.q_len == 0 || a.q_len > P.max_q_len || a.rows(P) > P.small_rows);
+    }
     sp = span(P, a, 0, a.q_len - 1);
   }
 }
@@ -672,12 +745,12 @@ static Layout layout(const dsa_kv8_params* p, int sms) {
   L.shares = at;
   at += up(L.n_shares * sizeof(Share));
   L.arrived = at;
-  at += up(L.n_shares * sizeof(int));
+  at += up(L.n_shares * 3 * sizeof(int));
   L.tiles = at;
   L.max_tiles = (int)(p->n_tokens * group / TILE_ROWS + p->n_req);
   at += up((size_t)L.max_tiles * sizeof(Tile));
   L.partial = at;
-  at += up((size_t)L.n_shares * 2 * (rows * p->d + 2 * rows) * sizeof(float));
+  at += up((size_t)L.n_shares * 4 * (rows * p->d + 2 * rows) * sizeof(float));
   L.bytes = at;
   return L;
 }
