@@ -201,8 +201,14 @@ def _ptr(x):
     return x.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object, which takes longer than a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
