@@ -7,7 +7,8 @@
  * The value of a code is e4m3 * scale.  A request's token at position p is row
  * p % page_size of page block_table[r][p / page_size] (see dsa_page_map.h, which builds
  * the tables and the slots page * page_size + p % page_size).
- *   d is 64 or 128; page_size is 16, 32, 64 or 128; 1 <= h_kv <= DSA_KV8_MAX_HEADS.
+ *   d is 64 or 128; page_size is 16, 32, 64 or 128; 1 <= h_kv <= DSA_KV8_MAX_HEADS;
+ *   n_pages * h_kv * page_size < 2^32 - 1.
  *
  * ---- dsa_kv8_insert: quantise new tokens' keys and values into their pages.
  * Token i of the batch goes to row slots[i] % page_size of page slots[i] / page_size;
@@ -73,7 +74,8 @@
  * allocate nothing and can be captured in a CUDA graph.  They return DSA_OK, or one of the
  * following with nothing enqueued:
  *   - DSA_ERR_INVALID_ARG: a bad size or parameter, a null or misaligned pointer;
- *   - DSA_ERR_UNSUPPORTED_SHAPE: d, page_size, h_kv, h_q / h_kv or n_req not served;
+ *   - DSA_ERR_UNSUPPORTED_SHAPE: d, page_size, h_kv, h_q / h_kv, n_req or a product of sizes
+ *     not served (attention: n_tokens * h_q / h_kv < 2^31);
  *   - DSA_ERR_WORKSPACE_TOO_SMALL (attention);
  *   - DSA_ERR_UNSUPPORTED_DEVICE: not compute capability 10.3;
  *   - DSA_ERR_CUDA.

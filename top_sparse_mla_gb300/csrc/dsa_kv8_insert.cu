@@ -5,8 +5,8 @@
 // one KV head, keys or values; a run that passes the window's end is finished by the CTA
 // where it starts, so no two CTAs touch one page.  D / 8 lanes hold a token (16 bytes
 // each), so that a row is read in one piece:
-//   1. every token of the CTA's runs is read once into registers, and its largest
-//      magnitude goes into its run's maximum (shared memory, an integer maximum of the
+//   1. every token of the CTA's runs is read once into registers (while the slots, from
+//      which the runs follow, are fetched), and its largest magnitude goes into its run's maximum (shared memory, an integer maximum of the
 //      bits, which order as the magnitudes do);
 //   2. one thread per run forms the scale from the maximum's exponent, writes it, and
 //      lists the run if the page's older rows have to be rescaled;
@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "dsa_kv8.h"
 #include "ptx_sm103.cuh"
@@ -24,6 +25,7 @@
 namespace dsa_kv8_insert_impl {
 
 constexpr int THREADS = 256;
+constexpr uint32_t NONE = 0xFFFFFFFFu;
 constexpr int WINDOW = 64;   // most tokens in which a CTA's runs start
 
 struct Params {
@@ -37,9 +39,18 @@ struct Params {
   int n_tokens, h_kv, page_shift, window;
 };
 
-__device__ __forceinline__ float2 to_f32x2(uint32_t w, int fp16) {
-  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+template <bool FP16>
+__device__ __forceinline__ float2 to_f32x2(uint32_t w) {
+  if (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// larger of two values each, by lane of the word; a NaN loses
+template <bool FP16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (FP16) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // least power of two s >= 2^-64 with amax <= 448 s = 1.75 * 2^8 s, at most 2^64
@@ -50,13 +61,14 @@ __device__ __forceinline__ float page_scale(uint32_t amax_bits) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-template <int D, int PASSES>
-__global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__ Params P, int fp16) {
+template <int D, int PASSES, bool FP16>
+__global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__ Params P) {
   constexpr int LANES = D / 8;                    // lanes of one token
   constexpr int GROUPS = THREADS / LANES;         // tokens per pass
   constexpr int SPAN = PASSES * GROUPS;           // tokens that the CTA may hold
   __shared__ long long s_slot[SPAN + 1];          // [i + 1]: slot of token t0 + i
   __shared__ int s_run[SPAN];                     // where a token's run starts, -1: not this CTA's
+  __shared__ uint2 s_to[SPAN];                    // its row in the pool and 1 / scale; NONE
   __shared__ uint32_t s_amax[WINDOW];             // by the run's first token
   __shared__ float s_scale[WINDOW];
   __shared__ int s_last[THREADS / 32];
@@ -64,10 +76,25 @@ __global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__
   __shared__ float s_old_ratio[WINDOW];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int t0 = blockIdx.x * P.window;
-  const int head = blockIdx.y, which = blockIdx.z;
+  // heads first, then keys and values, then windows: CTAs that run together read whole
+  // rows of the inputs and write whole pages
+  const int head = blockIdx.x % P.h_kv, which = (blockIdx.x / P.h_kv) & 1;
+  const int t0 = blockIdx.x / P.h_kv / 2 * P.window;
   const int page_mask = (1 << P.page_shift) - 1;
   static_assert(SPAN <= THREADS, "one thread per token");
+
+  // 1a. the window's values, before it is known which of them are the CTA's (all but a
+  // run's end that began in front of the window): the runs are found while they arrive
+  const int group = tid / LANES, part = tid % LANES;
+  const uint16_t* src = P.x[which] + head * P.hd[which] + part * 8;
+  uint4 x[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * GROUPS + group;
+    x[p] = make_uint4(0u, 0u, 0u, 0u);
+    if (p < WINDOW / GROUPS && i < P.window && t0 + i < P.n_tokens)
+      x[p] = dsa::ldg_nc(src + (t0 + i) * P.ld[which]);
+  }
 
   // slots and runs
   long long slot = -1;
@@ -92,6 +119,11 @@ __global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__
   const uint32_t upto = breaks & (0xFFFFFFFFu >> (31 - lane));
   int from = upto ? 32 * w + 31 - __clz(upto) : -1;
   if (lane == 31) s_last[w] = from;
+  // the scale of a page that a run continues, used when the maxima are known
+  float* const scale_at = P.scale[which] + (slot >> P.page_shift) * P.h_kv + head;
+  const bool own = tid < P.window && starts, continues = own && (slot & page_mask) != 0;
+  float old = 0.f;
+  if (continues) old = *scale_at;
   __syncthreads();
   for (int u = w - 1; u >= 0 && from < 0; --u) from = s_last[u];
   // `from` is the run's start if a run starts there: -1 (the run began before this window)
@@ -99,40 +131,30 @@ __global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__
   if (tid < SPAN) s_run[tid] = (slot >= 0 && from >= 0 && from < P.window) ? from : -1;
   __syncthreads();
 
-  // 1. values into registers, maxima of the runs
-  const int group = tid / LANES, part = tid % LANES;
-  const uint16_t* src = P.x[which] + head * P.hd[which] + part * 8;
-  uint4 x[PASSES];
+  // 1b. the values of runs that pass the window's end
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int i = p * GROUPS + group;
-    x[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (s_run[i] >= 0) x[p] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + i) * P.ld[which]));
+    if ((p >= WINDOW / GROUPS || i >= P.window) && s_run[i] >= 0) x[p] = dsa::ldg_nc(src + (t0 + i) * P.ld[which]);
   }
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const uint32_t v[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-    float m = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = to_f32x2(v[k], fp16);
-      m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));   // a NaN is left out by the maximum
-    }
-#pragma unroll
-    for (int o = LANES / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const int run = s_run[p * GROUPS + group];
-    if (part == 0 && run >= 0) atomicMax(&s_amax[run], __float_as_uint(m));
+    if (!__any_sync(0xFFFFFFFFu, run >= 0)) continue;
+    constexpr uint32_t ABS = 0x7FFF7FFFu;
+    uint32_t m2 = max2<FP16>(max2<FP16>(x[p].x & ABS, x[p].y & ABS), max2<FP16>(x[p].z & ABS, x[p].w & ABS));
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) m2 = max2<FP16>(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
+    const float2 m = to_f32x2<FP16>(m2);
+    // fmaxf leaves out a NaN (which is all that was there, if it is still here)
+    if (part == 0 && run >= 0) atomicMax(&s_amax[run], __float_as_uint(fmaxf(0.f, fmaxf(m.x, m.y))));
   }
   __syncthreads();
 
   // 2. scales
-  if (tid < P.window && starts) {
-    const long long page = slot >> P.page_shift;
-    const int o0 = (int)slot & page_mask;
-    float* at = P.scale[which] + page * P.h_kv + head;
+  if (own) {
     float s = page_scale(s_amax[tid]);
-    if (o0 > 0) {
-      const float old = *at;
+    if (continues) {
       if (old >= s) {
         s = old;
       } else {
@@ -141,28 +163,32 @@ __global__ void __launch_bounds__(THREADS) insert_kernel(const __grid_constant__
         s_old_ratio[k] = old / s;
       }
     }
-    *at = s;
+    *scale_at = s;
     s_scale[tid] = 1.0f / s;
+  }
+  __syncthreads();
+  if (tid < SPAN) {
+    const int run = s_run[tid];
+    const uint32_t row = (((uint32_t)(slot >> P.page_shift) * P.h_kv + head) << P.page_shift) + ((uint32_t)slot & page_mask);
+    s_to[tid] = run >= 0 ? make_uint2(row, __float_as_uint(s_scale[run])) : make_uint2(NONE, 0u);
   }
   __syncthreads();
 
   // 3. codes
+  uint8_t* const dst = P.pool[which] + part * 8;
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int i = p * GROUPS + group;
-    const int run = s_run[i];
-    if (run < 0) continue;
-    const float inv = s_scale[run];
+    const uint2 to = s_to[p * GROUPS + group];
+    if (to.x == NONE) continue;
+    const float inv = __uint_as_float(to.y);
     const uint32_t v[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
     uint32_t c[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 f = to_f32x2(v[k], fp16);
+      const float2 f = to_f32x2<FP16>(v[k]);
       c[k] = dsa::f32x2_to_e4m3x2(f.x * inv, f.y * inv);
     }
-    const long long sl = s_slot[i + 1];
-    const long long row = (((sl >> P.page_shift) * P.h_kv + head) << P.page_shift) + (sl & page_mask);
-    *reinterpret_cast<uint2*>(P.pool[which] + row * D + part * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    *reinterpret_cast<uint2*>(dst + (uint64_t)to.x * D) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
   }
 
   // the older rows of pages whose scale grew: (run, row) pairs over the groups
@@ -214,7 +240,7 @@ extern "C" int dsa_kv8_insert(const void* k, int64_t k_ld, int64_t k_hd, const v
   if (n_tokens < 0 || n_tokens > (1 << 30) || n_pages < 0 || h_kv < 1 || (type != DSA_KV8_BF16 && type != DSA_KV8_FP16))
     return DSA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
-      h_kv > DSA_KV8_MAX_HEADS)
+      h_kv > DSA_KV8_MAX_HEADS || (long long)n_pages * h_kv * page_size >= (1LL << 32) - 1)   // rows are numbered in 32 bits
     return DSA_ERR_UNSUPPORTED_SHAPE;
   if (n_tokens == 0) return DSA_OK;
   if (bad_pitch(k_ld, k_hd, h_kv, d) || bad_pitch(v_ld, v_hd, h_kv, d)) return DSA_ERR_INVALID_ARG;
@@ -246,16 +272,23 @@ extern "C" int dsa_kv8_insert(const void* k, int64_t k_ld, int64_t k_hd, const v
   P.h_kv = h_kv;
   P.page_shift = __builtin_ctz(page_size);
   P.window = WINDOW;
-  const dim3 grid((unsigned)((n_tokens + P.window - 1) / P.window), (unsigned)h_kv, 2);
-  const int fp16 = type == DSA_KV8_FP16;
+  const long long ctas = (long long)((n_tokens + P.window - 1) / P.window) * h_kv * 2;
+  if (ctas >= (1LL << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  const unsigned grid = (unsigned)ctas;
   cudaStream_t st = (cudaStream_t)stream;
   // WINDOW + page_size - 1 tokens fit the CTA's registers: 128 for pages of up to 64 tokens, 192 for 128
-  if (d == 128) {
-    if (page_size <= 64) insert_kernel<128, 8><<<grid, THREADS, 0, st>>>(P, fp16);
-    else insert_kernel<128, 12><<<grid, THREADS, 0, st>>>(P, fp16);
-  } else {
-    if (page_size <= 64) insert_kernel<64, 4><<<grid, THREADS, 0, st>>>(P, fp16);
-    else insert_kernel<64, 6><<<grid, THREADS, 0, st>>>(P, fp16);
-  }
+  const bool wide = page_size > 64;
+  auto launch = [&](auto fp16) {
+    constexpr bool F = decltype(fp16)::value;
+    if (d == 128) {
+      if (!wide) insert_kernel<128, 8, F><<<grid, THREADS, 0, st>>>(P);
+      else insert_kernel<128, 12, F><<<grid, THREADS, 0, st>>>(P);
+    } else {
+      if (!wide) insert_kernel<64, 4, F><<<grid, THREADS, 0, st>>>(P);
+      else insert_kernel<64, 6, F><<<grid, THREADS, 0, st>>>(P);
+    }
+  };
+  if (type == DSA_KV8_FP16) launch(std::true_type());
+  else launch(std::false_type());
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
