@@ -361,3 +361,23 @@ def test_a_workspace_that_is_too_small_is_refused():
     with pytest.raises(native.DsaError) as err:
         c.run(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
     assert err.value.code == native.DSA_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    c = Case(31, [(1, 50), (1, 20)], h=1, g=2)
+    D = c.device()
+    n = len(c.lens)
+    one_row = D["table"][:1].expand(n, -1)                       # rows that overlap
+    for name, bad in (("table", one_row), ("table", D["table"].long()), ("table", D["table"].t().contiguous().t()[:, :1]),
+                      ("cu", D["cu"][:-1]), ("kv", D["kv"].cpu()), ("ks", D["ks"].double()), ("vs", D["vs"][:-1]),
+                      ("vp", D["vp"].transpose(2, 3)), ("q", D["q"].half()), ("q", D["q"][:, :1]), ("kp", D["kp"][:, :, :8])):
+        p = native.dsa_kv8_params_init(D["q"], D["kp"], D["table"], max_q_len=1)
+        E = dict(D, **{name: bad})
+        out = torch.full((c.n, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(native.dsa_kv8_attn_workspace_size(p), dtype=torch.uint8, device="cuda")
+        if name == "table" and bad.dtype == torch.int32 and bad.shape[1] == 1 and p.table_cols == 1:
+            continue
+        with pytest.raises(native.DsaError) as err:
+            native.dsa_kv8_attn_fwd(E["q"], E["kp"], E["vp"], E["ks"], E["vs"], E["table"], E["cu"], E["kv"], out, p, ws)
+        assert err.value.code == native.DSA_ERR_INVALID_ARG
+        assert (out == 7).all()

@@ -276,6 +276,9 @@ def dsa_kv_insert(kv, positions, slots, kv_norm_w, pool, rms_eps: float = 1e-6, 
         raise DsaError(rc, "dsa_kv_insert")
 
 
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+
+
 def _refuse(where: str, what: str) -> None:
     raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {what}")
 
@@ -289,7 +292,8 @@ def _device(where: str, x) -> int:
 
 
 def _dense(where: str, dev: int, *specs) -> None:
-    """Each (tensor, name, dtype, shape) is a contiguous tensor of that dtype and shape on device dev."""
+    """Each (tensor, name, dtype, shape) is a contiguous tensor of that dtype and shape on device dev.  (The entry
+    points look at their tensors in one expression first, which takes half the time, and come here for the reason.)"""
     for x, name, dtype, shape in specs:
         if x.dtype is not dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
             _refuse(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current CUDA "
@@ -298,19 +302,22 @@ def _dense(where: str, dev: int, *specs) -> None:
 
 def _table_pitch(where: str, dev: int, x, n_req: int, cols: int) -> int:
     """Row pitch of a block table: int32 [n_req, cols] with dense rows."""
-    if (x.dtype is not torch.int32 or x.shape != (n_req, cols) or (cols > 1 and x.stride(1) != 1)
+    ld, one = x.stride() if x.dim() == 2 else (0, 0)
+    if (x.dtype is not _I32 or x.shape != (n_req, cols) or (cols > 1 and one != 1) or (n_req > 1 and ld < cols)
             or x.get_device() != dev):
-        _refuse(where, "block_table must be an int32 [n_req, cols] tensor with dense rows on the current CUDA device")
-    return max(x.stride(0), cols) if n_req > 1 else cols
+        _refuse(where, "block_table must be an int32 [n_req, cols] tensor of dense rows that do not overlap, on the "
+                "current CUDA device")
+    return ld if n_req > 1 else cols
 
 
 def _heads(where: str, dev: int, x, name: str, dtype, n: int, h: int, d: int):
     """(token pitch, head pitch) of a [n, h, d] tensor whose last dimension is dense."""
-    if x.dtype is not dtype or x.shape != (n, h, d) or (n > 0 and x.stride(2) != 1) or x.get_device() != dev:
+    ld, hd, one = x.stride() if x.dim() == 3 else (0, 0, 0)
+    if x.dtype is not dtype or x.shape != (n, h, d) or (n > 0 and one != 1) or x.get_device() != dev:
         _refuse(where, f"{name} must be a {dtype} tensor of shape {(n, h, d)} with a dense last dimension on the "
                 f"current CUDA device, got {x.dtype} {tuple(x.shape)} on {x.device}")
     # a pitch that no second row uses may be anything: give the dense one
-    return (x.stride(0) if n > 1 else h * d), (x.stride(1) if h > 1 else d)
+    return (ld if n > 1 else h * d), (hd if h > 1 else d)
 
 
 def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu_new, kv_lens, positions, slots,
@@ -322,17 +329,24 @@ def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu
     where = "dsa_page_map"
     n_req, n_tokens, cols = ctx_lens.shape[0], slots.shape[0], block_table.shape[-1]
     dev = _device(where, ctx_lens)
-    i32 = torch.int32
-    by_token, by_req = (n_tokens,), (n_req,)
-    _dense(where, dev, (ctx_lens, "ctx_lens", i32, by_req), (new_lens, "new_lens", i32, by_req),
-           (free_pages, "free_pages", i32, (free_pages.shape[0],)), (cu_new, "cu_new", i32, (n_req + 1,)),
-           (kv_lens, "kv_lens", i32, by_req), (positions, "positions", i32, by_token),
-           (slots, "slots", torch.int64, by_token), (info, "info", i32, (2,)))
+    t, r = (n_tokens,), (n_req,)
+    if not (ctx_lens.dtype is new_lens.dtype is free_pages.dtype is cu_new.dtype is kv_lens.dtype is positions.dtype
+            is info.dtype is _I32 and slots.dtype is _I64 and ctx_lens.shape == new_lens.shape == kv_lens.shape == r
+            and positions.shape == slots.shape == t and cu_new.numel() == n_req + 1 and info.numel() == 2
+            and ctx_lens.is_contiguous() and new_lens.is_contiguous() and free_pages.is_contiguous()
+            and cu_new.is_contiguous() and kv_lens.is_contiguous() and positions.is_contiguous()
+            and slots.is_contiguous() and info.is_contiguous()
+            and new_lens.get_device() == free_pages.get_device() == cu_new.get_device() == kv_lens.get_device()
+            == positions.get_device() == slots.get_device() == info.get_device() == dev):
+        _dense(where, dev, (ctx_lens, "ctx_lens", _I32, r), (new_lens, "new_lens", _I32, r),
+               (free_pages, "free_pages", _I32, (free_pages.numel(),)), (cu_new, "cu_new", _I32, (n_req + 1,)),
+               (kv_lens, "kv_lens", _I32, r), (positions, "positions", _I32, t), (slots, "slots", _I64, t),
+               (info, "info", _I32, (2,)))
     if token_req is not None:
-        _dense(where, dev, (token_req, "token_req", i32, by_token))
+        _dense(where, dev, (token_req, "token_req", _I32, t))
     ld = _table_pitch(where, dev, block_table, n_req, cols)
     rc = library().dsa_page_map(ctx_lens.data_ptr(), new_lens.data_ptr(), n_req, block_table.data_ptr(), ld, cols,
-                                free_pages.data_ptr(), free_pages.shape[0], page_size, n_tokens, cu_new.data_ptr(),
+                                free_pages.data_ptr(), free_pages.numel(), page_size, n_tokens, cu_new.data_ptr(),
                                 kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), _ptr(token_req),
                                 info.data_ptr(), _stream(stream))
     if rc != DSA_OK:
@@ -346,8 +360,12 @@ def _kv8_pools(where, dev, k_pool, v_pool, k_scale, v_scale):
     shape = k_pool.shape
     if len(shape) != 4:
         _refuse(where, "k_pool must be [n_pages, h_kv, page_size, d]")
-    _dense(where, dev, (k_pool, "k_pool", torch.uint8, shape), (v_pool, "v_pool", torch.uint8, shape),
-           (k_scale, "k_scale", torch.float32, shape[:2]), (v_scale, "v_scale", torch.float32, shape[:2]))
+    if not (k_pool.dtype is v_pool.dtype is _U8 and k_scale.dtype is v_scale.dtype is _F32 and v_pool.shape == shape
+            and k_scale.shape == v_scale.shape == shape[:2] and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and k_pool.get_device() == v_pool.get_device() == k_scale.get_device() == v_scale.get_device() == dev):
+        _dense(where, dev, (k_pool, "k_pool", _U8, shape), (v_pool, "v_pool", _U8, shape),
+               (k_scale, "k_scale", _F32, shape[:2]), (v_scale, "v_scale", _F32, shape[:2]))
     return shape
 
 
@@ -362,7 +380,8 @@ def dsa_kv8_insert(k, v, slots, k_pool, v_pool, k_scale, v_scale, status=None, s
     n, dtype = slots.shape[0], k.dtype
     if dtype not in _KV8_TYPES:
         _refuse(where, "k must be bfloat16 or float16")
-    _dense(where, dev, (slots, "slots", torch.int64, (n,)))
+    if not (slots.dtype is _I64 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == dev):
+        _dense(where, dev, (slots, "slots", _I64, (n,)))
     k_ld, k_hd = _heads(where, dev, k, "k", dtype, n, h_kv, d)
     v_ld, v_hd = _heads(where, dev, v, "v", dtype, n, h_kv, d)
     if status is not None and (status.element_size() != 4 or status.get_device() != dev):
@@ -422,9 +441,11 @@ def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_
         _refuse(where, "q's type is not that of p")
     q_ld, q_hd = _heads(where, dev, q, "q", dtype, n, h_q, p.d)
     out_ld, out_hd = _heads(where, dev, out, "out", dtype, n, h_q, p.d)
-    _dense(where, dev, (cu_q, "cu_q", torch.int32, (n_req + 1,)), (kv_lens, "kv_lens", torch.int32, (n_req,)))
+    if not (cu_q.dtype is kv_lens.dtype is _I32 and cu_q.shape == (n_req + 1,) and kv_lens.shape == (n_req,)
+            and cu_q.is_contiguous() and kv_lens.is_contiguous() and cu_q.get_device() == kv_lens.get_device() == dev):
+        _dense(where, dev, (cu_q, "cu_q", _I32, (n_req + 1,)), (kv_lens, "kv_lens", _I32, (n_req,)))
     if lse is not None:
-        _dense(where, dev, (lse, "lse", torch.float32, (n, h_q)))
+        _dense(where, dev, (lse, "lse", _F32, (n, h_q)))
     table_ld = _table_pitch(where, dev, block_table, n_req, p.table_cols)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(where, "the workspace must be contiguous and on the current CUDA device")
