@@ -23,9 +23,9 @@ constexpr int UNIT_STEPS = 8;     // what a unit (request, KV head) costs a CTA 
 constexpr int MIN_SHARE = UNIT_STEPS + 8;   // a CTA's least share: a unit's beginning and two steps a warp
 constexpr int JOIN = 16;          // partial results that one CTA joins at a time
 constexpr int PLAN_THREADS = 1024;
-// rows_kernel's CTAs per SM, by tiles of 8 query rows: what its registers leave room for.
+// rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+constexpr int ctas_per_sm(int d, int nt) { return (nt == 1 ? 4 : nt == 2 ? 3 : 2) + (d == 64 ? (nt == 1 ? 2 : 1) : 0); }
 constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
 
 // ------------------------------------------------------------------------------ plan
@@ -663,7 +663,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
 }
 
 template <int D, int NT, int NW>
-__global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) rows_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) rows_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   RowSmem<D, NT, NW>& S = *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -740,7 +740,7 @@ static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 static Layout layout(const dsa_kv8_params* p, int sms) {
   Layout L;
   const size_t group = p->h_q / p->h_kv, rows = 8 * (size_t)row_tiles(p);
-  L.n_shares = ctas_per_sm(row_tiles(p)) * sms;
+  L.n_shares = ctas_per_sm(p->d, row_tiles(p)) * sms;
   size_t at = 256;
   L.shares = at;
   at += up(L.n_shares * sizeof(Share));
