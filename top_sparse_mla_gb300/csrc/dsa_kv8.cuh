@@ -14,6 +14,7 @@ namespace dsa_kv8 {
 
 constexpr int STEP = 16;          // cached tokens of one step of a warp; every page size is a multiple
 constexpr int TILE_ROWS = 256;    // query rows of a tile
+constexpr int MAX_PIECES = 16;    // of a tile's blocks
 constexpr float LAG = 8.0f;       // how far, in powers of two, a running maximum may lag
 
 struct Share {   // where a CTA's share of the steps begins
@@ -33,6 +34,7 @@ struct Header {
   uint32_t status;
   int n_tiles;
   long long share;   // steps of every CTA
+  int pieces;        // most pieces that the blocks of a tile and head are cut into
 };
 
 struct Params {
@@ -48,9 +50,12 @@ struct Params {
   int* arrived;
   Tile* tiles;
   float* partial;
+  float* tile_partial;   // of a tile's half, by unit and piece: O [D / 4][128] float4, then m [128], l [128]
+  int* tile_arrived;     // by unit and half
   int n_tokens, n_req, h_q, h_kv, group, n_pages, page_shift, cap, max_q_len, window, fp16;
   int small_rows;   // requests with at most this many rows go to rows_kernel
-  int n_shares, max_tiles;
+  int n_shares, max_tiles, n_ctas;   // n_ctas: of the tiles' kernel
+  int tile_split;   // whether a tile's blocks may be cut into pieces
   float scale_log2;   // softmax_scale * log2 e
 };
 
@@ -118,6 +123,6 @@ __device__ __forceinline__ float bounded_scale(float s) {
 }
 
 // dsa_kv8_tiles.cu: the tiles of the requests with more rows than rows_kernel takes
-int launch_tiles(int d, int grid, const Params& P, cudaStream_t st);
+int launch_tiles(int d, const Params& P, cudaStream_t st);
 
 }  // namespace dsa_kv8

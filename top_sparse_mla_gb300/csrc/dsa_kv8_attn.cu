@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 
   const long long total = all * P.h_kv;
   const long long share = max((total + P.n_shares - 1) / P.n_shares, (long long)MIN_SHARE);
+  if (P.tile_arrived)
+    for (int i = tid; i < 2 * P.n_ctas; i += PLAN_THREADS) P.tile_arrived[i] = 0;
   for (int b = tid; b < P.n_shares; b += PLAN_THREADS) {
     Share s;
     s.req = -1;
@@ -173,6 +175,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   if (tid == 0) {
     P.header->status = s_bad;
     P.header->n_tiles = n_tiles;
+    // few units: their blocks are cut into pieces, so that every CTA has one
+    const long long units = (long long)n_tiles * P.h_kv;
+    P.header->pieces = units > 0 && P.tile_split ? (int)min(max(P.n_ctas / units, 1LL), (long long)MAX_PIECES) : 1;
     P.header->share = share;
   }
 }
@@ -730,9 +735,14 @@ static int row_tiles(const dsa_kv8_params* p) {
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
+// whether a request may have more rows than rows_kernel takes
+static bool has_tiles(const dsa_kv8_params* p) {
+  return (long long)p->max_q_len * (p->h_q / p->h_kv) > 8 * row_tiles(p);
+}
+
 struct Layout {
   int n_shares, max_tiles;
-  size_t shares, arrived, tiles, partial, bytes;
+  size_t shares, arrived, tiles, partial, tile_arrived, tile_partial, bytes;
 };
 
 static size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -751,6 +761,13 @@ static Layout layout(const dsa_kv8_params* p, int sms) {
   at += up((size_t)L.max_tiles * sizeof(Tile));
   L.partial = at;
   at += up((size_t)L.n_shares * 4 * (rows * p->d + 2 * rows) * sizeof(float));
+  L.tile_arrived = L.tile_partial = 0;   // no tiles
+  if (has_tiles(p)) {
+    L.tile_arrived = at;
+    at += up((size_t)2 * sms * sizeof(int));
+    L.tile_partial = at;
+    at += up((size_t)sms * 2 * 128 * (p->d + 2) * sizeof(float));
+  }
   L.bytes = at;
   return L;
 }
@@ -773,7 +790,7 @@ static int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st,
 }
 
 template <int D>
-static int launch_all(const dsa_kv8_params* p, const Params& P, int sms, cudaStream_t st) {
+static int launch_all(const dsa_kv8_params* p, const Params& P, cudaStream_t st) {
   int rc;
   switch (row_tiles(p)) {
     case 1:
@@ -786,10 +803,7 @@ static int launch_all(const dsa_kv8_params* p, const Params& P, int sms, cudaStr
       rc = launch(rows_kernel<D, 4, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 4, ROW_WARPS>), st, P, true);
   }
   if (rc != DSA_OK) return rc;
-  if ((long long)p->max_q_len * P.group > P.small_rows) {
-    const long long units = (long long)P.max_tiles * P.h_kv;
-    rc = launch_tiles(D, (int)(units < sms ? units : sms), P, st);
-  }
+  if (has_tiles(p)) rc = launch_tiles(D, P, st);
   return rc;
 }
 
@@ -881,6 +895,11 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   P.arrived = reinterpret_cast<int*>(ws + L.arrived);
   P.tiles = reinterpret_cast<Tile*>(ws + L.tiles);
   P.partial = reinterpret_cast<float*>(ws + L.partial);
+  P.tile_arrived = L.tile_arrived ? reinterpret_cast<int*>(ws + L.tile_arrived) : nullptr;
+  P.tile_partial = L.tile_partial ? reinterpret_cast<float*>(ws + L.tile_partial) : nullptr;
+  P.n_ctas = sms;
+  // where even the most tiles that these sizes allow leave half of the CTAs without one
+  P.tile_split = 2LL * L.max_tiles * p->h_kv <= sms;
   P.n_tokens = p->n_tokens;
   P.n_req = p->n_req;
   P.h_q = p->h_q;
@@ -901,7 +920,7 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   const size_t smem = (size_t)(p->n_req + 1) * 2 * sizeof(long long);
   const int rc1 = launch(plan_kernel, 1, PLAN_THREADS, smem, st, P, false);
   if (rc1 != DSA_OK) return rc1;
-  return p->d == 128 ? launch_all<128>(p, P, sms, st) : launch_all<64>(p, P, sms, st);
+  return p->d == 128 ? launch_all<128>(p, P, st) : launch_all<64>(p, P, st);
 }
 
 }  // extern "C"

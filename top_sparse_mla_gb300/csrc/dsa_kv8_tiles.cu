@@ -44,8 +44,11 @@ enum {
   B_KFULL = 0, B_KFREE = 2, B_VFULL = 4, B_VFREE = 6,   // fp16 tiles, by buffer
   B_SFULL = 8, B_PFULL = 10, B_QFULL = 12, B_OFULL = 14,   // scores, weights, queries, result, by half
   B_RAWFULL = 16, B_RAWFREE = 18,   // codes of keys (0) and values (1)
-  B_SCALES = 20, B_DRAIN = 24, N_BAR = 26
+  B_SCALES = 20, B_DRAIN = 24,
+  B_GROUP = 26,                     // the warps of a half meet
+  N_BAR = 28
 };
+constexpr float NOTHING = -1.0e30f;   // m of a piece in which a row saw nothing
 constexpr int N_SCALES = 4;      // blocks whose scales are kept: see copies()
 
 template <int D>
@@ -54,7 +57,7 @@ struct TileSmem {
   static constexpr int PANEL = BLOCK * 128;       // 64 dims of it
   static constexpr int RAWTILE = BLOCK * D;       // codes of a K or V block
   static constexpr int Q = 0, K = 2 * OPERAND, V = 4 * OPERAND, RAW = 6 * OPERAND, SCALES = RAW + 2 * RAWTILE;
-  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * N_BAR, BYTES = MISC + 16;
+  static constexpr int BAR = SCALES + N_SCALES * 8 * 16, MISC = BAR + 8 * N_BAR, BYTES = MISC + 32;
   static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 template <int D>
@@ -65,7 +68,8 @@ struct Tmem {   // columns
 struct Ctx {
   uint8_t* sm;
   uint32_t sb, bars;
-  volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2], [3]: groups of the K and V codes that have a page
+  volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2], [3]: groups of the K
+                        // and V codes that have a page, [4], [5]: a half's CTA is the last to arrive
   uint32_t* status;
 };
 
@@ -106,20 +110,31 @@ DSA_DEV void commit(uint32_t bar_addr) {
   __syncwarp();
 }
 
-// A unit as every role sees it.
+// A unit as every role sees it: the blocks of one piece of a tile, for one KV head.
 struct Unit {
-  Tile t;
-  int head;
-  int blocks[2];   // blocks of each half; 0 for a half without rows
+  Tile t;          // t.lo: of the piece
+  int head, index, piece, pieces;   // index: of (tile, head)
+  int blocks[2];   // blocks of each half; 0 for a half without rows or without blocks in the piece
+  bool rows[2];
 };
-// The units are in the order of the tiles, longest first; the CTAs take them forwards and backwards in turn, so that no CTA has the longer one of every
-// round (forwards only, the first CTA of a 2123-token prefill had 40 blocks where the mean
-// is 31).
-DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
+struct Work {
+  int n_tiles, pieces;
+};
+// Where there are fewer (tile, head) pairs than CTAs, the blocks of each are cut into up to
+// Work::pieces pieces of at least two blocks, which their CTAs join in the end.
+//
+// The units are in the order of the tiles, longest first; the CTAs take them forwards and
+// backwards in turn, so that no CTA has the longer one of every round (forwards only, the
+// first CTA of a 2123-token prefill had 40 blocks where the mean is 31).
+template <bool SPLIT>
+DSA_DEV bool unit(const Params& P, long long round, const Work& work, Unit& x) {
   const long long u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-  if (u >= (long long)n_tiles * P.h_kv) return false;
-  const int i = (int)(u / P.h_kv);
-  x.head = (int)(u - (long long)i * P.h_kv);
+  const long long per = SPLIT ? (long long)P.h_kv * work.pieces : P.h_kv;
+  if (u >= work.n_tiles * per) return false;
+  const int i = (int)(u / per), rest = (int)(u - i * per);
+  x.piece = SPLIT ? rest / P.h_kv : 0;
+  x.head = rest - x.piece * P.h_kv;
+  x.index = i * P.h_kv + x.head;
   const int4* at = reinterpret_cast<const int4*>(P.tiles + i);
   const int4 a = __ldg(at), b = __ldg(at + 1);
   x.t.req = a.x; x.t.row0 = a.y; x.t.q0 = a.z; x.t.rows = a.w;
@@ -128,9 +143,17 @@ DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
   for (int h = 0; h < 2; ++h) {
     const int r0 = x.t.row0 + 128 * h, r1 = min(r0 + 128, x.t.rows) - 1;
     const int hi = x.t.pos0 + r1 / P.group + 1;   // past the last token that the half sees
-    x.blocks[h] = r0 < x.t.rows ? max((hi - x.t.lo + BLOCK - 1) / BLOCK, 1) : 0;
-    if (r0 < x.t.rows && hi <= x.t.lo) x.blocks[h] = 1;
+    x.rows[h] = r0 < x.t.rows;
+    x.blocks[h] = x.rows[h] ? (hi > x.t.lo ? (hi - x.t.lo + BLOCK - 1) / BLOCK : 1) : 0;
   }
+  x.pieces = 1;
+  if (!SPLIT) return true;
+  const int all = max(x.blocks[0], x.blocks[1]);
+  x.pieces = min(work.pieces, max(all / 2, 1));
+  const int b0 = (int)((long long)all * x.piece / x.pieces), b1 = (int)((long long)all * (x.piece + 1) / x.pieces);
+  x.t.lo += b0 * BLOCK;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) x.blocks[h] = x.piece < x.pieces ? min(max(x.blocks[h] - b0, 0), b1 - b0) : 0;
   return true;
 }
 
@@ -142,8 +165,8 @@ DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
 // The scales of block g (counted over all units) are in slot g % 4.  They are written when
 // the codes of block g - 1 have left their buffer, so the V tile of block g - 2 was written,
 // so the products of block g - 4 are done: the softmax has left the slot.
-template <int D>
-DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
+template <int D, bool SPLIT>
+DSA_DEV void copies(const Params& P, const Ctx& c, const Work& work) {
   using SM = TileSmem<D>;
   constexpr uint32_t GROUP_BYTES = 16 * D;
   const int lane = threadIdx.x & 31, grp = lane & 7;
@@ -151,7 +174,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   uint32_t g = 0;
   bool ok = true;
   Unit x;
-  for (long long u = 0; ok && unit(P, u, n_tiles, x); ++u) {
+  for (long long u = 0; ok && unit<SPLIT>(P, u, work, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int32_t* table = P.table + x.t.req * P.table_ld;
     auto entry = [&](int i) -> int {
@@ -222,8 +245,8 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
 // Block g uses buffer g % 2 of K and V.  A lane turns 16 codes into two 16-byte units of a
 // swizzled row.  A quarter warp holds four chunks of an even row and the other four of the
 // odd row behind it, which meet in no bank, neither here nor there.
-template <int D>
-DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
+template <int D, bool SPLIT>
+DSA_DEV void dequant(const Params& P, const Ctx& c, const Work& work) {
   using SM = TileSmem<D>;
   constexpr int CHUNKS = D / 16;            // 16-byte chunks of a row
   constexpr int ROWS = 128 / CHUNKS;        // rows of one pass of the four warps: 16 or 32
@@ -236,7 +259,7 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   const uint32_t s0 = ((2 * (chunk & 3)) ^ (sub & 7)) << 4, s1 = ((2 * (chunk & 3) + 1) ^ (sub & 7)) << 4;
   uint32_t g = 0;
   Unit x;
-  for (long long u = 0; unit(P, u, n_tiles, x); ++u) {
+  for (long long u = 0; unit<SPLIT>(P, u, work, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int p_first = x.t.pos0 + x.t.row0 / P.group;
     const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
@@ -282,8 +305,8 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
 // ------------------------------------------------------------------------------ products
 // The whole warp runs this role and one elected lane issues each product: with
 // warp-uniform control flow the descriptors stay in uniform registers.
-template <int D>
-DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles) {
+template <int D, bool SPLIT>
+DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, const Work& work) {
   using SM = TileSmem<D>;
   using TM = Tmem<D>;
   constexpr uint32_t ID_QK = idesc_f16(128, BLOCK, 0, 0);
@@ -295,7 +318,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
   uint32_t np[2] = {0, 0};        // blocks of each half
   uint32_t nq[2] = {0, 0};        // units of each half
   Unit x;
-  for (long long u = 0; unit(P, u, n_tiles, x); ++u) {
+  for (long long u = 0; unit<SPLIT>(P, u, work, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     for (int i = 0; i <= blocks; ++i) {
       const int kb = (g + i) & 1, vb = kb ^ 1;
@@ -364,18 +387,18 @@ DSA_DEV float max3(float a, float b, float c) {
   return r;
 }
 
-template <int D>
-DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, int h) {
+template <int D, bool SPLIT>
+DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& work, int h) {
   using SM = TileSmem<D>;
   using TM = Tmem<D>;
   const int row_in = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;   // the warp's 32 lanes of tensor memory
   const uint32_t ts = tmem + lanes + TM::S + 128 * h, to = tmem + lanes + TM::O + D * h;
-  uint32_t g = 0, ns = 0, no = 0;
+  uint32_t g = 0, ns = 0, no = 0, meets = 0;
   Unit x;
-  for (long long u = 0; unit(P, u, n_tiles, x); ++u) {
+  for (long long u = 0; unit<SPLIT>(P, u, work, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
-    if (mine == 0) {
+    if (!(h == 0 ? x.rows[0] : x.rows[1]) || (SPLIT && x.piece >= x.pieces)) {
       g += blocks;
       continue;
     }
@@ -386,8 +409,8 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
     const int pos_min = x.t.pos0 + first / P.group, pos_max = x.t.pos0 + min(first + 127, x.t.rows - 1) / P.group;
     const int head = x.head * P.group + row - qi * P.group;
     // ---- the query row (its buffer was last read for this half's last scores)
-    float row_scale;
-    {
+    float row_scale = 1.0f;
+    if (!SPLIT || mine > 0) {
       const uint16_t* src = P.q + (x.t.q0 + qi) * P.q_ld + head * P.q_hd;
       uint4 v[D / 8];
       float mx = 0.f;
@@ -532,26 +555,92 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       arrive_w(c, B_PFULL + h);
     }
     // ---- result
-    if (!wait_w(c, B_OFULL + h, no & 1)) return;
-    ++no;
-    tc_fence_after();
-    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays one
+    if (!SPLIT || mine > 0) {
+      if (!wait_w(c, B_OFULL + h, no & 1)) return;
+      ++no;
+      tc_fence_after();
+    }
     uint16_t* dst = P.out + (x.t.q0 + qi) * P.out_ld + head * P.out_hd;
-#pragma unroll 1
-    for (int k = 0; k < D; k += 32) {
-      uint32_t o[32];
-      tmem_ld32(to + k, o);
-      tc_wait_ld();
-      if (live) {
+    auto write = [&](int k, const uint32_t (&o)[32], float inv) {
+      if (!live) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 v;
-          v.x = pack(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv, P.fp16);
-          v.y = pack(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv, P.fp16);
-          v.z = pack(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv, P.fp16);
-          v.w = pack(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv, P.fp16);
-          *reinterpret_cast<uint4*>(dst + k + 8 * e) = v;
+      for (int e = 0; e < 4; ++e) {
+        uint4 v;
+        v.x = pack(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv, P.fp16);
+        v.y = pack(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv, P.fp16);
+        v.z = pack(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv, P.fp16);
+        v.w = pack(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv, P.fp16);
+        *reinterpret_cast<uint4*>(dst + k + 8 * e) = v;
+      }
+    };
+    auto inverse = [](float sum) { return sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum); };   // a NaN sum stays one
+    if (!SPLIT || x.pieces == 1) {
+      const float inv = inverse(l);
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + k, o);
+        tc_wait_ld();
+        write(k, o, inv);
+      }
+    } else {
+      // one of several pieces: the half's last CTA to arrive joins them in their order
+      constexpr int PSIZE = 128 * (D + 2);
+      auto buffer = [&](int piece) { return P.tile_partial + ((long long)(x.index * work.pieces + piece) * 2 + h) * PSIZE; };
+      float* own = buffer(x.piece);
+      if (!SPLIT || mine > 0) {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + k, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(own)[(k / 4 + e) * 128 + row_in] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
+      }
+      own[128 * D + row_in] = fresh ? NOTHING : m;
+      own[128 * D + 128 + row_in] = l;
+      __threadfence();
+      arrive_w(c, B_GROUP + h);
+      if (!wait_w(c, B_GROUP + h, meets++ & 1)) return;
+      if (row_in == 0) c.misc[4 + h] = atomicAdd(P.tile_arrived + 2 * x.index + h, 1) == x.pieces - 1;
+      arrive_w(c, B_GROUP + h);
+      if (!wait_w(c, B_GROUP + h, meets++ & 1)) return;
+      if (!c.misc[4 + h]) {
+        g += blocks;
+        continue;
+      }
+      __threadfence();
+      m = NOTHING;
+      for (int p = 0; p < x.pieces; ++p) m = fmaxf(m, __ldcg(buffer(p) + 128 * D + row_in));
+      l = 0.f;
+      for (int p = 0; p < x.pieces; ++p)
+        l = fmaf(__ldcg(buffer(p) + 128 * D + 128 + row_in), ex2(__ldcg(buffer(p) + 128 * D + row_in) - m), l);
+      const float inv = inverse(l);
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 1
+        for (int p = 0; p < x.pieces; ++p) {
+          const float pm = __ldcg(buffer(p) + 128 * D + row_in);
+          if (pm == NOTHING) continue;   // its O may not be there
+          const float f = ex2(pm - m);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(buffer(p)) + (k / 4 + e) * 128 + row_in);
+            o[4 * e] = fmaf(v.x, f, o[4 * e]);
+            o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
+            o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
+            o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
+          }
+        }
+        uint32_t bits[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) bits[e] = __float_as_uint(o[e]);
+        write(k, bits, inv);
       }
     }
     if (live && P.lse)
@@ -560,7 +649,7 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
   }
 }
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using SM = TileSmem<D>;
@@ -583,6 +672,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
       mbar_init(bar(c, B_OFULL + i), 1);
       mbar_init(bar(c, B_RAWFULL + i), 1);
       mbar_init(bar(c, B_RAWFREE + i), 4);
+      mbar_init(bar(c, B_GROUP + i), 4);
     }
     for (int i = 0; i < N_SCALES; ++i) mbar_init(bar(c, B_SCALES + i), 1);
     mbar_init(bar(c, B_DRAIN), 1);
@@ -594,15 +684,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)c.misc[0];
-  const int n_tiles = P.header->n_tiles;
+  const Work work{P.header->n_tiles, P.header->pieces};
   if (warp < W_DQ) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    softmax<D>(P, c, tmem, n_tiles, warp >> 2);
+    softmax<D, SPLIT>(P, c, tmem, work, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    if (warp < W_MMA) dequant<D>(P, c, n_tiles);
-    else if (warp == W_MMA) products<D>(P, c, tmem, n_tiles);
-    else if (warp == W_COPY) copies<D>(P, c, n_tiles);
+    if (warp < W_MMA) dequant<D, SPLIT>(P, c, work);
+    else if (warp == W_MMA) products<D, SPLIT>(P, c, tmem, work);
+    else if (warp == W_COPY) copies<D, SPLIT>(P, c, work);
   }
   if (warp == W_MMA) commit(bar(c, B_DRAIN));
   tc_fence_before();
@@ -621,20 +711,23 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   }
 }
 
-template <int D>
-static int launch_one(int grid, const Params& P, cudaStream_t st) {
+template <int D, bool SPLIT>
+static int launch_one(const Params& P, cudaStream_t st) {
   constexpr int smem = TileSmem<D>::BYTES;
   // the kernel's groups trade the registers that its launch gave them
   cudaFuncAttributes a;
-  if (cudaFuncGetAttributes(&a, tiles_kernel<D>) != cudaSuccess || a.numRegs != LAUNCH_REGS) return DSA_ERR_CUDA;
-  if (cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (cudaFuncGetAttributes(&a, tiles_kernel<D, SPLIT>) != cudaSuccess || a.numRegs != LAUNCH_REGS) return DSA_ERR_CUDA;
+  if (cudaFuncSetAttribute(tiles_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  tiles_kernel<D><<<grid, TILE_THREADS, smem, st>>>(P);
+  tiles_kernel<D, SPLIT><<<P.n_ctas, TILE_THREADS, smem, st>>>(P);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-int launch_tiles(int d, int grid, const Params& P, cudaStream_t st) {
-  return d == 128 ? launch_one<128>(grid, P, st) : launch_one<64>(grid, P, st);
+// The kernel that can split a tile's blocks is a copy of its own: with the joining in it,
+// the other one's loops took a tenth longer.
+int launch_tiles(int d, const Params& P, cudaStream_t st) {
+  if (P.tile_split) return d == 128 ? launch_one<128, true>(P, st) : launch_one<64, true>(P, st);
+  return d == 128 ? launch_one<128, false>(P, st) : launch_one<64, false>(P, st);
 }
 
 }  // namespace dsa_kv8
