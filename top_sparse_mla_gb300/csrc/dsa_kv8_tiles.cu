@@ -48,7 +48,7 @@ enum {
   B_GROUP = 26,                     // the warps of a half meet
   N_BAR = 28
 };
-constexpr float NOTHING = -1.0e30f;   // m of a piece in which a row saw nothing
+constexpr float NOTHING = -1.0e30f;   // m of a piece in which a row saw nothing; its O is 0
 constexpr int N_SCALES = 4;      // blocks whose scales are kept: see copies()
 
 template <int D>
@@ -121,7 +121,8 @@ struct Work {
   int n_tiles, pieces;
 };
 // Where there are fewer (tile, head) pairs than CTAs, the blocks of each are cut into up to
-// Work::pieces pieces of at least two blocks, which their CTAs join in the end.
+// Work::pieces pieces of at least two blocks, which their CTAs join in the end.  A block
+// takes about 2.2 us and a piece 1.5 us of the joining, so sqrt(1.5 blocks) pieces are best.
 //
 // The units are in the order of the tiles, longest first; the CTAs take them forwards and
 // backwards in turn, so that no CTA has the longer one of every round (forwards only, the
@@ -149,7 +150,7 @@ DSA_DEV bool unit(const Params& P, long long round, const Work& work, Unit& x) {
   x.pieces = 1;
   if (!SPLIT) return true;
   const int all = max(x.blocks[0], x.blocks[1]);
-  x.pieces = min(work.pieces, max(all / 2, 1));
+  x.pieces = max(min(min(work.pieces, all / 2), (int)sqrtf(1.5f * (float)all)), 1);
   const int b0 = (int)((long long)all * x.piece / x.pieces), b1 = (int)((long long)all * (x.piece + 1) / x.pieces);
   x.t.lo += b0 * BLOCK;
 #pragma unroll
@@ -598,6 +599,9 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
           for (int e = 0; e < 8; ++e)
             reinterpret_cast<uint4*>(own)[(k / 4 + e) * 128 + row_in] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
+      } else {
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) reinterpret_cast<uint4*>(own)[k / 4 * 128 + row_in] = make_uint4(0u, 0u, 0u, 0u);
       }
       own[128 * D + row_in] = fresh ? NOTHING : m;
       own[128 * D + 128 + row_in] = l;
@@ -613,8 +617,10 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
       }
       __threadfence();
       m = NOTHING;
+#pragma unroll 4
       for (int p = 0; p < x.pieces; ++p) m = fmaxf(m, __ldcg(buffer(p) + 128 * D + row_in));
       l = 0.f;
+#pragma unroll 4
       for (int p = 0; p < x.pieces; ++p)
         l = fmaf(__ldcg(buffer(p) + 128 * D + 128 + row_in), ex2(__ldcg(buffer(p) + 128 * D + row_in) - m), l);
       const float inv = inverse(l);
@@ -624,18 +630,26 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
 #pragma unroll 1
-        for (int p = 0; p < x.pieces; ++p) {
-          const float pm = __ldcg(buffer(p) + 128 * D + row_in);
-          if (pm == NOTHING) continue;   // its O may not be there
-          const float f = ex2(pm - m);
+        for (int p0 = 0; p0 < x.pieces; p0 += 2) {   // two at a time: their loads are under way together
+          float4 v[2][8];
+          float f[2];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(buffer(p)) + (k / 4 + e) * 128 + row_in);
-            o[4 * e] = fmaf(v.x, f, o[4 * e]);
-            o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
-            o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
-            o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
+          for (int y = 0; y < 2; ++y) {
+            const float* from = buffer(min(p0 + y, x.pieces - 1));
+            const float pm = __ldcg(from + 128 * D + row_in);
+            f[y] = p0 + y < x.pieces ? ex2(pm - m) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[y][e] = __ldcg(reinterpret_cast<const float4*>(from) + (k / 4 + e) * 128 + row_in);
           }
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = fmaf(v[y][e].x, f[y], o[4 * e]);
+              o[4 * e + 1] = fmaf(v[y][e].y, f[y], o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(v[y][e].z, f[y], o[4 * e + 2]);
+              o[4 * e + 3] = fmaf(v[y][e].w, f[y], o[4 * e + 3]);
+            }
         }
         uint32_t bits[32];
 #pragma unroll
