@@ -671,6 +671,7 @@ template <int D, int NT, int NW>
 __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) rows_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   RowSmem<D, NT, NW>& S = *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the tiles' kernel, if there is one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x;
   const long long share = P.header->share;

@@ -698,6 +698,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)c.misc[0];
+  // launched as a programmatic dependent of rows_kernel, which waited for the plan
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Work work{P.header->n_tiles, P.header->pieces};
   if (warp < W_DQ) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
@@ -733,8 +735,17 @@ static int launch_one(const Params& P, cudaStream_t st) {
   if (cudaFuncGetAttributes(&a, tiles_kernel<D, SPLIT>) != cudaSuccess || a.numRegs != LAUNCH_REGS) return DSA_ERR_CUDA;
   if (cudaFuncSetAttribute(tiles_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  tiles_kernel<D, SPLIT><<<P.n_ctas, TILE_THREADS, smem, st>>>(P);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)P.n_ctas);
+  cfg.blockDim = dim3(TILE_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, SPLIT>, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 // The kernel that can split a tile's blocks is a copy of its own: with the joining in it,
