@@ -75,7 +75,8 @@
  * following with nothing enqueued:
  *   - DSA_ERR_INVALID_ARG: a bad size or parameter, a null or misaligned pointer;
  *   - DSA_ERR_UNSUPPORTED_SHAPE: d, page_size, h_kv, h_q / h_kv, n_req or a product of sizes
- *     not served (attention: n_tokens * h_q / h_kv < 2^31);
+ *     not served (attention: n_tokens * h_q / h_kv < 2^31; a window above 2^30 only with
+ *     table_cols * page_size <= 2^30);
  *   - DSA_ERR_WORKSPACE_TOO_SMALL (attention);
  *   - DSA_ERR_UNSUPPORTED_DEVICE: not compute capability 10.3;
  *   - DSA_ERR_CUDA.

@@ -175,6 +175,15 @@ def test_prefill_and_mixed_batches(d, page, dtype, h, g, window):
     _check(Case(d + g + window, PREFILL, h=h, g=g, d=d, page=page, dtype=dtype, window=window))
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 5000])
+def test_windows_wider_than_every_context(window):
+    # (3, 2) and (70, 60): queries at negative positions, whose window would begin before -2^31
+    for lens in ([(1, 40), (3, 2), (2, 90)], [(70, 60), (130, 400)]):
+        c, e = Case(32, lens, h=1, g=4, page=16, window=window), Case(32, lens, h=1, g=4, page=16)
+        a, b = _check(c), _check(e)
+        assert torch.equal(a[0][1:-2], b[0][1:-2]) and torch.equal(a[1], b[1])
+
+
 def test_groups_of_many_heads_in_prefill():
     _check(Case(3, [(9, 30), (33, 100)], h=1, g=16, page=16))
     _check(Case(4, [(3, 30), (5, 100)], h=1, g=128, d=64, page=32, dtype="fp16"))

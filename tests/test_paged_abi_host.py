@@ -54,7 +54,7 @@ def test_insert(lib):
                 dict(slots=FAKE + 4), dict(status=FAKE + 2), dict(kp=None), dict(vs=None), dict(kp=FAKE + 8),
                 dict(ks=FAKE + 2)):
         assert call(**bad) == BAD, bad
-    for shape in (dict(d=96), dict(d=256), dict(page=48), dict(page=256), dict(page=8), dict(h=1025)):
+    for shape in (dict(d=96), dict(d=256), dict(page=48), dict(page=256), dict(page=8), dict(h=1025), dict(pages=1 << 23)):
         assert call(**shape) == SHAPE, shape
     assert call(n=0, k=None, v=None, slots=None, kp=None) == OK      # an empty batch is a no-op
     for ok in (dict(), dict(h=1, k_hd=0, v_hd=0), dict(pages=0, kp=None, vp=None, ks=None, vs=None),
@@ -91,8 +91,9 @@ def test_attention(lib):
         assert call(_params(lib, **bad)) == BAD, bad
         assert lib.dsa_kv8_attn_workspace_size(ctypes.byref(_params(lib, **bad)), 152) == 0
     for shape in (dict(d=96), dict(page_size=48), dict(n_req=8193), dict(h_kv=2048, h_q=2048), dict(h_q=129 * 8),
-                  dict(n_tokens=1 << 30)):
-        assert call(_params(lib, **shape)) == SHAPE, shape
+                  dict(n_tokens=1 << 30), dict(n_pages=1 << 23), dict(window=(1 << 30) + 1, table_cols=1 << 25)):
+        assert call(_params(lib, **shape), ld=1 << 25) == SHAPE, shape
+    assert call(_params(lib, window=(1 << 31) - 1)) in NO_GPU
     for bad in (dict(q=None), dict(out=None), dict(cu=None), dict(kv=None), dict(table=None), dict(kp=None), dict(vs=None),
                 dict(q=FAKE + 8), dict(out=FAKE + 4), dict(kp=FAKE + 8), dict(q_ld=8196), dict(q_hd=64), dict(out_hd=132),
                 dict(out_ld=64), dict(ld=15), dict(ws=None), dict(ws=FAKE + 16), dict(lse=FAKE + 2)):

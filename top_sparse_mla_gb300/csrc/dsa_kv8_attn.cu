@@ -723,7 +723,8 @@ static int check(const dsa_kv8_params* p) {
       (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) ||
       p->n_req > DSA_KV8_MAX_REQ || p->h_kv > DSA_KV8_MAX_HEADS || p->h_q / p->h_kv > DSA_KV8_MAX_GROUP ||
       (long long)p->n_tokens * (p->h_q / p->h_kv) >= (1LL << 31) ||
-      (long long)p->n_pages * p->h_kv * p->page_size >= (1LL << 32) - 1)   // rows of a pool are numbered in 32 bits
+      (long long)p->n_pages * p->h_kv * p->page_size >= (1LL << 32) - 1 ||   // rows of a pool are numbered in 32 bits
+      (p->window > (1 << 30) && (long long)p->table_cols * p->page_size > (1LL << 30)))
     return DSA_ERR_UNSUPPORTED_SHAPE;
   return DSA_OK;
 }
@@ -912,7 +913,9 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   const long long cap = (long long)p->table_cols * p->page_size, most = (1LL << 31) - 1024;
   P.cap = (int)(cap < most ? cap : most);
   P.max_q_len = p->max_q_len;
-  P.window = p->window;
+  // a window that nothing passes is none; others stay where a position minus the window
+  // (at least -2^30 minus 2^30) is an int
+  P.window = p->window < P.cap ? p->window : 0;
   P.fp16 = p->type == DSA_KV8_FP16;
   P.small_rows = 8 * row_tiles(p);
   P.n_shares = L.n_shares;
