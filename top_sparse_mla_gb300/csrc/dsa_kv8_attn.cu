@@ -232,6 +232,7 @@ struct Steps {
   const Params& P;
   const int32_t* table;
   int head, lo, hi, first, end, stride;
+  const uint8_t *k_lane, *v_lane;   // the pools at the lane's place in a step
   Codes<D> C;
   int page, raw_next;   // the first step's page, the entry of the one behind it
   float ks, vs;
@@ -241,13 +242,13 @@ struct Steps {
     return (s < end && base < hi) ? __ldg(table + (base >> P.page_shift)) : -1;
   }
   __device__ __forceinline__ int valid(int raw) const { return (raw < 0 || raw >= P.n_pages) ? -1 : raw; }
-  __device__ __forceinline__ long long row_of(int page_, int s) const {
-    return (((long long)page_ * P.h_kv + head) << P.page_shift) + ((lo + s * STEP) & ((1 << P.page_shift) - 1));
+  // first row of a step in the pools
+  __device__ __forceinline__ uint32_t row_of(int page_, int s) const {
+    return (((uint32_t)page_ * P.h_kv + head) << P.page_shift) + ((lo + s * STEP) & ((1 << P.page_shift) - 1));
   }
   __device__ __forceinline__ void load_k(int page_, int s) {
     if (page_ < 0) return;
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const uint8_t* k = P.k_pool + (row_of(page_, s) + r) * D + 16 * c;
+    const uint8_t* k = k_lane + (uint64_t)row_of(page_, s) * D;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       C.k[0][j] = dsa::ldg_nc(k + 64 * j);
@@ -256,8 +257,7 @@ struct Steps {
   }
   __device__ __forceinline__ void load_v(int page_, int s) {
     if (page_ < 0) return;
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const uint8_t* v = P.v_pool + (row_of(page_, s) + 2 * c) * D + r * (D / 8);
+    const uint8_t* v = v_lane + (uint64_t)row_of(page_, s) * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint8_t* at = v + ((i & 1) + (i >> 1) * 8) * D;
@@ -270,7 +270,7 @@ struct Steps {
     }
   }
   __device__ __forceinline__ float load_scale(const float* scale, int page_) const {
-    return page_ < 0 ? 1.0f : __ldg(scale + (long long)page_ * P.h_kv + head);
+    return page_ < 0 ? 1.0f : __ldg(scale + (uint64_t)((uint32_t)page_ * P.h_kv + head));
   }
   // two parts, so that the queries can be fetched between them
   __device__ __forceinline__ void begin() {
@@ -338,7 +338,9 @@ __device__ __forceinline__ void rows_steps(const Params& P, Steps<D>& W, int see
       W.load_k(page_next, s + stride);
       // t = x + log2(v_scale), masked
       const float vsc = bounded_scale(vs);
-      const float bias = log2f(vsc), vinv = 1.0f / vsc;
+      float bias, vinv;   // 2^-22 relative, as the exponential
+      asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(bias) : "f"(vsc));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(vinv) : "f"(vsc));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -452,7 +454,8 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
   const int pos_min = pos0 + row0 / P.group, pos_max = pos0 + min(row0 + R8 - 1, rows - 1) / P.group;
   const int hi = min(pos_max + 1, a.kv);
   const int seen_lo = P.window > 0 ? max(pos_min - P.window + 1, 0) : 0;
-  Steps<D> W{P, P.table + req * P.table_ld, head, sp.lo, hi, step0 + w, step1, NW};
+  Steps<D> W{P, P.table + req * P.table_ld, head, sp.lo, hi, step0 + w, step1, NW,
+             P.k_pool + r * D + 16 * c, P.v_pool + 2 * c * D + r * (D / 8)};
   W.begin();
 
   // queries: fp16 after a scaling of each row by a power of two that brings its largest
