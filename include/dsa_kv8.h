@@ -55,7 +55,8 @@
  *   block_table  int32 [n_req][table_cols], row pitch table_ld
  *   cu_q         int32 [n_req + 1], ascending, within [0, n_tokens] (values outside are
  *                taken as the nearest bound)
- *   kv_lens      int32 [n_req]; at most table_cols * page_size is read
+ *   kv_lens      int32 [n_req] (values outside [0, table_cols * page_size] are taken as the
+ *                nearest bound, the queries' positions with them)
  *   lse          fp32 [n_tokens][h_q] or NULL
  *   max_q_len    no request has more query rows (a request that does is skipped, its rows
  *                unwritten, and the call's status gets DSA_STATUS_QUERY_TOO_LONG); it

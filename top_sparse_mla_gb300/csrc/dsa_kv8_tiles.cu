@@ -37,7 +37,9 @@ constexpr int W_DQ = 8, W_MMA = 12, W_COPY = 13, TILE_THREADS = 16 * 32;   // wa
 // is what 16 warps of 128 were launched with.
 constexpr int LAUNCH_REGS = 128, SOFTMAX_REGS = 152, OTHER_REGS = 104;
 static_assert(SOFTMAX_REGS + OTHER_REGS == 2 * LAUNCH_REGS, "more registers than the CTA has would be waited for");
-constexpr unsigned long long WAIT_LIMIT_CYCLES = 4000000000ull;   // ~2 s at 2 GHz
+// ~10 s at 2 GHz: the group of a half that a CTA's units do not have waits through them,
+// which with contexts of a million tokens may be hundreds of milliseconds
+constexpr unsigned long long WAIT_LIMIT_CYCLES = 20000000000ull;
 
 // barriers
 enum {
@@ -238,7 +240,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, const Work& work) {
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
       for (uint32_t b = g > 0 ? g - 1 : 0; b <= g; ++b)
-        while (!mbar_wait_susp(bar(c, B_RAWFULL + kv), b & 1) && clock64() - start < WAIT_LIMIT_CYCLES / 4) {
+        while (!mbar_wait_susp(bar(c, B_RAWFULL + kv), b & 1) && clock64() - start < WAIT_LIMIT_CYCLES / 8) {
         }
   }
 }
