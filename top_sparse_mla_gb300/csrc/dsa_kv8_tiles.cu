@@ -139,7 +139,7 @@ DSA_DEV bool unit(const Params& P, long long round, const Work& work, Unit& x) {
   x.head = rest - x.piece * P.h_kv;
   x.index = i * P.h_kv + x.head;
   const int4* at = reinterpret_cast<const int4*>(P.tiles + i);
-  const int4 a = __ldg(at), b = __ldg(at + 1);
+  const int4 a = __ldcg(at), b = __ldcg(at + 1);   // not __ldg: written while this kernel may be there already
   x.t.req = a.x; x.t.row0 = a.y; x.t.q0 = a.z; x.t.rows = a.w;
   x.t.pos0 = b.x; x.t.lo = b.y; x.t.hi = b.z;
 #pragma unroll
@@ -390,6 +390,54 @@ DSA_DEV float max3(float a, float b, float c) {
   return r;
 }
 
+DSA_DEV const uint16_t* shfl_ptr(const uint16_t* p, int from) {
+  return reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(p), from));
+}
+
+// Scales the warp's 32 rows of queries to fp16 and writes them into a half's tile.  `mine`
+// is this lane's row, null for one that is not there, and `row0` the warp's first row of
+// the tile.  Returns what undoes the scaling of this lane's row.  Lanes side by side read
+// neighbours of a row: a lane for a row touches 32 lines with every load, which took a
+// 2123-token prefill 109 us in place of 104.
+template <int D, bool FP16>
+DSA_DEV float queries(const uint16_t* mine, uint32_t tile, int row0) {
+  constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;   // lanes of a row, rows of a load; LANES loads
+  const int lane = threadIdx.x & 31, sub = lane / LANES, chunk = lane % LANES;
+  uint4 v[LANES];
+#pragma unroll
+  for (int t = 0; t < LANES; ++t) {
+    const uint16_t* src = shfl_ptr(mine, AT_ONCE * t + sub);
+    v[t] = src ? ldg_nc(src + 8 * chunk) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // largest magnitudes, as 16-bit patterns in pairs: lane l ends with those of load l % LANES
+  uint32_t mx[LANES];
+#pragma unroll
+  for (int t = 0; t < LANES; ++t)
+    mx[t] = __vmaxu2(__vmaxu2(v[t].x & 0x7FFF7FFFu, v[t].y & 0x7FFF7FFFu), __vmaxu2(v[t].z & 0x7FFF7FFFu, v[t].w & 0x7FFF7FFFu));
+#pragma unroll
+  for (int n = LANES / 2; n >= 1; n >>= 1)
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const bool high = lane & n;
+      mx[j] = __vmaxu2(high ? mx[j + n] : mx[j], __shfl_xor_sync(0xFFFFFFFFu, high ? mx[j] : mx[j + n], n));
+    }
+  float back;
+  const float down = row_scaling(unpack(max(mx[0] >> 16, mx[0] & 0xFFFFu), FP16).x, back);
+  const uint32_t at = tile + (chunk >> 3) * (BLOCK * 128) + (row0 + sub) * 128;
+#pragma unroll
+  for (int t = 0; t < LANES; ++t) {
+    const float f = __shfl_sync(0xFFFFFFFFu, down, sub * LANES + t);
+    uint32_t p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 y = unpack(word(v[t], e), FP16);
+      p[e] = pack_f16x2(y.x * f, y.y * f);
+    }
+    sts128(at + AT_ONCE * t * 128 + (((chunk ^ (AT_ONCE * t + sub)) & 7) << 4), make_uint4(p[0], p[1], p[2], p[3]));
+  }
+  return __shfl_sync(0xFFFFFFFFu, back, lane / AT_ONCE + lane % AT_ONCE * LANES);
+}
+
 template <int D, bool SPLIT>
 DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& work, int h) {
   using SM = TileSmem<D>;
@@ -414,30 +462,9 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
     // ---- the query row (its buffer was last read for this half's last scores)
     float row_scale = 1.0f;
     if (!SPLIT || mine > 0) {
-      const uint16_t* src = P.q + (x.t.q0 + qi) * P.q_ld + head * P.q_hd;
-      uint4 v[D / 8];
-      float mx = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) v[k] = live ? ldg_nc(src + 8 * k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack(word(v[k], e), P.fp16);
-          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      const float down = row_scaling(mx, row_scale);
-      const uint32_t base = c.sb + SM::Q + h * SM::OPERAND + row_in * 128;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        uint32_t p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack(word(v[k], e), P.fp16);
-          p[e] = pack_f16x2(f.x * down, f.y * down);
-        }
-        sts128(base + (k >> 3) * SM::PANEL + (((k & 7) ^ (row_in & 7)) << 4), make_uint4(p[0], p[1], p[2], p[3]));
-      }
+      const uint16_t* src = live ? P.q + (x.t.q0 + qi) * P.q_ld + head * P.q_hd : nullptr;
+      const uint32_t tile = c.sb + SM::Q + h * SM::OPERAND;
+      row_scale = P.fp16 ? queries<D, true>(src, tile, row_in & ~31) : queries<D, false>(src, tile, row_in & ~31);
       fence_async_smem();
       tc_fence_before();   // this half's O was read before
       arrive_w(c, B_QFULL + h);
@@ -507,13 +534,13 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
               if (i > 0) {
                 // the product of the block before is done: these scores were issued after it
 #pragma unroll 1
-                for (int k = 0; k < D; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(to + k, o);
+                for (int k = 0; k < D; k += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(to + k, o);
                   tc_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st16(to + k, o);
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st32(to + k, o);
                 }
               }
               if (s == 1) {   // the weights of the block's first part
