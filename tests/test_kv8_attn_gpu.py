@@ -204,6 +204,26 @@ def test_many_requests():
                 dtype="fp16"))
 
 
+@pytest.mark.parametrize("n", [127, 128, 129, 512, 513])
+@pytest.mark.parametrize("kw", [dict(h=1, g=2, d=128), dict(h=3, g=12, d=64)])
+def test_batches_at_the_sizes_where_the_shares_are_found_otherwise(n, kw):
+    rng = np.random.default_rng(n)
+    _check(Case(n, [(int(a), int(b)) for a, b in zip(rng.integers(0, 3, n), rng.integers(0, 50, n))], page=16, **kw))
+
+
+@pytest.mark.parametrize("lens,h,g", [
+    ([(1, 30000)], 1, 4),                       # all CTAs on one unit, joined in two levels
+    ([(1, 6000), (0, 10), (1, 5), (1, 2500)], 2, 8),
+    ([(2, 9000), (1, 700)], 3, 8),
+    ([(4, 5000), (3, 5001)], 4, 8),
+    ([(1, 300 + 7 * i) for i in range(38)], 2, 2),   # two CTAs a unit, on 152
+    ([(1, 300 + 7 * i) for i in range(39)], 2, 2),
+])
+def test_few_units_shared_by_wide_ctas(lens, h, g):
+    _check(Case(40, lens, h=h, g=g, page=64))
+    _check(Case(41, lens, h=h, g=g, page=16, window=900, dtype="fp16"))
+
+
 @pytest.mark.parametrize("kw", [
     dict(v_scale=[2.0 ** -64, 2.0 ** -40]), dict(v_scale=[2.0 ** 40, 2.0 ** 39]), dict(v_scale=[2.0 ** -30, 1.0, 2.0 ** 10]),
     dict(q_mag=2.0 ** 60, k_mag=2.0 ** -60), dict(q_mag=2.0 ** -60, k_mag=2.0 ** 60), dict(q_mag=30.0), dict(scale=-0.1),

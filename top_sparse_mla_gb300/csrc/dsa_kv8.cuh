@@ -54,6 +54,8 @@ struct Params {
   int* tile_arrived;     // by unit and half
   int n_tokens, n_req, h_q, h_kv, group, n_pages, page_shift, cap, max_q_len, window, fp16;
   int small_rows;   // requests with at most this many rows go to rows_kernel
+  int unit_steps, min_share;   // what a unit costs a CTA beside its steps, and a CTA's least share, in steps
+  int own_plan;     // whether rows_kernel's CTAs find their shares for themselves
   int n_shares, max_tiles, n_ctas;   // n_ctas: of the tiles' kernel
   int tile_split;   // whether a tile's blocks may be cut into pieces
   float scale_log2;   // softmax_scale * log2 e

@@ -19,43 +19,74 @@ namespace dsa_kv8 {
 
 constexpr int MAX_ROWS = 32;      // most query rows of a request in rows_kernel
 constexpr int ROW_WARPS = 4;      // warps of a rows_kernel CTA
-constexpr int UNIT_STEPS = 8;     // what a unit (request, KV head) costs a CTA beside its steps, in steps
-constexpr int MIN_SHARE = UNIT_STEPS + 8;   // a CTA's least share: a unit's beginning and two steps a warp
-constexpr int JOIN = 16;          // partial results that one CTA joins at a time
+constexpr int UNIT_STEPS = 2;     // what a unit (request, KV head) costs a CTA beside its steps, in steps of every warp
+constexpr int MIN_STEPS = 2;      // the fewest steps of a warp that are worth a unit's beginning
 constexpr int PLAN_THREADS = 1024;
+constexpr int FEW_THREADS = 256;  // of the plan, where rows_kernel's CTAs find their shares
 // rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
 constexpr int ctas_per_sm(int d, int nt) { return (nt == 1 ? 4 : nt == 2 ? 3 : 2) + (d == 64 ? (nt == 1 ? 2 : 1) : 0); }
 constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
 
+// the steps of each of a request's units with what a unit costs beside them; 0 for a
+// request that is not rows_kernel's
+__device__ __forceinline__ int unit_steps(const Params& P, const Request& a) {
+  const bool ours = a.q_len > 0 && a.q_len <= P.max_q_len && a.rows(P) <= P.small_rows;
+  return ours ? P.unit_steps + span(P, a, 0, a.q_len - 1).steps : 0;
+}
+__device__ __forceinline__ long long share_of(const Params& P, long long total) {
+  return max((total + P.n_shares - 1) / P.n_shares, (long long)P.min_share);
+}
+// where among its units the share with `rest` steps of request r in front of it begins
+__device__ __forceinline__ Share share_at(const Params& P, int r, long long rest, long long steps) {
+  Share s;
+  s.req = r;
+  s.head = (int)(rest / steps);
+  s.step = rest - s.head * steps - P.unit_steps;
+  return s;
+}
+
 // ------------------------------------------------------------------------------ plan
-// The steps of the small requests, all heads of all requests in a row and UNIT_STEPS more
+// The steps of the small requests, all heads of all requests in a row and P.unit_steps more
 // in front of each unit's for its beginning and end, are cut into equal shares, one for
 // each CTA: a share may begin and end inside a unit, and the CTAs are done at the same time
 // whatever the lengths.  The tiles of the other requests are listed.
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params P) {
+//
+// Of few requests (P.own_plan) every CTA of rows_kernel finds its share for itself while
+// this kernel, for the counters and the tiles, is still on its way.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ Params P) {
   extern __shared__ long long s_step[];   // [n_req + 1] exclusive prefix of the steps
   long long* s_tile = s_step + P.n_req + 1;   // [n_req + 1] of the tiles
-  __shared__ long long s_step_warp[32], s_tile_warp[32];
-  __shared__ int s_place[PLAN_THREADS];
+  __shared__ long long s_step_warp[THREADS / 32], s_tile_warp[THREADS / 32];
+  __shared__ int s_place[THREADS];
   __shared__ uint32_t s_bad;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = P.n_req;
   if (tid == 0) s_bad = 0;
+  for (int b = tid; b < 3 * P.n_shares; b += THREADS) P.arrived[b] = 0;
   __syncthreads();
-  for (int r = tid; r < n; r += PLAN_THREADS) {
+  if (P.own_plan && !P.tile_arrived) {   // no shares and no tiles to find
+    for (int r = tid; r < n; r += THREADS)
+      if (request(P, r).q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
+    __syncthreads();
+    if (tid == 0) {
+      P.header->status = s_bad;
+      P.header->n_tiles = 0;
+    }
+    return;
+  }
+  for (int r = tid; r < n; r += THREADS) {
     const Request a = request(P, r);
     const int rows = a.rows(P);
-    long long steps = 0;
     int tiles = 0;
     if (a.q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
     else if (rows > P.small_rows) tiles = (rows + TILE_ROWS - 1) / TILE_ROWS;
-    else if (rows > 0) steps = UNIT_STEPS + span(P, a, 0, a.q_len - 1).steps;
-    s_step[r] = steps;
+    s_step[r] = unit_steps(P, a);
     s_tile[r] = tiles;
   }
   __syncthreads();
-  const int per = ((n + PLAN_THREADS - 1) / PLAN_THREADS) | 1;   // odd: no bank conflicts
+  const int per = ((n + THREADS - 1) / THREADS) | 1;   // odd: no bank conflicts
   const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
   long long st = 0, ti = 0;
   for (int r = r0; r < r1; ++r) {
@@ -78,7 +109,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   __syncthreads();
   long long st_ex = st_in - st, ti_ex = ti_in - ti, all = 0, all_tiles = 0;
 #pragma unroll
-  for (int u = 0; u < 32; ++u) {
+  for (int u = 0; u < THREADS / 32; ++u) {
     if (u < w) {
       st_ex += s_step_warp[u];
       ti_ex += s_tile_warp[u];
@@ -100,14 +131,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
   __syncthreads();
 
   const long long total = all * P.h_kv;
-  const long long share = max((total + P.n_shares - 1) / P.n_shares, (long long)MIN_SHARE);
+  const long long share = share_of(P, total);
   if (P.tile_arrived)
-    for (int i = tid; i < 2 * P.n_ctas; i += PLAN_THREADS) P.tile_arrived[i] = 0;
-  for (int b = tid; b < P.n_shares; b += PLAN_THREADS) {
-    Share s;
-    s.req = -1;
-    s.head = 0;
-    s.step = 0;
+    for (int i = tid; i < 2 * P.n_ctas; i += THREADS) P.tile_arrived[i] = 0;
+  // few requests: the CTAs find them for themselves
+  for (int b = tid; b < (P.own_plan ? 0 : P.n_shares); b += THREADS) {
+    Share s{-1, 0, 0};
     const long long f = b * share;
     if (f < total) {
       int lo = 0, hi = n;   // the request with s_step[lo] * h_kv <= f < s_step[lo + 1] * h_kv
@@ -115,19 +144,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
         const int mid = (lo + hi) >> 1;
         if (s_step[mid] * P.h_kv <= f) lo = mid; else hi = mid;
       }
-      const long long steps = s_step[lo + 1] - s_step[lo], rest = f - s_step[lo] * P.h_kv;
-      s.req = lo;
-      s.head = (int)(rest / steps);
-      s.step = rest - s.head * steps - UNIT_STEPS;
+      s = share_at(P, lo, f - s_step[lo] * P.h_kv, s_step[lo + 1] - s_step[lo]);
     }
     P.shares[b] = s;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) P.arrived[3 * b + i] = 0;
   }
   // ascending cu_q cannot give more tiles than the list has room for
   const int n_tiles = (int)min(all_tiles, (long long)P.max_tiles);
   if (n_tiles > 0) {
-    // the longest first (by cached tokens in blocks of 128, all above 1023 alike): a count
+    // the longest first (by cached tokens in blocks of 128, all above THREADS - 1 alike): a count
     // of each length, the places behind the longer ones, then the tiles.  The order among
     // equal ones changes no result.
     auto tile = [&](int i) {
@@ -149,10 +173,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       t.pad = 0;
       return t;
     };
-    auto length = [](const Tile& t) { return PLAN_THREADS - 1 - min(max(t.hi - t.lo, 0) / 128, PLAN_THREADS - 1); };
+    auto length = [](const Tile& t) { return THREADS - 1 - min(max(t.hi - t.lo, 0) / 128, THREADS - 1); };
     s_place[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < n_tiles; i += PLAN_THREADS) atomicAdd(&s_place[length(tile(i))], 1);
+    for (int i = tid; i < n_tiles; i += THREADS) atomicAdd(&s_place[length(tile(i))], 1);
     __syncthreads();
     const int count = s_place[tid];
     int before = count;
@@ -167,7 +191,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     for (int v = 0; v < w; ++v) before += (int)s_step_warp[v];
     s_place[tid] = before;
     __syncthreads();
-    for (int i = tid; i < n_tiles; i += PLAN_THREADS) {
+    for (int i = tid; i < n_tiles; i += THREADS) {
       const Tile t = tile(i);
       P.tiles[atomicAdd(&s_place[length(t)], 1)] = t;
     }
@@ -430,7 +454,11 @@ struct RowSmem {
   uint16_t q[NT == 1 ? 8 : 8 * NT * (D + 8)];
   float q_scale[8 * NT];
   int last;
+  Share share;
+  long long scan[NW], share_steps;
 };
+
+__device__ __forceinline__ void wait_for_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Steps [step0, step1) of one unit by the whole CTA, joined over its warps.  Rows
 // [row0, row0 + 8 NT) of the request.  The unit is in `pieces`, which CTAs first_cta,
@@ -447,6 +475,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
                                           int piece) {
   constexpr int R8 = 8 * NT;
   constexpr int PSIZE = R8 * D + 2 * R8;   // floats of one partial result
+  constexpr int JOIN = NW > ROW_WARPS ? 32 : 16;   // partial results that one CTA joins at a time
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, r = lane >> 2, c = lane & 3;
   const int rows = a.rows(P);
   const int pos0 = a.kv - a.q_len;
@@ -661,6 +690,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
       if (last) __threadfence();
       return last;
     };
+    wait_for_plan();   // it sets the counters
     const int groups = (pieces + JOIN - 1) / JOIN, lead = piece / JOIN * JOIN;
     if (arrive(P.arrived + 3 * (first_cta + lead) + (lead == 0 ? 1 : 0), min(JOIN, pieces - lead))) {
       join(lead, 1, min(JOIN, pieces - lead), 0, groups > 1 ? buffer(lead, 1) : nullptr);
@@ -670,15 +700,47 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
   __syncthreads();   // the shared memory is used again
 }
 
+// This CTA's share, and in share_steps the steps of each share: what the plan kernel computes, for at
+// most as many requests as the CTA has threads.
 template <int D, int NT, int NW>
-__global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) rows_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  RowSmem<D, NT, NW>& S = *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the tiles' kernel, if there is one
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ Share own_share(const Params& P, RowSmem<D, NT, NW>& S, int b) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const long long steps = tid < P.n_req ? unit_steps(P, request(P, tid)) : 0;
+  if (tid == 0) S.share = Share{-1, 0, 0};
+  long long in = steps;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, in, o);
+    if (lane >= o) in += v;
+  }
+  if (lane == 31) S.scan[w] = in;
+  __syncthreads();
+  long long before = in - steps, all = 0;
+#pragma unroll
+  for (int u = 0; u < NW; ++u) {
+    if (u < w) before += S.scan[u];
+    all += S.scan[u];
+  }
+  const long long share = share_of(P, all * P.h_kv), f = b * share;
+  if (before * P.h_kv <= f && f < (before + steps) * P.h_kv) S.share = share_at(P, tid, f - before * P.h_kv, steps);
+  if (tid == 0) S.share_steps = share;
+  __syncthreads();
+  return S.share;
+}
+
+template <int D, int NT, int NW>
+__device__ __forceinline__ void rows_share(const Params& P, RowSmem<D, NT, NW>& S) {
   const int b = blockIdx.x;
-  const long long share = P.header->share;
-  const Share at = P.shares[b];
+  Share at;
+  long long share;
+  if (P.own_plan) {
+    at = own_share(P, S, b);
+    share = S.share_steps;
+  } else {
+    wait_for_plan();
+    at = P.shares[b];
+    share = P.header->share;
+  }
   int req = at.req, head = at.head;
   if (req < 0) return;
   long long step = at.step, left = share;   // step: of the unit, below 0 in its beginning
@@ -700,8 +762,8 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) rows_kernel(const
     }
     left -= min(left, sp.steps - step);
     if (left == 0) return;
-    unit += sp.steps + UNIT_STEPS;
-    step = -UNIT_STEPS;
+    unit += sp.steps + P.unit_steps;
+    step = -P.unit_steps;
     if (++head < P.h_kv) continue;
     head = 0;
     if (++req >= P.n_req) return;
@@ -712,6 +774,14 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) rows_kernel(const
     }
     sp = span(P, a, 0, a.q_len - 1);
   }
+}
+
+template <int D, int NT, int NW>
+__global__ void __launch_bounds__(32 * NW, NW > ROW_WARPS ? 1 : ctas_per_sm(D, NT)) rows_kernel(const __grid_constant__ Params P) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the tiles' kernel, if there is one
+  rows_share<D, NT, NW>(P, *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw));
+  wait_for_plan();   // what waits for this kernel needs the plan
 }
 
 // ------------------------------------------------------------------------------ host
@@ -745,6 +815,17 @@ static bool has_tiles(const dsa_kv8_params* p) {
   return (long long)p->max_q_len * (p->h_q / p->h_kv) > 8 * row_tiles(p);
 }
 
+// Whether a CTA of rows_kernel has all the warps that an SM holds, or four of them.  With
+// few units, which many CTAs share, wider CTAs leave fewer pieces to join.  Heads of 128, us,
+// wide and not: 4 requests of up to 8k tokens, 64/8 heads, 15.2 and 17.3; 8 such 18.7 and
+// 22.2; 2 of up to 32k, 32/8 heads, 4 queries, 34.3 and 37.0; one of 512 tokens, 8/1 heads,
+// 8.4 and 9.5; but 16 of up to 2k (128 units) 16.0 and 14.3, and one of 16 tokens 9.8 and 8.0.
+// Heads of 64 (24 warps): 12 of up to 4k tokens, 16/4 heads, 14.2 and 11.5.
+static bool wide(const dsa_kv8_params* p, int sms) {
+  const long long units = (long long)p->n_req * p->h_kv, most = (long long)p->table_cols * p->page_size;
+  return p->d == 128 && 2 * units <= sms && most >= 256;
+}
+
 struct Layout {
   int n_shares, max_tiles;
   size_t shares, arrived, tiles, partial, tile_arrived, tile_partial, bytes;
@@ -755,7 +836,7 @@ static size_t up(size_t x) { return (x + 255) / 256 * 256; }
 static Layout layout(const dsa_kv8_params* p, int sms) {
   Layout L;
   const size_t group = p->h_q / p->h_kv, rows = 8 * (size_t)row_tiles(p);
-  L.n_shares = ctas_per_sm(p->d, row_tiles(p)) * sms;
+  L.n_shares = wide(p, sms) ? sms : ctas_per_sm(p->d, row_tiles(p)) * sms;
   size_t at = 256;
   L.shares = at;
   at += up(L.n_shares * sizeof(Share));
@@ -794,22 +875,19 @@ static int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st,
   return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
+template <int D, int NT>
+static int launch_rows(const Params& P, bool wide, cudaStream_t st) {
+  constexpr int W = ROW_WARPS, WW = D == 128 ? W * ctas_per_sm(D, NT) : W;
+  return wide ? launch(rows_kernel<D, NT, WW>, P.n_shares, 32 * WW, sizeof(RowSmem<D, NT, WW>), st, P, true)
+              : launch(rows_kernel<D, NT, W>, P.n_shares, 32 * W, sizeof(RowSmem<D, NT, W>), st, P, true);
+}
+
 template <int D>
-static int launch_all(const dsa_kv8_params* p, const Params& P, cudaStream_t st) {
-  int rc;
-  switch (row_tiles(p)) {
-    case 1:
-      rc = launch(rows_kernel<D, 1, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 1, ROW_WARPS>), st, P, true);
-      break;
-    case 2:
-      rc = launch(rows_kernel<D, 2, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 2, ROW_WARPS>), st, P, true);
-      break;
-    default:
-      rc = launch(rows_kernel<D, 4, ROW_WARPS>, P.n_shares, 32 * ROW_WARPS, sizeof(RowSmem<D, 4, ROW_WARPS>), st, P, true);
-  }
+static int launch_all(const dsa_kv8_params* p, const Params& P, bool wide, cudaStream_t st) {
+  const int nt = row_tiles(p);
+  const int rc = nt == 1 ? launch_rows<D, 1>(P, wide, st) : nt == 2 ? launch_rows<D, 2>(P, wide, st) : launch_rows<D, 4>(P, wide, st);
   if (rc != DSA_OK) return rc;
-  if (has_tiles(p)) rc = launch_tiles(D, P, st);
-  return rc;
+  return has_tiles(p) ? launch_tiles(D, P, st) : DSA_OK;
 }
 
 }  // namespace dsa_kv8
@@ -922,12 +1000,18 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   P.fp16 = p->type == DSA_KV8_FP16;
   P.small_rows = 8 * row_tiles(p);
   P.n_shares = L.n_shares;
+  const bool is_wide = wide(p, sms);
+  const int warps = is_wide ? ROW_WARPS * ctas_per_sm(p->d, row_tiles(p)) : ROW_WARPS;
+  P.unit_steps = UNIT_STEPS * warps;
+  P.min_share = P.unit_steps + MIN_STEPS * warps;
+  P.own_plan = p->n_req <= 32 * warps;
   P.max_tiles = L.max_tiles;
   P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   const size_t smem = (size_t)(p->n_req + 1) * 2 * sizeof(long long);
-  const int rc1 = launch(plan_kernel, 1, PLAN_THREADS, smem, st, P, false);
+  const int rc1 = P.own_plan ? launch(plan_kernel<FEW_THREADS>, 1, FEW_THREADS, smem, st, P, false)
+                             : launch(plan_kernel<PLAN_THREADS>, 1, PLAN_THREADS, smem, st, P, false);
   if (rc1 != DSA_OK) return rc1;
-  return p->d == 128 ? launch_all<128>(p, P, st) : launch_all<64>(p, P, st);
+  return p->d == 128 ? launch_all<128>(p, P, is_wide, st) : launch_all<64>(p, P, is_wide, st);
 }
 
 }  // extern "C"
