@@ -224,6 +224,21 @@ def test_few_units_shared_by_wide_ctas(lens, h, g):
     _check(Case(41, lens, h=h, g=g, page=16, window=900, dtype="fp16"))
 
 
+# 12, 10, 8, 6, 4 and 2 CTAs for each tile and head, on 152
+@pytest.mark.parametrize("h,kw", [(h, dict(d=128, page=64)) for h in (1, 5, 7, 10, 16, 30)] +
+                         [(h, kw) for h in (2, 6) for kw in (dict(d=64, page=16, dtype="fp16"), dict(d=128, page=32, window=1700))])
+def test_a_few_tiles_whose_blocks_are_split_over_a_cluster(h, kw):
+    _check(Case(50 + h, [(33, 3101)], h=h, g=8, **kw))
+
+
+def test_split_tiles_with_halves_that_end_apart():
+    _check(Case(60, [(200, 700)], h=1, g=2, page=16))               # the halves' last blocks differ
+    _check(Case(61, [(17, 2000), (40, 41), (9, 9)], h=2, g=8))      # a half without rows; a tile too short to split
+    _check(Case(62, [(100, 0), (90, 60), (33, 2500)], h=1, g=8))    # rows that see nothing
+    _check(Case(63, [(256, 4000)], h=1, g=1, window=130, page=32))  # pieces that some rows do not see at all
+    _check(Case(64, [(250, 250), (3, 4000)], h=1, g=3, d=64, page=16))
+
+
 @pytest.mark.parametrize("kw", [
     dict(v_scale=[2.0 ** -64, 2.0 ** -40]), dict(v_scale=[2.0 ** 40, 2.0 ** 39]), dict(v_scale=[2.0 ** -30, 1.0, 2.0 ** 10]),
     dict(q_mag=2.0 ** 60, k_mag=2.0 ** -60), dict(q_mag=2.0 ** -60, k_mag=2.0 ** 60), dict(q_mag=30.0), dict(scale=-0.1),

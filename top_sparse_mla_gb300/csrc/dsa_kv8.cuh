@@ -14,7 +14,7 @@ namespace dsa_kv8 {
 
 constexpr int STEP = 16;          // cached tokens of one step of a warp; every page size is a multiple
 constexpr int TILE_ROWS = 256;    // query rows of a tile
-constexpr int MAX_PIECES = 16;    // of a tile's blocks
+constexpr int MAX_CLUSTER = 16;
 constexpr float LAG = 8.0f;       // how far, in powers of two, a running maximum may lag
 
 struct Share {   // where a CTA's share of the steps begins
@@ -34,7 +34,6 @@ struct Header {
   uint32_t status;
   int n_tiles;
   long long share;   // steps of every CTA
-  int pieces;        // most pieces that the blocks of a tile and head are cut into
 };
 
 struct Params {
@@ -50,14 +49,13 @@ struct Params {
   int* arrived;
   Tile* tiles;
   float* partial;
-  float* tile_partial;   // of a tile's half, by unit and piece: O [D / 4][128] float4, then m [128], l [128]
-  int* tile_arrived;     // by unit and half
   int n_tokens, n_req, h_q, h_kv, group, n_pages, page_shift, cap, max_q_len, window, fp16;
   int small_rows;   // requests with at most this many rows go to rows_kernel
   int unit_steps, min_share;   // what a unit costs a CTA beside its steps, and a CTA's least share, in steps
   int own_plan;     // whether rows_kernel's CTAs find their shares for themselves
   int n_shares, max_tiles, n_ctas;   // n_ctas: of the tiles' kernel
-  int tile_split;   // whether a tile's blocks may be cut into pieces
+  int has_tiles;    // whether requests may have more rows than rows_kernel takes
+  int cluster;      // CTAs that share a tile and KV head; 0: a CTA has several of them
   float scale_log2;   // softmax_scale * log2 e
 };
 
@@ -125,6 +123,9 @@ __device__ __forceinline__ float bounded_scale(float s) {
 }
 
 // dsa_kv8_tiles.cu: the tiles of the requests with more rows than rows_kernel takes
+// How many CTAs should share each of at most `units` pairs of a tile and a KV head, with at
+// most `blocks` blocks of 128 cached tokens: 0 for one CTA alone.
+int cluster_size(int d, long long units, int blocks);
 int launch_tiles(int d, const Params& P, cudaStream_t st);
 
 }  // namespace dsa_kv8

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   if (tid == 0) s_bad = 0;
   for (int b = tid; b < 3 * P.n_shares; b += THREADS) P.arrived[b] = 0;
   __syncthreads();
-  if (P.own_plan && !P.tile_arrived) {   // no shares and no tiles to find
+  if (P.own_plan && !P.has_tiles) {   // no shares and no tiles to find
     for (int r = tid; r < n; r += THREADS)
       if (request(P, r).q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
     __syncthreads();
@@ -132,8 +132,6 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
 
   const long long total = all * P.h_kv;
   const long long share = share_of(P, total);
-  if (P.tile_arrived)
-    for (int i = tid; i < 2 * P.n_ctas; i += THREADS) P.tile_arrived[i] = 0;
   // few requests: the CTAs find them for themselves
   for (int b = tid; b < (P.own_plan ? 0 : P.n_shares); b += THREADS) {
     Share s{-1, 0, 0};
@@ -199,9 +197,6 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   if (tid == 0) {
     P.header->status = s_bad;
     P.header->n_tiles = n_tiles;
-    // few units: their blocks are cut into pieces, so that every CTA has one
-    const long long units = (long long)n_tiles * P.h_kv;
-    P.header->pieces = units > 0 && P.tile_split ? (int)min(max(P.n_ctas / units, 1LL), (long long)MAX_PIECES) : 1;
     P.header->share = share;
   }
 }
@@ -828,7 +823,7 @@ static bool wide(const dsa_kv8_params* p, int sms) {
 
 struct Layout {
   int n_shares, max_tiles;
-  size_t shares, arrived, tiles, partial, tile_arrived, tile_partial, bytes;
+  size_t shares, arrived, tiles, partial, bytes;
 };
 
 static size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -843,17 +838,10 @@ static Layout layout(const dsa_kv8_params* p, int sms) {
   L.arrived = at;
   at += up(L.n_shares * 3 * sizeof(int));
   L.tiles = at;
-  L.max_tiles = (int)(p->n_tokens * group / TILE_ROWS + p->n_req);
+  L.max_tiles = (int)((p->n_tokens * group + (TILE_ROWS - 1) * (size_t)p->n_req) / TILE_ROWS);   // ascending cu_q cannot give more
   at += up((size_t)L.max_tiles * sizeof(Tile));
   L.partial = at;
   at += up((size_t)L.n_shares * 4 * (rows * p->d + 2 * rows) * sizeof(float));
-  L.tile_arrived = L.tile_partial = 0;   // no tiles
-  if (has_tiles(p)) {
-    L.tile_arrived = at;
-    at += up((size_t)2 * sms * sizeof(int));
-    L.tile_partial = at;
-    at += up((size_t)sms * 2 * 128 * (p->d + 2) * sizeof(float));
-  }
   L.bytes = at;
   return L;
 }
@@ -978,11 +966,6 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   P.arrived = reinterpret_cast<int*>(ws + L.arrived);
   P.tiles = reinterpret_cast<Tile*>(ws + L.tiles);
   P.partial = reinterpret_cast<float*>(ws + L.partial);
-  P.tile_arrived = L.tile_arrived ? reinterpret_cast<int*>(ws + L.tile_arrived) : nullptr;
-  P.tile_partial = L.tile_partial ? reinterpret_cast<float*>(ws + L.tile_partial) : nullptr;
-  P.n_ctas = sms;
-  // where even the most tiles that these sizes allow leave half of the CTAs without one
-  P.tile_split = 2LL * L.max_tiles * p->h_kv <= sms;
   P.n_tokens = p->n_tokens;
   P.n_req = p->n_req;
   P.h_q = p->h_q;
@@ -998,6 +981,12 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   // (at least -2^30 minus 2^30) is an int
   P.window = p->window < P.cap ? p->window : 0;
   P.fp16 = p->type == DSA_KV8_FP16;
+  P.has_tiles = has_tiles(p);
+  // cached tokens that a tile's rows may see
+  const long long seen = P.window > 0 ? (long long)P.window + TILE_ROWS / P.group + 1 + STEP : P.cap;
+  const long long pairs = (long long)L.max_tiles * p->h_kv;
+  P.cluster = P.has_tiles && 2 * pairs <= sms ? cluster_size(p->d, pairs, (int)((min(seen, (long long)P.cap) + 127) / 128)) : 0;
+  P.n_ctas = P.cluster ? (int)pairs * P.cluster : sms;
   P.small_rows = 8 * row_tiles(p);
   P.n_shares = L.n_shares;
   const bool is_wide = wide(p, sms);

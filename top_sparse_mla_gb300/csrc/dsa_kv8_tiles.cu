@@ -24,6 +24,8 @@
 // than 2^15, so that each fits fp16; when they do not, m is set anew and O rescaled by a
 // power of two, exactly.  That is rare behind the first block.
 
+#include <atomic>
+
 #include "dsa_kv8.cuh"
 
 namespace dsa_kv8 {
@@ -47,8 +49,7 @@ enum {
   B_SFULL = 8, B_PFULL = 10, B_QFULL = 12, B_OFULL = 14,   // scores, weights, queries, result, by half
   B_RAWFULL = 16, B_RAWFREE = 18,   // codes of keys (0) and values (1)
   B_SCALES = 20, B_DRAIN = 24,
-  B_GROUP = 26,                     // the warps of a half meet
-  N_BAR = 28
+  N_BAR = 26
 };
 constexpr float NOTHING = -1.0e30f;   // m of a piece in which a row saw nothing; its O is 0
 constexpr int N_SCALES = 4;      // blocks whose scales are kept: see copies()
@@ -71,7 +72,7 @@ struct Ctx {
   uint8_t* sm;
   uint32_t sb, bars;
   volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2], [3]: groups of the K
-                        // and V codes that have a page, [4], [5]: a half's CTA is the last to arrive
+                        // and V codes that have a page
   uint32_t* status;
 };
 
@@ -115,29 +116,29 @@ DSA_DEV void commit(uint32_t bar_addr) {
 // A unit as every role sees it: the blocks of one piece of a tile, for one KV head.
 struct Unit {
   Tile t;          // t.lo: of the piece
-  int head, index, piece, pieces;   // index: of (tile, head)
+  int head, piece, pieces;
   int blocks[2];   // blocks of each half; 0 for a half without rows or without blocks in the piece
   bool rows[2];
 };
-struct Work {
-  int n_tiles, pieces;
-};
-// Where there are fewer (tile, head) pairs than CTAs, the blocks of each are cut into up to
-// Work::pieces pieces of at least two blocks, which their CTAs join in the end.  A block
-// takes about 2.2 us and a piece 1.5 us of the joining, so sqrt(1.5 blocks) pieces are best.
-//
 // The units are in the order of the tiles, longest first; the CTAs take them forwards and
 // backwards in turn, so that no CTA has the longer one of every round (forwards only, the
 // first CTA of a 2123-token prefill had 40 blocks where the mean is 31).
+//
+// SPLIT: where there are fewer (tile, head) pairs than CTAs, a cluster of P.cluster CTAs has
+// one of them, in pieces of at least two blocks, which the CTAs join in the end through
+// each other's shared memory (about 3 us where a block takes 2; a join through global
+// memory took 14 for 6 pieces).
 template <bool SPLIT>
-DSA_DEV bool unit(const Params& P, long long round, const Work& work, Unit& x) {
-  const long long u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-  const long long per = SPLIT ? (long long)P.h_kv * work.pieces : P.h_kv;
-  if (u >= work.n_tiles * per) return false;
-  const int i = (int)(u / per), rest = (int)(u - i * per);
-  x.piece = SPLIT ? rest / P.h_kv : 0;
-  x.head = rest - x.piece * P.h_kv;
-  x.index = i * P.h_kv + x.head;
+DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
+  long long u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (SPLIT) {
+    u = blockIdx.x / P.cluster;
+    x.piece = blockIdx.x % P.cluster;
+    if (round > 0) return false;
+  }
+  if (u >= (long long)n_tiles * P.h_kv) return false;
+  const int i = (int)(u / P.h_kv);
+  x.head = (int)(u - (long long)i * P.h_kv);
   const int4* at = reinterpret_cast<const int4*>(P.tiles + i);
   const int4 a = __ldcg(at), b = __ldcg(at + 1);   // not __ldg: written while this kernel may be there already
   x.t.req = a.x; x.t.row0 = a.y; x.t.q0 = a.z; x.t.rows = a.w;
@@ -149,10 +150,9 @@ DSA_DEV bool unit(const Params& P, long long round, const Work& work, Unit& x) {
     x.rows[h] = r0 < x.t.rows;
     x.blocks[h] = x.rows[h] ? (hi > x.t.lo ? (hi - x.t.lo + BLOCK - 1) / BLOCK : 1) : 0;
   }
-  x.pieces = 1;
   if (!SPLIT) return true;
   const int all = max(x.blocks[0], x.blocks[1]);
-  x.pieces = max(min(min(work.pieces, all / 2), (int)sqrtf(1.5f * (float)all)), 1);
+  x.pieces = max(min(P.cluster, all / 2), 1);
   const int b0 = (int)((long long)all * x.piece / x.pieces), b1 = (int)((long long)all * (x.piece + 1) / x.pieces);
   x.t.lo += b0 * BLOCK;
 #pragma unroll
@@ -169,7 +169,7 @@ DSA_DEV bool unit(const Params& P, long long round, const Work& work, Unit& x) {
 // the codes of block g - 1 have left their buffer, so the V tile of block g - 2 was written,
 // so the products of block g - 4 are done: the softmax has left the slot.
 template <int D, bool SPLIT>
-DSA_DEV void copies(const Params& P, const Ctx& c, const Work& work) {
+DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   using SM = TileSmem<D>;
   constexpr uint32_t GROUP_BYTES = 16 * D;
   const int lane = threadIdx.x & 31, grp = lane & 7;
@@ -177,7 +177,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, const Work& work) {
   uint32_t g = 0;
   bool ok = true;
   Unit x;
-  for (long long u = 0; ok && unit<SPLIT>(P, u, work, x); ++u) {
+  for (long long u = 0; ok && unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int32_t* table = P.table + x.t.req * P.table_ld;
     auto entry = [&](int i) -> int {
@@ -249,7 +249,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, const Work& work) {
 // swizzled row.  A quarter warp holds four chunks of an even row and the other four of the
 // odd row behind it, which meet in no bank, neither here nor there.
 template <int D, bool SPLIT>
-DSA_DEV void dequant(const Params& P, const Ctx& c, const Work& work) {
+DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   using SM = TileSmem<D>;
   constexpr int CHUNKS = D / 16;            // 16-byte chunks of a row
   constexpr int ROWS = 128 / CHUNKS;        // rows of one pass of the four warps: 16 or 32
@@ -262,7 +262,7 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, const Work& work) {
   const uint32_t s0 = ((2 * (chunk & 3)) ^ (sub & 7)) << 4, s1 = ((2 * (chunk & 3) + 1) ^ (sub & 7)) << 4;
   uint32_t g = 0;
   Unit x;
-  for (long long u = 0; unit<SPLIT>(P, u, work, x); ++u) {
+  for (long long u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int p_first = x.t.pos0 + x.t.row0 / P.group;
     const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
@@ -309,7 +309,7 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, const Work& work) {
 // The whole warp runs this role and one elected lane issues each product: with
 // warp-uniform control flow the descriptors stay in uniform registers.
 template <int D, bool SPLIT>
-DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, const Work& work) {
+DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles) {
   using SM = TileSmem<D>;
   using TM = Tmem<D>;
   constexpr uint32_t ID_QK = idesc_f16(128, BLOCK, 0, 0);
@@ -321,7 +321,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, const Work& 
   uint32_t np[2] = {0, 0};        // blocks of each half
   uint32_t nq[2] = {0, 0};        // units of each half
   Unit x;
-  for (long long u = 0; unit<SPLIT>(P, u, work, x); ++u) {
+  for (long long u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     for (int i = 0; i <= blocks; ++i) {
       const int kb = (g + i) & 1, vb = kb ^ 1;
@@ -438,16 +438,38 @@ DSA_DEV float queries(const uint16_t* mine, uint32_t tile, int row0) {
   return __shfl_sync(0xFFFFFFFFu, back, lane / AT_ONCE + lane % AT_ONCE * LANES);
 }
 
+DSA_DEV void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+DSA_DEV uint32_t at_rank(uint32_t addr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+DSA_DEV float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+DSA_DEV float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Returns whether the CTA's cluster has met (SPLIT).
 template <int D, bool SPLIT>
-DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& work, int h) {
+DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, int h) {
   using SM = TileSmem<D>;
   using TM = Tmem<D>;
   const int row_in = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;   // the warp's 32 lanes of tensor memory
   const uint32_t ts = tmem + lanes + TM::S + 128 * h, to = tmem + lanes + TM::O + D * h;
-  uint32_t g = 0, ns = 0, no = 0, meets = 0;
+  uint32_t g = 0, ns = 0, no = 0;
+  bool met = false;
   Unit x;
-  for (long long u = 0; unit<SPLIT>(P, u, work, x); ++u) {
+  for (long long u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
     if (!(h == 0 ? x.rows[0] : x.rows[1]) || (SPLIT && x.piece >= x.pieces)) {
       g += blocks;
@@ -473,8 +495,8 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
     bool fresh = true;   // m is not set: every score so far was masked
     for (int i = 0; i < mine; ++i) {
       const uint32_t gi = g + i;
-      if (!wait_w(c, B_SCALES + gi % N_SCALES, (gi / N_SCALES) & 1)) return;
-      if (!wait_w(c, B_SFULL + h, ns & 1)) return;
+      if (!wait_w(c, B_SCALES + gi % N_SCALES, (gi / N_SCALES) & 1)) return met;
+      if (!wait_w(c, B_SFULL + h, ns & 1)) return met;
       ++ns;
       tc_fence_after();
       const float4* sc = reinterpret_cast<const float4*>(c.sm + SM::SCALES) + (gi % N_SCALES) * 8;
@@ -586,22 +608,19 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
     }
     // ---- result
     if (!SPLIT || mine > 0) {
-      if (!wait_w(c, B_OFULL + h, no & 1)) return;
+      if (!wait_w(c, B_OFULL + h, no & 1)) return met;
       ++no;
       tc_fence_after();
     }
     uint16_t* dst = P.out + (x.t.q0 + qi) * P.out_ld + head * P.out_hd;
-    auto write = [&](int k, const uint32_t (&o)[32], float inv) {
+    auto write = [&](int k, const float* o, float inv) {   // 8 dims
       if (!live) return;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint4 v;
-        v.x = pack(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv, P.fp16);
-        v.y = pack(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv, P.fp16);
-        v.z = pack(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv, P.fp16);
-        v.w = pack(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv, P.fp16);
-        *reinterpret_cast<uint4*>(dst + k + 8 * e) = v;
-      }
+      uint4 v;
+      v.x = pack(o[0] * inv, o[1] * inv, P.fp16);
+      v.y = pack(o[2] * inv, o[3] * inv, P.fp16);
+      v.z = pack(o[4] * inv, o[5] * inv, P.fp16);
+      v.w = pack(o[6] * inv, o[7] * inv, P.fp16);
+      *reinterpret_cast<uint4*>(dst + k) = v;
     };
     auto inverse = [](float sum) { return sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum); };   // a NaN sum stays one
     if (!SPLIT || x.pieces == 1) {
@@ -611,85 +630,62 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, const Work& w
         uint32_t o[32];
         tmem_ld32(to + k, o);
         tc_wait_ld();
-        write(k, o, inv);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) write(k + e, reinterpret_cast<const float*>(o) + e, inv);
       }
     } else {
-      // one of several pieces: the half's last CTA to arrive joins them in their order
-      constexpr int PSIZE = 128 * (D + 2);
-      auto buffer = [&](int piece) { return P.tile_partial + ((long long)(x.index * work.pieces + piece) * 2 + h) * PSIZE; };
-      float* own = buffer(x.piece);
-      if (!SPLIT || mine > 0) {
-#pragma unroll 1
-        for (int k = 0; k < D; k += 32) {
-          uint32_t o[32];
-          tmem_ld32(to + k, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(own)[(k / 4 + e) * 128 + row_in] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
-      } else {
-#pragma unroll 4
-        for (int k = 0; k < D; k += 4) reinterpret_cast<uint4*>(own)[k / 4 * 128 + row_in] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      own[128 * D + row_in] = fresh ? NOTHING : m;
-      own[128 * D + 128 + row_in] = l;
-      __threadfence();
-      arrive_w(c, B_GROUP + h);
-      if (!wait_w(c, B_GROUP + h, meets++ & 1)) return;
-      if (row_in == 0) c.misc[4 + h] = atomicAdd(P.tile_arrived + 2 * x.index + h, 1) == x.pieces - 1;
-      arrive_w(c, B_GROUP + h);
-      if (!wait_w(c, B_GROUP + h, meets++ & 1)) return;
-      if (!c.misc[4 + h]) {
-        g += blocks;
-        continue;
-      }
-      __threadfence();
-      m = NOTHING;
-#pragma unroll 4
-      for (int p = 0; p < x.pieces; ++p) m = fmaxf(m, __ldcg(buffer(p) + 128 * D + row_in));
-      l = 0.f;
-#pragma unroll 4
-      for (int p = 0; p < x.pieces; ++p)
-        l = fmaf(__ldcg(buffer(p) + 128 * D + 128 + row_in), ex2(__ldcg(buffer(p) + 128 * D + row_in) - m), l);
-      const float inv = inverse(l);
+      // One of several pieces.  O of both halves goes over the K and V tiles, whose products
+      // are done, as [D / 4][128 rows][4]; m and l over the codes.
+      const int other = h == 0 ? x.blocks[1] : x.blocks[0];
+      if (other > 0 && !wait_w(c, B_OFULL + 1 - h, 0)) return met;
+      const uint32_t s_o = c.sb + SM::K + 2 * SM::OPERAND * h, s_ml = c.sb + SM::RAW + 1024 * h;
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
-        float o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 1
-        for (int p0 = 0; p0 < x.pieces; p0 += 2) {   // two at a time: their loads are under way together
-          float4 v[2][8];
-          float f[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float* from = buffer(min(p0 + y, x.pieces - 1));
-            const float pm = __ldcg(from + 128 * D + row_in);
-            f[y] = p0 + y < x.pieces ? ex2(pm - m) : 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[y][e] = __ldcg(reinterpret_cast<const float4*>(from) + (k / 4 + e) * 128 + row_in);
-          }
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o[4 * e] = fmaf(v[y][e].x, f[y], o[4 * e]);
-              o[4 * e + 1] = fmaf(v[y][e].y, f[y], o[4 * e + 1]);
-              o[4 * e + 2] = fmaf(v[y][e].z, f[y], o[4 * e + 2]);
-              o[4 * e + 3] = fmaf(v[y][e].w, f[y], o[4 * e + 3]);
-            }
+        uint32_t o[32];
+        if (mine > 0) {
+          tmem_ld32(to + k, o);
+          tc_wait_ld();
         }
-        uint32_t bits[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) bits[e] = __float_as_uint(o[e]);
-        write(k, bits, inv);
+        for (int e = 0; e < 8; ++e)
+          sts128(s_o + ((k / 4 + e) * 128 + row_in) * 16,
+                 mine > 0 ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_uint4(0u, 0u, 0u, 0u));
+      }
+      float* ml = reinterpret_cast<float*>(c.sm + SM::RAW + 1024 * h);
+      ml[row_in] = fresh ? NOTHING : m;
+      ml[128 + row_in] = l;
+      cluster_meet();
+      met = true;
+      // this CTA joins 8-dim chunks [c0, c1) of every row, in the order of the pieces
+      m = NOTHING;
+      for (int p = 0; p < x.pieces; ++p) m = fmaxf(m, ld_cluster(at_rank(s_ml, p) + 4 * row_in));
+      l = 0.f;
+      for (int p = 0; p < x.pieces; ++p) {
+        const uint32_t from = at_rank(s_ml, p) + 4 * row_in;
+        l = fmaf(ld_cluster(from + 512), ex2(ld_cluster(from) - m), l);
+      }
+      const float inv = inverse(l);
+      const int c0 = D / 8 * x.piece / x.pieces, c1 = D / 8 * (x.piece + 1) / x.pieces;
+      for (int k = c0; k < c1; ++k) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < x.pieces; ++p) {
+          const float f = ex2(ld_cluster(at_rank(s_ml, p) + 4 * row_in) - m);
+          const uint32_t from = at_rank(s_o, p) + (2 * k * 128 + row_in) * 16;
+          const float4 a = ld_cluster4(from), b = ld_cluster4(from + 128 * 16);
+          o[0] = fmaf(a.x, f, o[0]); o[1] = fmaf(a.y, f, o[1]); o[2] = fmaf(a.z, f, o[2]); o[3] = fmaf(a.w, f, o[3]);
+          o[4] = fmaf(b.x, f, o[4]); o[5] = fmaf(b.y, f, o[5]); o[6] = fmaf(b.z, f, o[6]); o[7] = fmaf(b.w, f, o[7]);
+        }
+        write(8 * k, o, inv);
       }
     }
-    if (live && P.lse)
+    if (live && P.lse && (!SPLIT || x.piece == 0))
       P.lse[(long long)(x.t.q0 + qi) * P.h_q + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
     g += blocks;
   }
+  return met;
 }
 
 template <int D, bool SPLIT>
@@ -715,7 +711,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
       mbar_init(bar(c, B_OFULL + i), 1);
       mbar_init(bar(c, B_RAWFULL + i), 1);
       mbar_init(bar(c, B_RAWFREE + i), 4);
-      mbar_init(bar(c, B_GROUP + i), 4);
     }
     for (int i = 0; i < N_SCALES; ++i) mbar_init(bar(c, B_SCALES + i), 1);
     mbar_init(bar(c, B_DRAIN), 1);
@@ -729,15 +724,20 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   const uint32_t tmem = (uint32_t)c.misc[0];
   // launched as a programmatic dependent of rows_kernel, which waited for the plan
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Work work{P.header->n_tiles, P.header->pieces};
+  const int n_tiles = P.header->n_tiles;
+  bool met = false;
   if (warp < W_DQ) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    softmax<D, SPLIT>(P, c, tmem, work, warp >> 2);
+    met = softmax<D, SPLIT>(P, c, tmem, n_tiles, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    if (warp < W_MMA) dequant<D, SPLIT>(P, c, work);
-    else if (warp == W_MMA) products<D, SPLIT>(P, c, tmem, work);
-    else if (warp == W_COPY) copies<D, SPLIT>(P, c, work);
+    if (warp < W_MMA) dequant<D, SPLIT>(P, c, n_tiles);
+    else if (warp == W_MMA) products<D, SPLIT>(P, c, tmem, n_tiles);
+    else if (warp == W_COPY) copies<D, SPLIT>(P, c, n_tiles);
+  }
+  if (SPLIT) {   // every thread twice: the pieces are there; and they have been read
+    if (!met) cluster_meet();
+    cluster_meet();
   }
   if (warp == W_MMA) commit(bar(c, B_DRAIN));
   tc_fence_before();
@@ -757,30 +757,76 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
 }
 
 template <int D, bool SPLIT>
-static int launch_one(const Params& P, cudaStream_t st) {
+static int configure(const Params& P, cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
   constexpr int smem = TileSmem<D>::BYTES;
   // the kernel's groups trade the registers that its launch gave them
   cudaFuncAttributes a;
   if (cudaFuncGetAttributes(&a, tiles_kernel<D, SPLIT>) != cudaSuccess || a.numRegs != LAUNCH_REGS) return DSA_ERR_CUDA;
   if (cudaFuncSetAttribute(tiles_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
+  if (SPLIT && cudaFuncSetAttribute(tiles_kernel<D, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  cfg = {};
   cfg.gridDim = dim3((unsigned)P.n_ctas);
   cfg.blockDim = dim3(TILE_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)max(P.cluster, 1);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return DSA_OK;
+}
+
+template <int D, bool SPLIT>
+static int launch_one(const Params& P, cudaStream_t st) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  const int rc = configure<D, SPLIT>(P, cfg, attr, st);
+  if (rc != DSA_OK) return rc;
   return cudaLaunchKernelEx(&cfg, tiles_kernel<D, SPLIT>, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-// The kernel that can split a tile's blocks is a copy of its own: with the joining in it,
-// the other one's loops took a tenth longer.
+// How many clusters of a size the current device holds at a time: a property of the device,
+// asked for once.
+template <int D>
+static int resident_clusters(int size) {
+  constexpr int DEVICES = 64;
+  static std::atomic<int> known[DEVICES][MAX_CLUSTER + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < DEVICES && known[dev][size].load(std::memory_order_relaxed) > 0) return known[dev][size].load(std::memory_order_relaxed) - 1;
+  Params P = {};
+  P.n_ctas = P.cluster = size;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (configure<D, true>(P, cfg, attr, nullptr) != DSA_OK) return 0;
+  cfg.attrs = attr + 1;   // the cluster's
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, tiles_kernel<D, true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();   // a size that this device cannot hold
+    n = 0;
+  }
+  if (dev < DEVICES) known[dev][size].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+int cluster_size(int d, long long units, int blocks) {
+  if (blocks < 4) return 0;   // no two pieces of two blocks
+  for (const int size : {12, 10, 8, 6, 4, 2})
+    if ((size <= blocks / 2 || size == 2) && units <= (d == 128 ? resident_clusters<128>(size) : resident_clusters<64>(size)))
+      return size;
+  return 0;
+}
+
+// The kernel that splits a tile's blocks is a copy of its own: with the joining in it, the
+// other one's loops took a tenth longer.
 int launch_tiles(int d, const Params& P, cudaStream_t st) {
-  if (P.tile_split) return d == 128 ? launch_one<128, true>(P, st) : launch_one<64, true>(P, st);
+  if (P.cluster) return d == 128 ? launch_one<128, true>(P, st) : launch_one<64, true>(P, st);
   return d == 128 ? launch_one<128, false>(P, st) : launch_one<64, false>(P, st);
 }
 
