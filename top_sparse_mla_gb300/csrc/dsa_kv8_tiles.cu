@@ -325,42 +325,44 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
     const int blocks = max(x.blocks[0], x.blocks[1]);
     for (int i = 0; i <= blocks; ++i) {
       const int kb = (g + i) & 1, vb = kb ^ 1;
+      // the values of a block are written before the next one's keys
       if (i < blocks && !wait_w(c, B_KFULL + kb, ((g + i) >> 1) & 1)) return;
-      if (i > 0 && !wait_w(c, B_VFULL + vb, ((g + i - 1) >> 1) & 1)) return;
+      if (i > 0 && i == blocks && !wait_w(c, B_VFULL + vb, ((g + i - 1) >> 1) & 1)) return;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (i > 0 && i - 1 < x.blocks[h]) {
+        const bool pv = i > 0 && i - 1 < x.blocks[h], qk = i < x.blocks[h];
+        if (pv) {
           if (!wait_w(c, B_PFULL + h, np[h] & 1)) return;
           ++np[h];
-          tc_fence_after();
-          if (elect_one())
+        } else if (qk) {
+          if (!wait_w(c, B_QFULL + h, nq[h] & 1)) return;
+          ++nq[h];
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          if (pv) {
 #pragma unroll
-          for (int k = 0; k < BLOCK / 16; ++k) {
+            for (int k = 0; k < BLOCK / 16; ++k)
               mma_ts(tmem + TM::O + D * h, tmem + TM::S + 128 * h + 8 * k,
                      d_v + ((uint32_t)(vb * SM::OPERAND + k * 2048) >> 4), ID_PV, (i > 1 || k > 0) ? 1u : 0u);
+            if (!qk) tc_commit(bar(c, B_OFULL + h));
           }
-          __syncwarp();
-          if (i == x.blocks[h]) commit(bar(c, B_OFULL + h));
-        }
-        if (i < x.blocks[h]) {
-          if (i == 0) {
-            if (!wait_w(c, B_QFULL + h, nq[h] & 1)) return;
-            ++nq[h];
-          }
-          tc_fence_after();
-          if (elect_one())
+          if (qk) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * SM::PANEL + (k & 3) * 32;
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * SM::PANEL + (k & 3) * 32;
               mma_ss(tmem + TM::S + 128 * h, d_q + ((h * SM::OPERAND + off) >> 4), d_k + ((kb * SM::OPERAND + off) >> 4),
                      ID_QK, k ? 1u : 0u);
+            }
+            tc_commit(bar(c, B_SFULL + h));
           }
-          __syncwarp();
-          commit(bar(c, B_SFULL + h));
+          if (h == 1) {
+            if (i < blocks) tc_commit(bar(c, B_KFREE + kb));
+            if (i > 0) tc_commit(bar(c, B_VFREE + vb));
+          }
         }
+        __syncwarp();
       }
-      if (i < blocks) commit(bar(c, B_KFREE + kb));
-      if (i > 0) commit(bar(c, B_VFREE + vb));
     }
     g += blocks;
   }
