@@ -251,6 +251,20 @@ def test_magnitudes(kw, lens):
     _check(c)
 
 
+@pytest.mark.parametrize("low,high", [(8, 22), (14, 26), (14, 30), (15, 40)])
+def test_scores_that_rise_within_and_between_blocks(low, high):
+    """Scores 0 for 128 tokens, then 64 at 2^low times their weight, then one at 2^high: what the 64 add up to is 64 * 2^(low - high)
+    of the mass, up to 1.5 %, and must not get lost when the maximum is moved."""
+    c = Case(70, [(40, 256)], h=1, g=8, d=128, page=16, v_scale=[1.0], poison=False, scale=float(np.log(2.0)))
+    c.ks[:] = 1.0
+    c.q[:] = 0.0
+    c.q[:, :, 0] = 1.0
+    c.kp[:] = 0
+    for j in range(128, 256):
+        c.kp[c.table[0, j // 16], 0, j % 16, 0] = codecs.e4m3_encode(np.array([low if j < 192 else high if j == 200 else 0.0]))[0]
+    _check(c)
+
+
 def test_queries_with_a_wide_range_in_one_row_and_zero_rows():
     c = Case(14, [(1, 200), (40, 120)], h=1, g=4, page=16)
     c.q[1:-2, :, ::3] *= 2.0 ** -12

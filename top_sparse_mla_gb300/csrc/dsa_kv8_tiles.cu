@@ -561,8 +561,7 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
                 tmem_st32(to + k, o);
               }
             }
-            if (s == 1) {   // the weights of the block's first part
-              const __half2 f2 = __float2half2_rn(f);
+            if (s == 1) {   // the weights of the block's first part; in fp32, where f has all its range
 #pragma unroll 1
               for (int k = 0; k < 32; k += 16) {
                 uint32_t o[16];
@@ -570,8 +569,8 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
                 tc_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f2);
-                  o[e] = *reinterpret_cast<const uint32_t*>(&y);
+                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&o[e]));
+                  o[e] = pack_f16x2(y.x * f, y.y * f);
                 }
                 tmem_st16(ts + k, o);
               }
