@@ -204,7 +204,7 @@ def test_many_requests():
                 dtype="fp16"))
 
 
-@pytest.mark.parametrize("n", [127, 128, 129, 512, 513])
+@pytest.mark.parametrize("n", [127, 128, 129, 513, 1536, 1537])
 @pytest.mark.parametrize("kw", [dict(h=1, g=2, d=128), dict(h=3, g=12, d=64)])
 def test_batches_at_the_sizes_where_the_shares_are_found_otherwise(n, kw):
     rng = np.random.default_rng(n)

@@ -52,7 +52,7 @@ struct Params {
   int n_tokens, n_req, h_q, h_kv, group, n_pages, page_shift, cap, max_q_len, window, fp16;
   int small_rows;   // requests with at most this many rows go to rows_kernel
   int unit_steps, min_share;   // what a unit costs a CTA beside its steps, and a CTA's least share, in steps
-  int own_plan;     // whether rows_kernel's CTAs find their shares for themselves
+  int own_plan;     // requests of a thread where rows_kernel's CTAs find their shares for themselves, else 0
   int n_shares, max_tiles, n_ctas;   // n_ctas: of the tiles' kernel
   int has_tiles;    // whether requests may have more rows than rows_kernel takes
   int cluster;      // CTAs that share a tile and KV head; 0: a CTA has several of them

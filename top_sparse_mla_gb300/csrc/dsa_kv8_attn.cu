@@ -22,6 +22,10 @@ constexpr int ROW_WARPS = 4;      // warps of a rows_kernel CTA
 constexpr int UNIT_STEPS = 2;     // what a unit (request, KV head) costs a CTA beside its steps, in steps of every warp
 constexpr int MIN_STEPS = 2;      // the fewest steps of a warp that are worth a unit's beginning
 constexpr int PLAN_THREADS = 1024;
+// Requests that a thread of rows_kernel looks at for its CTA's share, at most.  Up to 300
+// tokens, 16/2 heads, us, own shares and the plan's: 500 requests 19.9 and 23.5, 1024 32.7
+// and 35.4, 1500 47.4 and 50.8, 2048 (16 a thread) 63.3 and 63.6, 4096 124.7 and 111.3.
+constexpr int OWN_PLAN = 12;
 constexpr int FEW_THREADS = 256;  // of the plan, where rows_kernel's CTAs find their shares
 // rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
@@ -695,12 +699,14 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
   __syncthreads();   // the shared memory is used again
 }
 
-// This CTA's share, and in share_steps the steps of each share: what the plan kernel computes, for at
-// most as many requests as the CTA has threads.
+// This CTA's share, and in share_steps the steps of each share: what the plan kernel
+// computes.  A thread looks at P.own_plan requests.
 template <int D, int NT, int NW>
 __device__ __forceinline__ Share own_share(const Params& P, RowSmem<D, NT, NW>& S, int b) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const long long steps = tid < P.n_req ? unit_steps(P, request(P, tid)) : 0;
+  const int r0 = min(tid * P.own_plan, P.n_req), r1 = min(r0 + P.own_plan, P.n_req);
+  long long steps = 0;
+  for (int r = r0; r < r1; ++r) steps += unit_steps(P, request(P, r));
   if (tid == 0) S.share = Share{-1, 0, 0};
   long long in = steps;
 #pragma unroll
@@ -717,7 +723,15 @@ __device__ __forceinline__ Share own_share(const Params& P, RowSmem<D, NT, NW>& 
     all += S.scan[u];
   }
   const long long share = share_of(P, all * P.h_kv), f = b * share;
-  if (before * P.h_kv <= f && f < (before + steps) * P.h_kv) S.share = share_at(P, tid, f - before * P.h_kv, steps);
+  if (before * P.h_kv <= f && f < (before + steps) * P.h_kv)
+    for (int r = r0; r < r1; ++r) {
+      const long long here = unit_steps(P, request(P, r));
+      if (f < (before + here) * P.h_kv) {
+        S.share = share_at(P, r, f - before * P.h_kv, here);
+        break;
+      }
+      before += here;
+    }
   if (tid == 0) S.share_steps = share;
   __syncthreads();
   return S.share;
@@ -993,7 +1007,8 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   const int warps = is_wide ? ROW_WARPS * ctas_per_sm(p->d, row_tiles(p)) : ROW_WARPS;
   P.unit_steps = UNIT_STEPS * warps;
   P.min_share = P.unit_steps + MIN_STEPS * warps;
-  P.own_plan = p->n_req <= 32 * warps;
+  // the requests of a thread where the CTAs find their shares for themselves; 0: the plan kernel does
+  P.own_plan = p->n_req <= OWN_PLAN * 32 * warps ? (p->n_req + 32 * warps - 1) / (32 * warps) : 0;
   P.max_tiles = L.max_tiles;
   P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   const size_t smem = (size_t)(p->n_req + 1) * 2 * sizeof(long long);
