@@ -248,8 +248,9 @@ struct Codes {
 };
 
 // The steps of one warp: every `stride`-th one of [first, end).  A warp stops at the first
-// use of a value that it is still loading, so a step's table entry is loaded two steps
-// ahead and looked at one step later, its codes and scales one step ahead.
+// use of a value that it is still loading, so a step's table entry is loaded three steps
+// ahead and looked at one step later, when its codes are sent for to L2; codes and scales
+// are loaded one step ahead.
 template <int D>
 struct Steps {
   const Params& P;
@@ -257,7 +258,7 @@ struct Steps {
   int head, lo, hi, first, end, stride;
   const uint8_t *k_lane, *v_lane;   // the pools at the lane's place in a step
   Codes<D> C;
-  int page, raw_next;   // the first step's page, the entry of the one behind it
+  int page, raw_next, raw_after;   // the first step's page, the entries of the two behind it
   float ks, vs;
 
   __device__ __forceinline__ int entry(int s) const {
@@ -299,6 +300,15 @@ struct Steps {
   __device__ __forceinline__ void begin() {
     page = entry(first);
     raw_next = entry(first + stride);
+    raw_after = entry(first + 2 * stride);
+  }
+  // a step's codes from memory to L2: a lane for each of their lines
+  __device__ __forceinline__ void prefetch(int page_, int s) const {
+    constexpr int LINES = STEP * D / 128;   // of the keys, and of the values
+    const int lane = threadIdx.x & 31;
+    if (page_ < 0 || lane >= 2 * LINES) return;
+    const uint8_t* at = (lane < LINES ? P.k_pool : P.v_pool) + (uint64_t)row_of(page_, s) * D + (lane % LINES) * 128;
+    dsa::prefetch_line_l2(at);
   }
   __device__ __forceinline__ void load_first() {
     page = valid(page);
@@ -317,11 +327,17 @@ __device__ __forceinline__ void rows_steps(const Params& P, Steps<D>& W, int see
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int lo = W.lo, hi = W.hi, stride = W.stride;
   Codes<D>& C = W.C;
-  int page = W.page, raw_next = W.raw_next;
+  int page = W.page, raw_next = W.raw_next, raw_after = W.raw_after;
   float ks = W.ks, vs = W.vs;
+  // The registers have room for one step ahead, L2 for two.  us, with and without: 64
+  // requests of up to 32k tokens 309 and 317, 48 of up to 8k with 4 queries 89 and 93, 32
+  // rows 101 and 107; but one row tile in a wide CTA, which has few steps, 19.8 and 19.4.
+  const bool prefetch = NT > 1 || stride == ROW_WARPS;
   for (int s = W.first; s < W.end; s += stride) {
     const int page_next = W.valid(raw_next);
-    raw_next = W.entry(s + 2 * stride);
+    raw_next = raw_after;
+    raw_after = W.entry(s + 3 * stride);
+    if (prefetch) W.prefetch(W.valid(raw_next), s + 2 * stride);
     const float ks_next = W.load_scale(P.k_scale, page_next), vs_next = W.load_scale(P.v_scale, page_next);
     if (page < 0) {
       W.load_k(page_next, s + stride);
