@@ -69,7 +69,8 @@
  * Numerics: E4M3 codes are exact in fp16, and so are the queries after each row's scaling
  * by a power of two (values below 2^-30 of the row's largest are rounded); products
  * accumulate in fp32; scores, the running maximum and sums are fp32.  The softmax weights
- * are rounded to fp16 (2^-12 relative) for the product with the values, not for their sum.
+ * are rounded to fp16 (2^-12 relative, and 2^-25 of the row's largest weight) for the
+ * product with the values, not for their sum.
  *
  * Both calls are asynchronous on `stream` (a cudaStream_t, NULL = legacy default stream),
  * allocate nothing and can be captured in a CUDA graph.  They return DSA_OK, or one of the

@@ -15,8 +15,15 @@
 //   - warp 12 issues the products: S = Q K^T (128 x 128 x D) and O += P V (128 x D x 128,
 //     P in tensor memory).  The two halves alternate, so that one half's softmax runs
 //     under the other half's products.
+// What bounds it: a half's chain of scores, softmax (about 2100 cycles a block), weights and
+// products (1024) and their handoffs (500), while the two halves' products are 2048.  6
+// chunks of 2048 queries on up to 8k tokens, 32/4 heads of 128: 690 us, 1190 TFLOP/s, 0.61
+// of a large bf16 product's rate; a 2123-token prefill, 64/8 heads, whose units have 1 to 17
+// blocks: 96 us, 0.39.
+//
 // Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
-// and the CTA's roles stop, drain the tensor core and free its memory.
+// and the CTA's roles stop, drain the tensor core and free its memory.  The CTAs of a
+// cluster meet by its barrier, at which each of their threads comes by whatever way.
 //
 // Scores become u = S * (k_scale * softmax_scale * log2 e * row scaling) + (log2 v_scale - m)
 // and weights 2^u, with m an integer that was the row's maximum, rounded down, when it was
