@@ -218,10 +218,13 @@ def test_batches_at_the_sizes_where_the_shares_are_found_otherwise(n, kw):
     ([(4, 5000), (3, 5001)], 4, 8),
     ([(1, 300 + 7 * i) for i in range(38)], 2, 2),   # two CTAs a unit, on 152
     ([(1, 300 + 7 * i) for i in range(39)], 2, 2),
+    ([(1, 4000)] + [(1, 1 + 17 * i) for i in range(37)], 2, 2),
+    ([(1, 1 + 17 * i) for i in range(38)] + [(1, 4000)], 2, 2),
 ])
 def test_few_units_shared_by_wide_ctas(lens, h, g):
     _check(Case(40, lens, h=h, g=g, page=64))
     _check(Case(41, lens, h=h, g=g, page=16, window=900, dtype="fp16"))
+    _check(Case(42, lens, h=h, g=g, page=32, window=3600))
 
 
 # 12, 10, 8, 6, 4 and 2 CTAs for each tile and head, on 152

@@ -848,14 +848,16 @@ static bool has_tiles(const dsa_kv8_params* p) {
 }
 
 // Whether a CTA of rows_kernel has all the warps that an SM holds, or four of them.  With
-// few units, which many CTAs share, wider CTAs leave fewer pieces to join.  Heads of 128, us,
-// wide and not: 4 requests of up to 8k tokens, 64/8 heads, 15.2 and 17.3; 8 such 18.7 and
-// 22.2; 2 of up to 32k, 32/8 heads, 4 queries, 34.3 and 37.0; one of 512 tokens, 8/1 heads,
-// 8.4 and 9.5; but 16 of up to 2k (128 units) 16.0 and 14.3, and one of 16 tokens 9.8 and 8.0.
-// Heads of 64 (24 warps): 12 of up to 4k tokens, 16/4 heads, 14.2 and 11.5.
+// few units, which many CTAs share, wider CTAs leave fewer pieces to join; with short ones
+// their warps have nothing to do.  Heads of 128, 64/8 heads, us, wide and not: 4 requests of
+// up to 2500 tokens 14.6 and 13.2, 4000 15.2 and 17.3, 12000 17.9 and 21.9; 8 of 2500 15.1
+// and 13.7, 4000 15.2 and 17.7; 16 (128 units) of 2k 16.0 and 14.3.  Heads of 64 (24 warps):
+// 12 of up to 4k tokens, 16/4 heads, 14.2 and 11.5.
 static bool wide(const dsa_kv8_params* p, int sms) {
-  const long long units = (long long)p->n_req * p->h_kv, most = (long long)p->table_cols * p->page_size;
-  return p->d == 128 && 2 * units <= sms && most >= 256;
+  const long long units = (long long)p->n_req * p->h_kv;
+  long long most = (long long)p->table_cols * p->page_size;   // cached tokens that a request's queries see
+  if (p->window > 0 && most > (long long)p->window + p->max_q_len) most = (long long)p->window + p->max_q_len;
+  return p->d == 128 && 2 * units <= sms && most >= 3500;
 }
 
 struct Layout {
