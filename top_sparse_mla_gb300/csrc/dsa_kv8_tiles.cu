@@ -137,18 +137,21 @@ struct Unit {
 // each other's shared memory (about 3 us where a block takes 2; a join through global
 // memory took 14 for 6 pieces).
 template <bool SPLIT>
-DSA_DEV bool unit(const Params& P, long long round, int n_tiles, Unit& x) {
-  long long u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+DSA_DEV bool unit(const Params& P, uint32_t round, int n_tiles, Unit& x) {
+  // below 2^32: a unit that is not a request's last has 256 rows of q, 32 KB or more
+  uint32_t u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   if (SPLIT) {
     u = blockIdx.x / P.cluster;
     x.piece = blockIdx.x % P.cluster;
     if (round > 0) return false;
   }
-  if (u >= (long long)n_tiles * P.h_kv) return false;
-  const int i = (int)(u / P.h_kv);
-  x.head = (int)(u - (long long)i * P.h_kv);
+  if (u >= (unsigned long long)n_tiles * P.h_kv) return false;
+  const uint32_t i = u / (uint32_t)P.h_kv;
+  x.head = (int)(u - i * P.h_kv);
   const int4* at = reinterpret_cast<const int4*>(P.tiles + i);
-  const int4 a = __ldcg(at), b = __ldcg(at + 1);   // not __ldg: written while this kernel may be there already
+  // plain loads: the copying warp's bring the line to L1 for the other roles.  (Not __ldg: the
+  // plan may be written while this kernel is there already.)
+  const int4 a = at[0], b = at[1];
   x.t.req = a.x; x.t.row0 = a.y; x.t.q0 = a.z; x.t.rows = a.w;
   x.t.pos0 = b.x; x.t.lo = b.y; x.t.hi = b.z;
 #pragma unroll
@@ -185,7 +188,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   uint32_t g = 0;
   bool ok = true;
   Unit x;
-  for (long long u = 0; ok && unit<SPLIT>(P, u, n_tiles, x); ++u) {
+  for (uint32_t u = 0; ok && unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int32_t* table = P.table + x.t.req * P.table_ld;
     auto entry = [&](int i) -> int {
@@ -270,7 +273,7 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   const uint32_t s0 = ((2 * (chunk & 3)) ^ (sub & 7)) << 4, s1 = ((2 * (chunk & 3) + 1) ^ (sub & 7)) << 4;
   uint32_t g = 0;
   Unit x;
-  for (long long u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
+  for (uint32_t u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     const int p_first = x.t.pos0 + x.t.row0 / P.group;
     const int seen_lo = P.window > 0 ? max(p_first - P.window + 1, 0) : 0;
@@ -329,7 +332,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
   uint32_t np[2] = {0, 0};        // blocks of each half
   uint32_t nq[2] = {0, 0};        // units of each half
   Unit x;
-  for (long long u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
+  for (uint32_t u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
     for (int i = 0; i <= blocks; ++i) {
       const int kb = (g + i) & 1, vb = kb ^ 1;
@@ -479,7 +482,7 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
   uint32_t g = 0, ns = 0, no = 0;
   bool met = false;
   Unit x;
-  for (long long u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
+  for (uint32_t u = 0; unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
     if (!(h == 0 ? x.rows[0] : x.rows[1]) || (SPLIT && x.piece >= x.pieces)) {
       g += blocks;
