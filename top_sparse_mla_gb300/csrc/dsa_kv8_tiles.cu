@@ -17,9 +17,9 @@
 //     under the other half's products.
 // What bounds it: a half's chain of scores, softmax (about 2100 cycles a block), weights and
 // products (1024) and their handoffs (500), while the two halves' products are 2048.  6
-// chunks of 2048 queries on up to 8k tokens, 32/4 heads of 128: 690 us, 1190 TFLOP/s, 0.61
+// chunks of up to 2048 queries on up to 8k tokens, 32/4 heads of 128: 687 us, 1199 TFLOP/s, 0.61
 // of a large bf16 product's rate; a 2123-token prefill, 64/8 heads, whose units have 1 to 17
-// blocks: 96 us, 0.39.
+// blocks: 95 us, 0.40.
 //
 // Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
 // and the CTA's roles stop, drain the tensor core and free its memory.  The CTAs of a
