@@ -550,6 +550,9 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
         }
         const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
         if (__any_sync(0xFFFFFFFFu, fresh || top > MOST)) {
+          // what this thread stored last (O, or the weights of the block's first part) is read
+          // again below, and only this wait puts a tensor memory load behind a store
+          tc_wait_st();
           const bool up = top > (fresh ? -INFINITY : LAG);
           const float to_m = up ? floorf(m + top) : m;   // the largest weight is in [1, 2)
           const float delta = to_m - m, f = (up && !fresh) ? ex2(-delta) : 1.0f;
