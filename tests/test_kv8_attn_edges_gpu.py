@@ -2,6 +2,10 @@
 maximum, magnitudes and batch sizes at the ends of their ranges.  Case, its check and the error bound are those of
 test_kv8_attn_gpu."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -53,3 +57,20 @@ def test_maxima_that_move_in_both_parts_of_a_block(rise, lens, d):
         scores[at:] = best - 3
         scores[at] = best
     _check(_with_scores(rise + d, lens, scores, g=8, d=d, page=32))
+
+
+def _batch(n):
+    """n requests of up to two queries, a group of 2: all of them for rows_kernel."""
+    rng = np.random.default_rng(n)
+    return Case(n, [(int(a), int(b)) for a, b in zip(rng.integers(0, 3, n), rng.integers(0, 40, n))], h=1, g=2, d=64, page=16)
+
+
+# 2783 requests are the first whose prefix sums and the plan's other shared memory pass 48 KB together, 3072 the first
+# whose prefix sums do so alone.  A kernel keeps a limit that was raised: each size in a process of its own.
+@pytest.mark.parametrize("n", [2782, 2783, 3071, 3072, native.DSA_KV8_MAX_REQ])
+def test_large_batches_as_a_process_first_call(n):
+    code = f"import test_kv8_attn_edges_gpu as t; t._check(t._batch({n}))"
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    run = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
