@@ -2,12 +2,15 @@
 maximum, magnitudes and batch sizes at the ends of their ranges.  Case, its check and the error bound are those of
 test_kv8_attn_gpu."""
 
+import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import codecs
 from test_kv8_attn_gpu import Case, _check
@@ -74,3 +77,42 @@ def test_large_batches_as_a_process_first_call(n):
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
     run = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_large_batches_from_several_host_threads():
+    """The C calls of two batch sizes, each from two threads on streams of their own: a smaller batch's call lowered the limit of
+    shared memory between a larger one's setting it and its launch, which refused one in a hundred of the larger ones."""
+    lib = native.library()
+    cases = [_batch(n) for n in (3072, native.DSA_KV8_MAX_REQ)]
+    calls = []
+    for c in cases + cases:
+        D = c.device()
+        p = native.dsa_kv8_params_init(D["q"], D["kp"], D["table"], max_q_len=2, softmax_scale=c.scale)
+        out = torch.full((c.n, c.h * c.g, c.d), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((c.n, c.h * c.g), 7.0, device="cuda")
+        ws = torch.empty(native.dsa_kv8_attn_workspace_size(p), dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        pitch = (c.h * c.g * c.d, c.d)
+        args = (D["q"].data_ptr(), *pitch, *(D[x].data_ptr() for x in ("kp", "vp", "ks", "vs", "table")), D["table"].stride(0),
+                D["cu"].data_ptr(), D["kv"].data_ptr(), out.data_ptr(), *pitch, lse.data_ptr(), ctypes.byref(p), ws.data_ptr(),
+                ws.nbytes, stream.cuda_stream)
+        calls.append((c, D, out, lse, ws, p, stream, args))
+    torch.cuda.synchronize()
+    failed = [0] * len(calls)
+
+    def loop(i):
+        stream, args = calls[i][-2:]
+        for j in range(3000):
+            failed[i] += lib.dsa_kv8_attn_fwd(*args) != native.DSA_OK
+            if j % 16 == 15:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(calls)
+    for c, _, out, lse, *_ in calls[:2]:
+        c.check(out, lse)

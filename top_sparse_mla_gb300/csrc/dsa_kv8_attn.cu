@@ -885,8 +885,10 @@ static Layout layout(const dsa_kv8_params* p, int sms) {
   return L;
 }
 
+// `most` is the most dynamic shared memory that any call asks of the kernel.  The limit is set to
+// that and never to less: another host thread may set it between this one's setting and its launch.
 template <typename K>
-static int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st, const Params& P, bool dependent) {
+static int launch(K kernel, int grid, int threads, size_t smem, size_t most, cudaStream_t st, const Params& P, bool dependent) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -898,7 +900,7 @@ static int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st,
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 1 : 0;
   // the limit of 48 KB is for dynamic and static shared memory together; no kernel here has 8 KB of the latter
-  if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
     return DSA_ERR_CUDA;
   return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
@@ -906,8 +908,9 @@ static int launch(K kernel, int grid, int threads, size_t smem, cudaStream_t st,
 template <int D, int NT>
 static int launch_rows(const Params& P, bool wide, cudaStream_t st) {
   constexpr int W = ROW_WARPS, WW = D == 128 ? W * ctas_per_sm(D, NT) : W;
-  return wide ? launch(rows_kernel<D, NT, WW>, P.n_shares, 32 * WW, sizeof(RowSmem<D, NT, WW>), st, P, true)
-              : launch(rows_kernel<D, NT, W>, P.n_shares, 32 * W, sizeof(RowSmem<D, NT, W>), st, P, true);
+  constexpr size_t smem = sizeof(RowSmem<D, NT, W>), wide_smem = sizeof(RowSmem<D, NT, WW>);
+  return wide ? launch(rows_kernel<D, NT, WW>, P.n_shares, 32 * WW, wide_smem, wide_smem, st, P, true)
+              : launch(rows_kernel<D, NT, W>, P.n_shares, 32 * W, smem, smem, st, P, true);
 }
 
 template <int D>
@@ -1037,9 +1040,10 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   P.own_plan = p->n_req <= OWN_PLAN * 32 * warps ? (p->n_req + 32 * warps - 1) / (32 * warps) : 0;
   P.max_tiles = L.max_tiles;
   P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
-  const size_t smem = (size_t)(p->n_req + 1) * 2 * sizeof(long long);
-  const int rc1 = P.own_plan ? launch(plan_kernel<FEW_THREADS>, 1, FEW_THREADS, smem, st, P, false)
-                             : launch(plan_kernel<PLAN_THREADS>, 1, PLAN_THREADS, smem, st, P, false);
+  const auto plan_smem = [](int n_req) { return (size_t)(n_req + 1) * 2 * sizeof(long long); };
+  const size_t smem = plan_smem(p->n_req), most_smem = plan_smem(DSA_KV8_MAX_REQ);
+  const int rc1 = P.own_plan ? launch(plan_kernel<FEW_THREADS>, 1, FEW_THREADS, smem, most_smem, st, P, false)
+                             : launch(plan_kernel<PLAN_THREADS>, 1, PLAN_THREADS, smem, most_smem, st, P, false);
   if (rc1 != DSA_OK) return rc1;
   return p->d == 128 ? launch_all<128>(p, P, is_wide, st) : launch_all<64>(p, P, is_wide, st);
 }
