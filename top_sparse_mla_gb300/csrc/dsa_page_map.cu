@@ -240,9 +240,9 @@ extern "C" int dsa_page_map(const int32_t* ctx_lens, const int32_t* new_lens, in
   P.page = page_size;
   P.n_tokens = n_tokens;
   const size_t smem = (size_t)2 * (n_req + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {   // 48 KB are for dynamic and static shared memory together, and the latter is below 8 KB
     // raised on every call that needs it: it costs less than a microsecond, and only
-    // batches of more than 6143 requests come here
+    // batches of more than 5119 requests come here
     if (cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(2 * (DSA_PAGE_MAP_MAX_REQ + 1) * sizeof(int))) != cudaSuccess)
       return DSA_ERR_CUDA;
