@@ -116,3 +116,36 @@ def test_large_batches_from_several_host_threads():
     assert failed == [0] * len(calls)
     for c, _, out, lse, *_ in calls[:2]:
         c.check(out, lse)
+
+
+ROWS, ONE_CTA, CLUSTER, MANY = [(1, 300), (2, 700)], [(40, 384)], [(40, 1280)], [(9, 640)] * 70
+
+
+def _average(c):
+    """Values of 1 to 2, of which every output, an average of some of them, has to be one as well (2^-7: the rounding of
+    the weights to fp16 and of the result to bf16, 2^-11 + 2^-8 relative), and the logarithm of the sum of the weights has the
+    scores' size."""
+    values = np.random.default_rng(5).choice(np.arange(0x38, 0x41), c.vp.shape)   # the codes of 1, 1.125, .. 2
+    c.vp[:] = values
+    out, lse, status = c.run()
+    assert status == 0
+    a, b = int(c.cu[0]), int(c.cu[-1])
+    got = out[a:b].double().cpu().numpy()
+    low, high = got.min(), got.max()
+    assert low >= 1 - 2.0 ** -7 and high <= 2 + 2.0 ** -6, (low, high)   # NaN fails both
+    want = c.reference()[1][a:b]
+    assert np.abs(lse[a:b].double().cpu().numpy() - want).max() <= 2.0 ** -18 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER, MANY], ids=["rows", "one CTA", "cluster", "many tiles"])
+@pytest.mark.parametrize("mag", [2.0 ** 27, 2.0 ** 29, 2.0 ** 31, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("kind", ["high", "low", "both"])
+def test_scores_whose_steps_are_large(lens, mag, kind):
+    """The steps between fp32 values of these scores are powers of two that a weight cannot hold."""
+    c = _with_scores(81, lens, [-1.0 if kind == "low" else 1.0] * 1280, step_values=False, g=8, d=128, page=32)
+    c.scale = 0.7
+    c.q[:, :, 0] = mag
+    if kind == "both":
+        rng = np.random.default_rng(int(np.log2(mag)))
+        c.kp[..., 0] = rng.integers(0x30, 0x38, c.kp.shape[:3]) + 0x80 * rng.integers(0, 2, c.kp.shape[:3])
+    _average(c)

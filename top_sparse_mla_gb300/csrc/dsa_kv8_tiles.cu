@@ -554,8 +554,11 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
           // again below, and only this wait puts a tensor memory load behind a store
           tc_wait_st();
           const bool up = top > (fresh ? -INFINITY : LAG);
-          const float to_m = up ? floorf(m + top) : m;   // the largest weight is in [1, 2)
-          const float delta = to_m - m, f = (up && !fresh) ? ex2(-delta) : 1.0f;
+          // The largest weight is in [1, 2), and it is by delta that weights and sums are rescaled: from 2^23 on
+          // m + delta is rounded, and weights by m's rounded step (2^5 and more for scores from 2^28 on) would
+          // pass fp16's range.
+          const float delta = up ? floorf(top) : 0.f;
+          const float to_m = m + delta, f = (up && !fresh) ? ex2(-delta) : 1.0f;
           if (up) fresh = false;
           m = to_m;
           l *= f;
