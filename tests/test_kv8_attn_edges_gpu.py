@@ -149,3 +149,12 @@ def test_scores_whose_steps_are_large(lens, mag, kind):
         rng = np.random.default_rng(int(np.log2(mag)))
         c.kp[..., 0] = rng.integers(0x30, 0x38, c.kp.shape[:3]) + 0x80 * rng.integers(0, 2, c.kp.shape[:3])
     _average(c)
+
+
+@pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER], ids=["rows", "one CTA", "cluster"])
+def test_scores_far_below_zero(lens):
+    # every score is -0.7e32
+    c = _with_scores(80, lens, [-1.0] * 1280, step_values=False, g=8, d=128, page=32)
+    c.scale = 0.7
+    c.q[:, :, 0] = 1.0e32
+    _average(c)

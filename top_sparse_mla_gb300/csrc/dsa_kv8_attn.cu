@@ -20,6 +20,8 @@
 // l = sum w / v_scale is the softmax's sum: w is at most 2^8 (the maximum may lag by 8),
 // whatever the scales' magnitudes, so that it fits fp16.
 
+#include <float.h>
+
 #include "dsa_kv8.cuh"
 
 namespace dsa_kv8 {
@@ -37,7 +39,7 @@ constexpr int FEW_THREADS = 256;  // of the plan, where rows_kernel's CTAs find 
 // rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
 constexpr int ctas_per_sm(int d, int nt) { return (nt == 1 ? 4 : nt == 2 ? 3 : 2) + (d == 64 ? (nt == 1 ? 2 : 1) : 0); }
-constexpr float M_INIT = -1.0e30f;   // below every score, and finite: 2^(-inf - M_INIT) is 0
+constexpr float M_INIT = -FLT_MAX;   // below every score, and finite: 2^(-inf - M_INIT) is 0
 
 // the steps of each of a request's units with what a unit costs beside them; 0 for a
 // request that is not rows_kernel's

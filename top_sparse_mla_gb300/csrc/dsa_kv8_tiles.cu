@@ -32,6 +32,8 @@
 // weights that were looked at afterwards, and the part's weights formed once more, took a
 // 2123-token prefill, with its many short rows, 99.5 us against 94.9.)
 
+#include <float.h>
+
 #include <atomic>
 
 #include "dsa_kv8.cuh"
@@ -59,7 +61,7 @@ enum {
   B_SCALES = 20, B_DRAIN = 24,
   N_BAR = 26
 };
-constexpr float NOTHING = -1.0e30f;   // m of a piece in which a row saw nothing; its O is 0
+constexpr float NOTHING = -FLT_MAX;   // m of a piece in which a row saw nothing; its O is 0
 constexpr int N_SCALES = 4;      // blocks whose scales are kept: see copies()
 
 template <int D>
