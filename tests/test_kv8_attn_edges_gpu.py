@@ -158,3 +158,36 @@ def test_scores_far_below_zero(lens):
     c.scale = 0.7
     c.q[:, :, 0] = 1.0e32
     _average(c)
+
+
+@pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER, [(1, 9000)]], ids=["rows", "one CTA", "cluster", "many CTAs"])
+@pytest.mark.parametrize("scales", [[2.0 ** -64, 2.0 ** 64], [2.0 ** -63, 2.0 ** 40, 1.0, 2.0 ** 64], [2.0 ** -33, 2.0 ** -32, 2.0 ** 64]],
+                         ids=["ends", "spread", "border"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_value_scales_far_apart(lens, scales, d):
+    """A token's share of the softmax's sum does not depend on its page's value scale."""
+    _check(Case(82, lens, h=1, g=8, d=d, page=16, v_scale=scales, q_mag=0.5))
+
+
+@pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER], ids=["rows", "one CTA", "cluster"])
+def test_value_scales_that_rise_or_fall(lens):
+    """Pages of the least scale, then of the largest, and the other way round: the sum is rescaled by 2^-128, or gains so little."""
+    for order in (1, -1):
+        c = Case(83, lens, h=1, g=8, d=128, page=16, poison=False, q_mag=0.5)
+        for r, (_, kv) in enumerate(lens):
+            for j in range(-(-kv // 16)):
+                c.vs[c.table[r, j]] = 2.0 ** (64 * order * (1 if j >= kv // 32 else -1))
+        _check(c)
+
+
+@pytest.mark.parametrize("lens", [[(2, 700), (1, 300)] * 8, [(40, 700), (3, 1200)], [(33, 2100)], [(9, 640), (20, 700)] * 80],
+                         ids=["rows", "tiles", "cluster", "many tiles"])
+def test_value_scales_far_apart_under_a_window_and_in_some_requests(lens):
+    """Every third request has value scales far apart: units with and without them follow one another."""
+    c = Case(85, lens, h=2, g=8, d=64, page=32, window=333, poison=False, q_mag=0.5, v_scale=[1.0, 2.0])
+    rng = np.random.default_rng(6)
+    for r, (_, kv) in enumerate(lens):
+        if r % 3 == 0:
+            for j in range(-(-kv // 32)):
+                c.vs[c.table[r, j]] = rng.choice(np.array([2.0 ** -64, 2.0 ** -40, 1.0, 2.0 ** 63], np.float32), 2)
+    _check(c)

@@ -17,8 +17,8 @@
 // Scales.  With S = q . code_k summed in fp32 and x = S * k_scale * softmax_scale * log2 e,
 // the kernels take t = x + log2(v_scale) and w = 2^(t - m), m a running maximum of t.  Then
 // O = sum w * code_v is the weighted sum with every page's value scale in it, and
-// l = sum w / v_scale is the softmax's sum: w is at most 2^8 (the maximum may lag by 8),
-// whatever the scales' magnitudes, so that it fits fp16.
+// l = sum w / v_scale is the softmax's sum (see SMALL_SCALE): w is at most 2^8 (the maximum may
+// lag by 8), whatever the scales' magnitudes, so that it fits fp16.
 
 #include <float.h>
 
@@ -409,8 +409,9 @@ __device__ __forceinline__ void rows_steps(const Params& P, Steps<D>& W, int see
           if (j < seen_lo || j >= hi) C.v[i] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      // the running maximum, moved only when a score passes it by 2^LAG
-      bool up = false;
+      // the running maximum, moved only when a score passes it by 2^LAG, and for every page of a small
+      // value scale, whose part of the sum is formed there
+      bool up = vsc < SMALL_SCALE;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -425,13 +426,20 @@ __device__ __forceinline__ void rows_steps(const Params& P, Steps<D>& W, int see
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
             f[e] = ex2(R.m[nt][e] - t);
+            R.l[nt][e] = scaled(R.l[nt][e], R.m[nt][e] - t);
             R.m[nt][e] = t;
-            R.l[nt][e] *= f[e];
           }
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) R.o[nt][mt][e] *= f[e & 1];
+        }
+        if (vsc < SMALL_SCALE) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R.l[nt][e & 1] += ex2(x[nt][e] - R.m[nt][e & 1] - bias);
+          vinv = 0.f;
         }
       }
       uint32_t pf[NT][2];
@@ -642,7 +650,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
       o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z);
       o.w = fmaf(v.w, f, o.w);
-      l = fmaf(S.l[x][row], f, l);
+      l += scaled(S.l[x][row], S.m[x][row] - m);
     }
     if (pieces == 1) {
       write(row, k4, o, m, l);
@@ -681,7 +689,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
           for (int x = 0; x < 8; ++x) top = fmaxf(top, pm[x]);
           const float f0 = ex2(m - top);
           o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
-          l *= f0;
+          l = scaled(l, m - top);
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const float f = ex2(pm[x] - top);
@@ -689,7 +697,7 @@ __device__ __forceinline__ void rows_unit(const Params& P, RowSmem<D, NT, NW>& S
             o.y = fmaf(po[x].y, f, o.y);
             o.z = fmaf(po[x].z, f, o.z);
             o.w = fmaf(po[x].w, f, o.w);
-            l = fmaf(pl[x], f, l);
+            l += scaled(pl[x], pm[x] - top);
           }
           m = top;
         }

@@ -26,7 +26,7 @@
 // cluster meet by its barrier, at which each of their threads comes by whatever way.
 //
 // Scores become u = S * (k_scale * softmax_scale * log2 e * row scaling) + (log2 v_scale - m)
-// and weights 2^u, with m an integer that was the row's maximum, rounded down, when it was
+// and weights 2^u (their sum: see FAR_APART), with m an integer that was the row's maximum, rounded down, when it was
 // last set.  It is set anew, and O rescaled by a power of two, exactly, when a weight would
 // pass 2^15, so that each fits fp16.  That is rare behind the first block.  (Sums of 64
 // weights that were looked at afterwards, and the part's weights formed once more, took a
@@ -82,7 +82,7 @@ struct Ctx {
   uint8_t* sm;
   uint32_t sb, bars;
   volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2], [3]: groups of the K
-                        // and V codes that have a page
+                        // and V codes that have a page, [4], [5]: whether a half's unit has value scales far apart
   uint32_t* status;
 };
 
@@ -197,7 +197,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
       const int j = x.t.lo + i * BLOCK + 16 * grp;
       return (i < blocks && j < x.t.hi) ? __ldg(table + (j >> P.page_shift)) : -1;
     };
-    float ks = 1.f, vs = 1.f;
+    float ks = 1.f, vs = 1.f, least = FLT_MAX, most = 0.f;   // of this lane's groups
     auto load_scales = [&](int raw) {
       if (lane < 8 && raw >= 0 && raw < P.n_pages) {
         ks = __ldg(P.k_scale + (long long)raw * P.h_kv + x.head);
@@ -217,10 +217,18 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
       for (int kv = 0; kv < 2; ++kv) {
         if (!(ok = wait_w(c, B_RAWFREE + kv, (g & 1) ^ 1))) break;
         if (kv == 0) {
+          if (there && lane < 8) {
+            least = fminf(least, bounded_scale(vs));
+            most = fmaxf(most, bounded_scale(vs));
+          }
+          // whether the unit's value scales up to here are far apart
+          const float lo = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(least)));
+          const float hi = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
+          const float apart = hi > lo * FAR_APART ? 1.f : 0.f;
           if (lane < 8) {
             const float v = bounded_scale(vs);
             reinterpret_cast<float4*>(c.sm + SM::SCALES)[(g % N_SCALES) * 8 + lane] =
-                there ? make_float4(ks * P.scale_log2, log2f(v), 1.0f / v, 0.f) : make_float4(0.f, -INFINITY, 1.f, 0.f);
+                there ? make_float4(ks * P.scale_log2, log2f(v), 1.0f / v, apart) : make_float4(0.f, -INFINITY, 1.f, apart);
           }
           arrive_w(c, B_SCALES + g % N_SCALES);
           load_scales(raw_next);
@@ -318,6 +326,12 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
   }
 }
 
+DSA_DEV uint32_t ld_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------------------ products
 // The whole warp runs this role and one elected lane issues each product: with
 // warp-uniform control flow the descriptors stay in uniform registers.
@@ -358,7 +372,14 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
             for (int k = 0; k < BLOCK / 16; ++k)
               mma_ts(tmem + TM::O + D * h, tmem + TM::S + 128 * h + 8 * k,
                      d_v + ((uint32_t)(vb * SM::OPERAND + k * 2048) >> 4), ID_PV, (i > 1 || k > 0) ? 1u : 0u);
-            if (!qk) tc_commit(bar(c, B_OFULL + h));
+            if (!qk) {
+              // from the half's last block, whose scales stay until these products are done.  (Read by the
+              // softmax with every block it took 0.5 % longer; a branch in its loop, 5 %.)
+              const uint32_t at = c.sb + SM::SCALES + (g + i - 1) % N_SCALES * 128 + 12;
+              c.misc[4 + h] = ld_shared(at) != 0;
+              mbar_arrive(bar(c, B_OFULL + h));
+              tc_commit(bar(c, B_OFULL + h));
+            }
           }
           if (qk) {
 #pragma unroll
@@ -471,6 +492,37 @@ DSA_DEV float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+// The sum of 2^(score - m) over what a row sees of a unit's blocks, each score formed anew from the
+// row's queries in shared memory and the codes: for a unit whose value scales are far apart.
+template <int D>
+DSA_DEV float plain_sum(const Params& P, const Unit& x, const uint8_t* tile, int row_in, int blocks, int pos, float row_scale,
+                        float m) {
+  const int32_t* table = P.table + x.t.req * P.table_ld;
+  const int end = min(min(x.t.lo + blocks * BLOCK, x.t.hi), pos + 1);
+  float sum = 0.f;
+  for (int j = P.window > 0 ? max(x.t.lo, pos - P.window + 1) : x.t.lo; j < end; ++j) {
+    const int page = __ldg(table + (j >> P.page_shift));
+    if (page < 0 || page >= P.n_pages) continue;
+    const uint32_t unit = (uint32_t)page * P.h_kv + x.head;
+    const uint32_t row = (unit << P.page_shift) + (j & ((1 << P.page_shift) - 1));
+    const uint8_t* k = P.k_pool + (uint64_t)row * D;
+    float dot = 0.f;
+#pragma unroll 1
+    for (int c8 = 0; c8 < D / 8; ++c8) {
+      const uint2 codes = ldg_nc_v2(k + 8 * c8);
+      const uint4 q = *reinterpret_cast<const uint4*>(tile + (c8 >> 3) * (BLOCK * 128) + row_in * 128 + (((c8 ^ row_in) & 7) << 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t h2 = e4m3x2_to_f16x2(((e < 2 ? codes.x : codes.y) >> (16 * (e & 1))) & 0xFFFFu);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h2)), b = unpack(word(q, e), 1);
+        dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+      }
+    }
+    sum += ex2(fmaf(dot, __ldg(P.k_scale + unit) * P.scale_log2 * row_scale, -m));
+  }
+  return sum;
 }
 
 // Returns whether the CTA's cluster has met (SPLIT).
@@ -618,6 +670,8 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       if (!wait_w(c, B_OFULL + h, no & 1)) return met;
       ++no;
       tc_fence_after();
+      if (c.misc[4 + h])
+        l = live ? plain_sum<D>(P, x, c.sm + SM::Q + h * SM::OPERAND, row_in, mine, pos, row_scale, m) : 0.f;
     }
     uint16_t* dst = P.out + (x.t.q0 + qi) * P.out_ld + head * P.out_hd;
     auto write = [&](int k, const float* o, float inv) {   // 8 dims
@@ -669,7 +723,7 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       l = 0.f;
       for (int p = 0; p < x.pieces; ++p) {
         const uint32_t from = at_rank(s_ml, p) + 4 * row_in;
-        l = fmaf(ld_cluster(from + 512), ex2(ld_cluster(from) - m), l);
+        l += scaled(ld_cluster(from + 512), ld_cluster(from) - m);
       }
       const float inv = inverse(l);
       const int c0 = D / 8 * x.piece / x.pieces, c1 = D / 8 * (x.piece + 1) / x.pieces;
@@ -715,7 +769,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
       mbar_init(bar(c, B_SFULL + i), 1);
       mbar_init(bar(c, B_PFULL + i), 4);
       mbar_init(bar(c, B_QFULL + i), 4);
-      mbar_init(bar(c, B_OFULL + i), 1);
+      mbar_init(bar(c, B_OFULL + i), 2);
       mbar_init(bar(c, B_RAWFULL + i), 1);
       mbar_init(bar(c, B_RAWFREE + i), 4);
     }
