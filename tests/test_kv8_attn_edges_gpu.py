@@ -191,3 +191,28 @@ def test_value_scales_far_apart_under_a_window_and_in_some_requests(lens):
             for j in range(-(-kv // 32)):
                 c.vs[c.table[r, j]] = rng.choice(np.array([2.0 ** -64, 2.0 ** -40, 1.0, 2.0 ** 63], np.float32), 2)
     _check(c)
+
+
+@pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER, MANY], ids=["rows", "one CTA", "cluster", "many tiles"])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite_and_see_no_page(lens, what):
+    """A row that sees nothing is 0 with an lse of -inf, whatever its query holds."""
+    c = Case(84, lens, h=1, g=8, d=128, page=32)
+    c.table[:] = -1
+    c.q[:, ::3] = what
+    _check(c)
+
+
+@pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER, MANY], ids=["rows", "one CTA", "cluster", "many tiles"])
+def test_queries_that_are_not_finite_leave_other_rows_alone(lens):
+    """A row with a NaN that sees something is NaN, and the others are within the error bound."""
+    c = Case(86, lens, h=1, g=8, d=128, page=32)
+    c.q[:, 2::3, 5] = float("nan")
+    out, lse, status = c.run()
+    c.q[:, 2::3, 5] = 1.0
+    want, want_lse, _ = c.run()
+    assert status == 0
+    a, b = int(c.cu[0]), int(c.cu[-1])
+    assert out[a:b, 2::3].isnan().all() and lse[a:b, 2::3].isnan().all()
+    out[a:b, 2::3], lse[a:b, 2::3] = want[a:b, 2::3], want_lse[a:b, 2::3]
+    c.check(out, lse)

@@ -430,13 +430,28 @@ DSA_DEV const uint16_t* shfl_ptr(const uint16_t* p, int from) {
   return reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(p), from));
 }
 
+// Whether a row sees a cached token of a unit's blocks.
+DSA_DEV bool sees_any(const Params& P, const Unit& x, int blocks, int pos) {
+  const int32_t* table = P.table + x.t.req * P.table_ld;
+  const int end = min(min(x.t.lo + blocks * BLOCK, x.t.hi), pos + 1);
+  const int first = P.window > 0 ? max(x.t.lo, pos - P.window + 1) : x.t.lo;
+  for (int j = first & ~(STEP - 1); j < end; j += STEP) {   // a step lies in one page
+    const int page = __ldg(table + (j >> P.page_shift));
+    if (page >= 0 && page < P.n_pages) return true;
+  }
+  return false;
+}
+
 // Scales the warp's 32 rows of queries to fp16 and writes them into a half's tile.  `mine`
 // is this lane's row, null for one that is not there, and `row0` the warp's first row of
 // the tile.  Returns what undoes the scaling of this lane's row.  Lanes side by side read
 // neighbours of a row: a lane for a row touches 32 lines with every load, which took a
 // 2123-token prefill 109 us in place of 104.
+//
+// A query that is not finite makes its row NaN, also by way of missing pages (0 * NaN); where the
+// row sees nothing it has to be 0, and the query is taken as 0.
 template <int D, bool FP16>
-DSA_DEV float queries(const uint16_t* mine, uint32_t tile, int row0) {
+DSA_DEV float queries(const Params& P, const Unit& x, int blocks, int pos, const uint16_t* mine, uint32_t tile, int row0) {
   constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;   // lanes of a row, rows of a load; LANES loads
   const int lane = threadIdx.x & 31, sub = lane / LANES, chunk = lane % LANES;
   uint4 v[LANES];
@@ -458,7 +473,16 @@ DSA_DEV float queries(const uint16_t* mine, uint32_t tile, int row0) {
       mx[j] = __vmaxu2(high ? mx[j + n] : mx[j], __shfl_xor_sync(0xFFFFFFFFu, high ? mx[j] : mx[j + n], n));
     }
   float back;
-  const float down = row_scaling(unpack(max(mx[0] >> 16, mx[0] & 0xFFFFu), FP16).x, back);
+  const uint32_t largest = max(mx[0] >> 16, mx[0] & 0xFFFFu);
+  const int holder = lane / AT_ONCE + lane % AT_ONCE * LANES;   // of what belongs to this lane's row
+  const bool finite = largest < (FP16 ? 0x7C00u : 0x7F80u);
+  if (!__all_sync(0xFFFFFFFFu, finite)) {
+    const bool none = !__shfl_sync(0xFFFFFFFFu, finite, holder) && !sees_any(P, x, blocks, pos);
+#pragma unroll
+    for (int t = 0; t < LANES; ++t)
+      if (__shfl_sync(0xFFFFFFFFu, none, AT_ONCE * t + sub)) v[t] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const float down = row_scaling(unpack(largest, FP16).x, back);
   const uint32_t at = tile + (chunk >> 3) * (BLOCK * 128) + (row0 + sub) * 128;
 #pragma unroll
   for (int t = 0; t < LANES; ++t) {
@@ -471,7 +495,7 @@ DSA_DEV float queries(const uint16_t* mine, uint32_t tile, int row0) {
     }
     sts128(at + AT_ONCE * t * 128 + (((chunk ^ (AT_ONCE * t + sub)) & 7) << 4), make_uint4(p[0], p[1], p[2], p[3]));
   }
-  return __shfl_sync(0xFFFFFFFFu, back, lane / AT_ONCE + lane % AT_ONCE * LANES);
+  return __shfl_sync(0xFFFFFFFFu, back, holder);
 }
 
 DSA_DEV void cluster_meet() {
@@ -553,7 +577,8 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
     if (!SPLIT || mine > 0) {
       const uint16_t* src = live ? P.q + (x.t.q0 + qi) * P.q_ld + head * P.q_hd : nullptr;
       const uint32_t tile = c.sb + SM::Q + h * SM::OPERAND;
-      row_scale = P.fp16 ? queries<D, true>(src, tile, row_in & ~31) : queries<D, false>(src, tile, row_in & ~31);
+      row_scale = P.fp16 ? queries<D, true>(P, x, mine, pos, src, tile, row_in & ~31)
+                         : queries<D, false>(P, x, mine, pos, src, tile, row_in & ~31);
       fence_async_smem();
       tc_fence_before();   // this half's O was read before
       arrive_w(c, B_QFULL + h);
