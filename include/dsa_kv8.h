@@ -15,7 +15,7 @@
  * slots[i] < 0 skips it (padding).  The new tokens of one page are a run: consecutive
  * tokens of the batch with consecutive slots, as dsa_page_map numbers them.  Let the run
  * begin at row o0 of its page, and let amax be the largest magnitude among the run's
- * values of one head.  For each page and head, keys and values apart:
+ * finite values of one head (0 if there is none).  For each page and head, keys and values apart:
  *   - s = the least power of two with amax <= 448 s, within [2^-64, 2^64];
  *   - with o0 > 0 the rows before o0 are tokens that the page holds already: s is raised
  *     to the page's scale if that is larger, and where s is larger than the page's scale
@@ -26,7 +26,7 @@
  *     filled, but for values below 2^-6 s that were rounded at an earlier scale.
  * With o0 == 0 the page's old contents are forgotten.  Rows behind the run and other
  * pages are left as they were.  Non-finite inputs: an infinity saturates, a NaN gives the
- * E4M3 NaN code and does not change the scale.  If two runs of one call share a page, or
+ * E4M3 NaN code, and neither changes the scale.  If two runs of one call share a page, or
  * a slot occurs twice, that page's codes and scale are unspecified (nothing else is).
  *   k, v    bf16 or fp16 (`type`) [n_tokens][h_kv][d]: token pitch ld and head pitch hd in
  *           elements, both multiples of 8, hd >= d unless h_kv == 1; 16-byte aligned

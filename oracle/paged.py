@@ -72,7 +72,8 @@ def kv8_insert(pool, scale, x, slots):
             j += 1
         pg, o0 = divmod(int(slots[i]), page)
         for hh in range(h):
-            s = page_scale(float(np.max(np.abs(x[i:j, hh]))))
+            run = np.abs(x[i:j, hh])
+            s = page_scale(float(np.max(run, initial=0.0, where=np.isfinite(run))))
             old = float(scale[pg, hh])
             if o0 > 0 and old >= s:
                 s = old

@@ -59,6 +59,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// magnitudes of two values, a NaN for an infinity: |x| * 0 + |x|
+template <bool FP16>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
+  uint32_t r;
+  if (FP16) asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %1;\n\tfma.rn.f16x2 %0, a, %2, a;\n\t}" : "=r"(r) : "r"(w), "r"(0u));
+  else asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %1;\n\tfma.rn.bf16x2 %0, a, %2, a;\n\t}" : "=r"(r) : "r"(w), "r"(0u));
+  return r;
+}
+
 // E4M3 codes of f * s (two products in one instruction)
 __device__ __forceinline__ uint32_t scaled_codes(float2 f, float s) {
   uint64_t v, m;
@@ -154,8 +163,8 @@ __global__ void __launch_bounds__(THREADS, PASSES * D <= 1024 ? 4 : 2) insert_ke
     uint32_t m2 = 0u;   // of the tokens since the last run's end
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      constexpr uint32_t ABS = 0x7FFF7FFFu;
-      m2 = max2<FP16>(m2, max2<FP16>(max2<FP16>(x[p].x & ABS, x[p].y & ABS), max2<FP16>(x[p].z & ABS, x[p].w & ABS)));
+      m2 = max2<FP16>(m2, max2<FP16>(max2<FP16>(magnitudes<FP16>(x[p].x), magnitudes<FP16>(x[p].y)),
+                                     max2<FP16>(magnitudes<FP16>(x[p].z), magnitudes<FP16>(x[p].w))));
       // on to the next token, unless a run of the warp's ends here
       if (p + 1 < PASSES && __all_sync(0xFFFFFFFFu, to[p + 1 < PASSES ? p + 1 : p].y == to[p].y)) continue;
       const bool some = to[p].x != NONE;
