@@ -11,8 +11,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 from .build import LIB_PATH
 
 DSA_OK = 0
@@ -201,12 +199,26 @@ def _ptr(x):
     return x.data_ptr()
 
 
-# torch.cuda.current_stream() builds a Stream object, which takes longer than a launch
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# Bound by _bind_torch at the first call that needs them: a program that passes pointers and a
+# stream of its own needs no torch.
+torch = _raw_stream = _I32 = _I64 = _F32 = _U8 = None
+_KV8_TYPES = {}
+
+
+def _bind_torch() -> None:
+    global torch, _raw_stream, _I32, _I64, _F32, _U8
+    import torch as module
+    # torch.cuda.current_stream() builds a Stream object, which takes longer than a launch
+    _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", None)
+    _I32, _I64, _F32, _U8 = module.int32, module.int64, module.float32, module.uint8
+    _KV8_TYPES.update({module.bfloat16: DSA_KV8_BF16, module.float16: DSA_KV8_FP16})
+    torch = module
 
 
 def _stream(stream):
     if stream is None:
+        if torch is None:
+            _bind_torch()
         if _raw_stream is not None:
             return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
@@ -276,15 +288,14 @@ def dsa_kv_insert(kv, positions, slots, kv_norm_w, pool, rms_eps: float = 1e-6, 
         raise DsaError(rc, "dsa_kv_insert")
 
 
-_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
-
-
 def _refuse(where: str, what: str) -> None:
     raise DsaError(DSA_ERR_INVALID_ARG, f"{where}: {what}")
 
 
 def _device(where: str, x) -> int:
     """The current CUDA device, where the library launches; x has to be on it."""
+    if torch is None:
+        _bind_torch()
     dev = x.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         _refuse(where, "every tensor must be on the current CUDA device")
@@ -353,9 +364,6 @@ def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu
         raise DsaError(rc, where)
 
 
-_KV8_TYPES = {torch.bfloat16: DSA_KV8_BF16, torch.float16: DSA_KV8_FP16}
-
-
 def _kv8_pools(where, dev, k_pool, v_pool, k_scale, v_scale):
     shape = k_pool.shape
     if len(shape) != 4:
@@ -399,6 +407,8 @@ def dsa_kv8_params_init(q, k_pool, block_table, max_q_len=None, **overrides) -> 
     [n_req, cols]. max_q_len: most query rows of a request (default: n_tokens);
     overrides: window, softmax_scale."""
     where = "dsa_kv8_params_init"
+    if torch is None:
+        _bind_torch()
     if (q.dim() != 3 or k_pool.dim() != 4 or block_table.dim() != 2 or q.dtype not in _KV8_TYPES
             or q.shape[2] != k_pool.shape[3]):
         _refuse(where, "q, k_pool and block_table do not belong together")
