@@ -49,7 +49,8 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         jobs = [(src, os.path.join(objs, os.path.basename(src) + ".o")) for src in SOURCES]
         with ThreadPoolExecutor(len(jobs)) as pool:
             list(pool.map(lambda job: _run([nvcc, *flags, "-c", "-o", job[1], job[0]], verbose), jobs))
-        _run([nvcc, *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *[obj for _, obj in jobs]], verbose)
+        _run([nvcc, *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *[obj for _, obj in jobs], *(extra_flags or [])],
+             verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
