@@ -49,9 +49,7 @@ constexpr int W_DQ = 8, W_MMA = 12, W_COPY = 13, TILE_THREADS = 16 * 32;   // wa
 // is what 16 warps of 128 were launched with.
 constexpr int LAUNCH_REGS = 128, SOFTMAX_REGS = 152, OTHER_REGS = 104;
 static_assert(SOFTMAX_REGS + OTHER_REGS == 2 * LAUNCH_REGS, "more registers than the CTA has would be waited for");
-// ~10 s at 2 GHz: the group of a half that a CTA's units do not have waits through them,
-// which with contexts of a million tokens may be hundreds of milliseconds
-constexpr unsigned long long WAIT_LIMIT_CYCLES = 20000000000ull;
+constexpr unsigned long long WAIT_LIMIT_CYCLES = 20000000000ull;   // ~10 s at 2 GHz
 
 // barriers
 enum {
@@ -82,7 +80,8 @@ struct Ctx {
   uint8_t* sm;
   uint32_t sb, bars;
   volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2], [3]: groups of the K
-                        // and V codes that have a page, [4], [5]: whether a half's unit has value scales far apart
+                        // and V codes that have a page, [4], [5]: whether a half's unit has value scales far apart,
+                        // [6]: unit whose codes are being copied, [7]: blocks copied
   uint32_t* status;
 };
 
@@ -110,6 +109,29 @@ DSA_DEV bool wait_slow(uint32_t addr, uint32_t parity, volatile int* misc, uint3
 DSA_DEV bool wait_w(const Ctx& c, int b, uint32_t parity) {
   const uint32_t addr = bar(c, b);
   const bool ok = mbar_try(addr, parity) || wait_slow(addr, parity, c.misc, c.status);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Waits until unit u is being copied, or all are: for the group of a half that the unit before does
+// not have.  Such units may take longer than any other wait, so this one's limit is from the last
+// progress on.
+DSA_DEV bool wait_unit(const Ctx& c, uint32_t u) {
+  unsigned long long start = clock64();
+  int blocks = c.misc[7];
+  bool ok = true;
+  while (ok && (int)(u - (uint32_t)c.misc[6]) > 0) {
+    __nanosleep(100);
+    ok = c.misc[1] == 0;
+    if (c.misc[7] != blocks) {
+      blocks = c.misc[7];
+      start = clock64();
+    }
+    if (ok && clock64() - start > WAIT_LIMIT_CYCLES) {
+      atomicOr(c.status, DSA_STATUS_WAIT_TIMEOUT);
+      c.misc[1] = 1;
+      ok = false;
+    }
+  }
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
@@ -187,11 +209,12 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   constexpr uint32_t GROUP_BYTES = 16 * D;
   const int lane = threadIdx.x & 31, grp = lane & 7;
   const int page_mask = (1 << P.page_shift) - 1;
-  uint32_t g = 0;
+  uint32_t g = 0, u = 0;
   bool ok = true;
   Unit x;
-  for (uint32_t u = 0; ok && unit<SPLIT>(P, u, n_tiles, x); ++u) {
+  for (; ok && unit<SPLIT>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
+    if (lane == 0) c.misc[6] = (int)u;
     const int32_t* table = P.table + x.t.req * P.table_ld;
     auto entry = [&](int i) -> int {
       const int j = x.t.lo + i * BLOCK + 16 * grp;
@@ -236,6 +259,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
         const uint32_t full = bar(c, B_RAWFULL + kv);
         if (lane == 0) {
           c.misc[2 + kv] = (int)mask;
+          c.misc[7] = (int)g;
           asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(full),
                        "r"((uint32_t)__popc(mask) * GROUP_BYTES)
                        : "memory");
@@ -254,6 +278,7 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
       raw_next = raw_after;
     }
   }
+  if (lane == 0) c.misc[6] = (int)u;
   if (!ok) {
     // gave up: wait, with a limit, for the copies in flight.  Block g's keys were issued if
     // the values' wait ran out; both buffers' last copies belong to block g or g - 1.
@@ -564,6 +589,7 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
     const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
     if (!(h == 0 ? x.rows[0] : x.rows[1]) || (SPLIT && x.piece >= x.pieces)) {
       g += blocks;
+      if (!SPLIT && !wait_unit(c, u + 1)) return met;
       continue;
     }
     const int first = x.t.row0 + 128 * h, row = first + row_in;
@@ -801,7 +827,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
     for (int i = 0; i < N_SCALES; ++i) mbar_init(bar(c, B_SCALES + i), 1);
     mbar_init(bar(c, B_DRAIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    c.misc[1] = 0;
+    c.misc[1] = c.misc[6] = c.misc[7] = 0;
   }
   if (warp == W_MMA) tmem_alloc(c.sb + SM::MISC, Tmem<D>::COLS);
   tc_fence_before();
