@@ -101,6 +101,13 @@ extern "C" {
 #define DSA_KV8_MAX_HEADS 1024          /* KV heads */
 #define DSA_KV8_MAX_GROUP 128           /* query heads per KV head */
 #define DSA_KV8_MAX_REQ 8192            /* requests of one attention call */
+/* For tests of the failure path only: CTA 0 of the kernel that serves requests of many query
+ * rows (more than 32 with their heads, by KV head) stops copying after three blocks of 128
+ * cached tokens and waits for what nothing completes.  That wait runs out (about 1 s), the
+ * call's status gets DSA_STATUS_WAIT_TIMEOUT, and every role of the CTA stops, drains the
+ * tensor core and frees its tensor memory.  Rows that the CTA did not finish are unwritten
+ * or, where a cluster shares them, unspecified; the others are complete. */
+#define DSA_KV8_FLAG_TEST_WAIT_TIMEOUT 2u
 #define DSA_STATUS_QUERY_TOO_LONG 64u   /* a request had more than max_q_len query rows */
 
 int dsa_kv8_insert(const void* k, int64_t k_ld, int64_t k_hd, const void* v, int64_t v_ld, int64_t v_hd,
@@ -121,7 +128,7 @@ typedef struct dsa_kv8_params {
   int32_t window;       /* 0: none */
   int32_t type;         /* DSA_KV8_BF16 or DSA_KV8_FP16 */
   float softmax_scale;  /* finite; e.g. 1/sqrt(d) */
-  uint32_t flags;       /* 0 */
+  uint32_t flags;       /* 0, or DSA_KV8_FLAG_TEST_WAIT_TIMEOUT */
 } dsa_kv8_params;
 
 /* Fill `p` for the given shape: max_q_len = n_tokens, window 0, softmax_scale 1/sqrt(d),

@@ -63,6 +63,7 @@ struct Params {
   int n_shares, max_tiles, n_ctas;   // n_ctas: of the tiles' kernel
   int has_tiles;    // whether requests may have more rows than rows_kernel takes
   int cluster;      // CTAs that share a tile and KV head; 0: a CTA has several of them
+  uint32_t test_block;   // block of CTA 0 at which the copies stop (DSA_KV8_FLAG_TEST_WAIT_TIMEOUT)
   float scale_log2;   // softmax_scale * log2 e
 };
 

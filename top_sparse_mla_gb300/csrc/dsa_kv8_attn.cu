@@ -832,7 +832,8 @@ static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 static int check(const dsa_kv8_params* p) {
   if (!p || p->n_tokens < 0 || p->n_tokens > (1 << 30) || p->n_req < 0 || p->h_q < 1 || p->h_kv < 1 ||
       p->h_q % p->h_kv != 0 || p->n_pages < 0 || p->table_cols < 0 || p->max_q_len < 0 || p->window < 0 ||
-      (p->type != DSA_KV8_BF16 && p->type != DSA_KV8_FP16) || !isfinite(p->softmax_scale) || p->flags != 0)
+      (p->type != DSA_KV8_BF16 && p->type != DSA_KV8_FP16) || !isfinite(p->softmax_scale) ||
+      (p->flags & ~DSA_KV8_FLAG_TEST_WAIT_TIMEOUT) != 0)
     return DSA_ERR_INVALID_ARG;
   if ((p->d != 64 && p->d != 128) ||
       (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) ||
@@ -1049,6 +1050,7 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   // the requests of a thread where the CTAs find their shares for themselves; 0: the plan kernel does
   P.own_plan = p->n_req <= OWN_PLAN * 32 * warps ? (p->n_req + 32 * warps - 1) / (32 * warps) : 0;
   P.max_tiles = L.max_tiles;
+  P.test_block = p->flags & DSA_KV8_FLAG_TEST_WAIT_TIMEOUT ? 3u : 0xFFFFFFFFu;
   P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   const auto plan_smem = [](int n_req) { return (size_t)(n_req + 1) * 2 * sizeof(long long); };
   const size_t smem = plan_smem(p->n_req), most_smem = plan_smem(DSA_KV8_MAX_REQ);

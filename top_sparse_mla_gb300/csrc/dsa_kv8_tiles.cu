@@ -135,6 +135,16 @@ DSA_DEV bool wait_unit(const Ctx& c, uint32_t u) {
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// For tests of the failure path: a wait that runs out, after an eighth of the limit.
+DSA_DEV bool wait_in_vain(const Ctx& c) {
+  const unsigned long long start = clock64();
+  while (!mbar_wait_susp(bar(c, B_DRAIN), 0) && clock64() - start < WAIT_LIMIT_CYCLES / 8) {
+  }
+  atomicOr(c.status, DSA_STATUS_WAIT_TIMEOUT);
+  c.misc[1] = 1;
+  return false;
+}
+
 DSA_DEV bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -230,6 +240,10 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
     int raw = entry(0), raw_next = entry(1);
     load_scales(raw);
     for (int i = 0; i < blocks; ++i, ++g) {
+      if (g == P.test_block && blockIdx.x == 0) {
+        ok = wait_in_vain(c);
+        break;
+      }
       const int raw_after = entry(i + 2);
       const bool there = raw >= 0 && raw < P.n_pages;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there && lane < 8);
