@@ -15,7 +15,8 @@
  * slots[i] < 0 skips it (padding).  The new tokens of one page are a run: consecutive
  * tokens of the batch with consecutive slots, as dsa_page_map numbers them.  Let the run
  * begin at row o0 of its page, and let amax be the largest magnitude among the run's
- * finite values of one head (0 if there is none).  For each page and head, keys and values apart:
+ * finite values of one head (0 if there is none).  For each page and head, keys and values
+ * apart:
  *   - s = the least power of two with amax <= 448 s, within [2^-64, 2^64];
  *   - with o0 > 0 the rows before o0 are tokens that the page holds already: s is raised
  *     to the page's scale if that is larger, and where s is larger than the page's scale
@@ -64,13 +65,18 @@
  * The workspace needs no initialisation and holds the status word of the last call
  * (dsa_sparse_attn_read_status reads it).  Calls that share a workspace must not overlap
  * on the GPU.  Results do not depend on the other requests' order of completion: the same
- * inputs give the same bits.
+ * inputs give the same bits.  On-chip waits are bounded: where one runs out (10 s without an
+ * end), the status gets DSA_STATUS_WAIT_TIMEOUT and rows are missing or wrong.
  *
  * Numerics: E4M3 codes are exact in fp16, and so are the queries after each row's scaling
- * by a power of two (values below 2^-30 of the row's largest are rounded); products
- * accumulate in fp32; scores, the running maximum and sums are fp32.  The softmax weights
- * are rounded to fp16 (2^-12 relative, and 2^-25 of the row's largest weight) for the
- * product with the values, not for their sum.
+ * by a power of two, down to 2^-22 (fp16) or 2^-25 (bf16) of the row's largest magnitude;
+ * smaller ones are rounded, by at most 2^-32 of the largest.  Products accumulate in fp32;
+ * scores, the running maximum and sums are fp32.  For the product with the values, not for
+ * their sum, the softmax weight p_j of a token times its page's value scale is rounded to
+ * fp16: by 2^-11 relative, or by 2^-25 of the largest p_j * v_scale_j of the row where that
+ * is more.  So out's error beside its own rounding is at most 2^-11 sum_j p_j |v_j| and
+ * 2^-25 max_j(p_j * v_scale_j) sum_j |code_j|: a page whose value scale is far below another's
+ * that the row sees counts with fewer bits, in dims where the other page's values are small.
  *
  * Both calls are asynchronous on `stream` (a cudaStream_t, NULL = legacy default stream),
  * allocate nothing and can be captured in a CUDA graph.  They return DSA_OK, or one of the
@@ -81,7 +87,9 @@
  *     table_cols * page_size <= 2^30);
  *   - DSA_ERR_WORKSPACE_TOO_SMALL (attention);
  *   - DSA_ERR_UNSUPPORTED_DEVICE: not compute capability 10.3;
- *   - DSA_ERR_CUDA.
+ *   - DSA_ERR_CUDA: a CUDA call failed, or the library was built such that the kernel for
+ *     many query rows did not get the 128 registers a thread that its roles redistribute
+ *     (with another compiler, or flags for debugging).
  */
 #ifndef DSA_KV8_H_
 #define DSA_KV8_H_

@@ -124,8 +124,8 @@ __device__ __forceinline__ uint32_t pack(float a, float b, int fp16) {
 }
 
 // The power of two 2^-e that brings a row's largest magnitude to [2^7, 2^8), where the
-// row's values are exact in fp16 down to 2^-22 of the largest in bf16's and fp16's
-// significands; `back` is 2^e.  Both stay normal numbers.
+// row's values are exact in fp16 down to 2^-25 of the largest with bf16's significands and
+// 2^-22 with fp16's; `back` is 2^e.  Both stay normal numbers.
 __device__ __forceinline__ float row_scaling(float largest, float& back) {
   const int e = largest > 0.f ? min(max((int)(__float_as_uint(largest) >> 23) - 127 - 7, -100), 120) : 0;
   back = __uint_as_float((uint32_t)(127 + e) << 23);

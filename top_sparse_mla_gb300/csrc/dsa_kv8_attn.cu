@@ -10,15 +10,20 @@
 // (decode, drafted tokens) go to rows_kernel below; the others are cut into tiles.
 //
 // What bounds rows_kernel: memory for 8 rows (64 requests of up to 32k tokens, 64/8 heads of
-// 128: 2.04 GB in 308 us, 6.6 TB/s, 0.98 of a copy's rate); the latency of a step for 16 (48
-// requests of up to 8k, 4 queries, 89 us, 0.69) and 32 rows, whose registers leave 12 and 8
-// warps on an SM; ramp and join, about 9 us, for one request of 32k (19.5 us, floor 10).
+// 128: 2.04 GB in 308 us, 6.6 TB/s, 0.97 of a copy's rate); the latency of a step for 16 (48
+// requests of up to 8k, 4 queries, 90 us, 0.67) and 32 rows, whose registers leave 12 and 8
+// warps on an SM; ramp and join, about 10 us, for one request of 32k (20.1 us, floor 10).
 //
 // Scales.  With S = q . code_k summed in fp32 and x = S * k_scale * softmax_scale * log2 e,
 // the kernels take t = x + log2(v_scale) and w = 2^(t - m), m a running maximum of t.  Then
 // O = sum w * code_v is the weighted sum with every page's value scale in it, and
 // l = sum w / v_scale is the softmax's sum (see SMALL_SCALE): w is at most 2^8 (the maximum may
 // lag by 8), whatever the scales' magnitudes, so that it fits fp16.
+//
+// That w is rounded to fp16 for its product (2^-11, and 2^-25 of a row's largest) is a choice: a
+// second product with what the rounding left would double that contraction, half of the work, and
+// the result's own rounding hides it.  Against 64 bits bf16 outputs are off by 0.0017 of their norm,
+// with w in fp32 by the same; fp16 ones under a window of 640 by 0.00023, in fp32 by 0.00021.
 
 #include <float.h>
 
@@ -858,7 +863,9 @@ static bool has_tiles(const dsa_kv8_params* p) {
   return (long long)p->max_q_len * (p->h_q / p->h_kv) > 8 * row_tiles(p);
 }
 
-// Whether a CTA of rows_kernel has all the warps that an SM holds, or four of them.  With
+// Whether a CTA of rows_kernel has all the warps that an SM holds, or four of them.  The lengths are
+// on the GPU, so the rule goes by the most that a request may have, the table's columns; the figures
+// are for tables as wide as the longest request, and a wider one takes the wide CTAs' figure.  With
 // few units, which many CTAs share, wider CTAs leave fewer pieces to join; with short ones
 // their warps have nothing to do.  Heads of 128, 64/8 heads, us, wide and not: 4 requests of
 // up to 2500 tokens 14.6 and 13.2, 4000 15.2 and 17.3, 12000 17.9 and 21.9; 8 of 2500 15.1

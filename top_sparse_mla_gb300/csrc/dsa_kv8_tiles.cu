@@ -17,9 +17,9 @@
 //     under the other half's products.
 // What bounds it: a half's chain of scores, softmax (about 2100 cycles a block), weights and
 // products (1024) and their handoffs (500), while the two halves' products are 2048.  6
-// chunks of up to 2048 queries on up to 8k tokens, 32/4 heads of 128: 687 us, 1199 TFLOP/s, 0.61
+// chunks of up to 2048 queries on up to 8k tokens, 32/4 heads of 128: 691 us, 1192 TFLOP/s, 0.61
 // of a large bf16 product's rate; a 2123-token prefill, 64/8 heads, whose units have 1 to 17
-// blocks: 95 us, 0.40.
+// blocks: 98 us, 0.39.
 //
 // Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
 // and the CTA's roles stop, drain the tensor core and free its memory.  The CTAs of a
@@ -212,7 +212,10 @@ DSA_DEV bool unit(const Params& P, uint32_t round, int n_tiles, Unit& x) {
 //
 // The scales of block g (counted over all units) are in slot g % 4.  They are written when
 // the codes of block g - 1 have left their buffer, so the V tile of block g - 2 was written,
-// so the products of block g - 4 are done: the softmax has left the slot.
+// so the products of block g - 4 are done: the softmax has left the slot.  The softmax reads them
+// behind its wait for the scores, which come after them by way of the keys' signals; its wait for
+// B_SCALES holds by itself only for a half that has had every block, since one that skipped units
+// meets an older phase's parity.
 template <int D, bool SPLIT>
 DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   using SM = TileSmem<D>;

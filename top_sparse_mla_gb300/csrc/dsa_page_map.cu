@@ -9,9 +9,11 @@
 // table only where the request had it before the call and from the free list otherwise,
 // so no thread reads an entry that another one writes.
 //
-// Bound by latency: two dependent loads and four barriers.  4.9 us for 16 requests of a
-// token each and 7.0 for 1021 in a graph, 5.6 for 71 k tokens of 33 requests, whose 1.2 MB
-// are 0.2 us of memory.
+// Bound by latency: three barriers, three dependent loads for a token that continues a page
+// (the lengths, the lengths of its own request, the table) and some 64-bit divisions by the
+// page size; one CTA has two barriers more for the status.  5.0 us for 16 requests of a token
+// each and 7.0 for 1021 in a graph, 6.0 for 71 k tokens of 33 requests, whose 1.2 MB are 0.2 us
+// of memory.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
