@@ -216,3 +216,11 @@ def test_queries_that_are_not_finite_leave_other_rows_alone(lens):
     assert out[a:b, 2::3].isnan().all() and lse[a:b, 2::3].isnan().all()
     out[a:b, 2::3], lse[a:b, 2::3] = want[a:b, 2::3], want_lse[a:b, 2::3]
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("lens,h", [([(1, 300), (1, 2000)], 2), ([(1, 20 + i) for i in range(9)], 8), ([(2, 700), (1, 5)], 1), ([(40, 90)], 2),
+                                    ([(9, 200)] * 8, 2), ([(40, 90)] * 80, 1)])
+@pytest.mark.parametrize("d,window", [(128, 0), (128, 100), (64, 0)])
+def test_tables_far_wider_than_their_contexts(lens, h, d, window):
+    """Room for 64k tokens a request, as an engine's tables have it: what the launches go by is the room."""
+    _check(Case(98, lens, h=h, g=8, d=d, page=16, window=window, cols_more=4096))
