@@ -161,8 +161,9 @@ def test_scores_far_below_zero(lens):
 
 
 @pytest.mark.parametrize("lens", [ROWS, ONE_CTA, CLUSTER, [(1, 9000)]], ids=["rows", "one CTA", "cluster", "many CTAs"])
-@pytest.mark.parametrize("scales", [[2.0 ** -64, 2.0 ** 64], [2.0 ** -63, 2.0 ** 40, 1.0, 2.0 ** 64], [2.0 ** -33, 2.0 ** -32, 2.0 ** 64]],
-                         ids=["ends", "spread", "border"])
+@pytest.mark.parametrize("scales", [[2.0 ** -64, 2.0 ** 64], [2.0 ** -63, 2.0 ** 40, 1.0, 2.0 ** 64], [2.0 ** -33, 2.0 ** -32, 2.0 ** 64],
+                                    [2.0 ** -31, 2.0 ** 59], [2.0 ** -31, 2.0 ** 60]],
+                         ids=["ends", "spread", "border", "below 2^90", "above 2^90"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_value_scales_far_apart(lens, scales, d):
     """A token's share of the softmax's sum does not depend on its page's value scale."""

@@ -21,7 +21,7 @@ constexpr int MAX_CLUSTER = 16;
 // and without: 1024 windowed requests 44.4 and 43.9, 48 verified 89.5 and 88.9, one of 32k 20.1 and
 // 19.8; a 2123-token prefill 96.0 and 95.1, 6 chunks 690 and 686.
 constexpr float SMALL_SCALE = 2.3283064365386963e-10f;   // 2^-32
-constexpr float FAR_APART = 1.8446744073709552e19f;      // 2^64
+constexpr float FAR_APART = 1.2379400392853803e27f;      // 2^90: w stays a normal number for every p above 2^-36
 constexpr float LAG = 8.0f;       // how far, in powers of two, a running maximum may lag
 
 struct Share {   // where a CTA's share of the steps begins
