@@ -225,3 +225,26 @@ def test_queries_that_are_not_finite_leave_other_rows_alone(lens):
 def test_tables_far_wider_than_their_contexts(lens, h, d, window):
     """Room for 64k tokens a request, as an engine's tables have it: what the launches go by is the room."""
     _check(Case(98, lens, h=h, g=8, d=d, page=16, window=window, cols_more=4096))
+
+
+@pytest.mark.parametrize("lens", [[(1, 300), (2, 0), (4, 90), (1, 17)], [(40, 300), (33, 0), (9, 128), (60, 90)], [(40, 1280), (1, 0)]],
+                         ids=["rows", "tiles", "cluster"])
+@pytest.mark.parametrize("window", [0, 50])
+def test_lengths_outside_their_range_are_taken_as_the_nearest_bound(lens, window):
+    c = Case(99, lens, h=1, g=8, d=64, page=16, window=window, poison=False, pad=0)
+    room = c.table.shape[1] * c.page
+    c.kv[0], c.kv[1] = room, 0
+    D = c.device()
+    want = c.run(dev=D)
+    assert want[2] == 0
+    far = dict(D, kv=D["kv"].clone(), cu=D["cu"].clone())
+    far["kv"][0], far["kv"][1] = 2 ** 31 - 1, -2 ** 31
+    far["cu"][-1] = 2 ** 31 - 1
+    got = c.run(dev=far)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.check(*want[:2])
+    # the first request's rows begin in front of the batch: they are those from row 0 on
+    far["cu"][0], D["cu"][0] = -2 ** 31, 0
+    most = max(q for q, _ in lens) + 1
+    a, b = c.run(dev=far, max_q_len=most), c.run(dev=D, max_q_len=most)
+    assert torch.equal(a[0][1:], b[0][1:]) and torch.equal(a[1][1:], b[1][1:])
