@@ -65,8 +65,8 @@
  * The workspace needs no initialisation and holds the status word of the last call
  * (dsa_sparse_attn_read_status reads it).  Calls that share a workspace must not overlap
  * on the GPU.  Results do not depend on the other requests' order of completion: the same
- * inputs give the same bits.  On-chip waits are bounded: where one runs out (10 s without an
- * end), the status gets DSA_STATUS_WAIT_TIMEOUT and rows are missing or wrong.
+ * inputs give the same bits.  On-chip waits are bounded: where one runs out (after about 10 s),
+ * the status gets DSA_STATUS_WAIT_TIMEOUT, and rows may be missing or wrong.
  *
  * Numerics: E4M3 codes are exact in fp16, and so are the queries after each row's scaling
  * by a power of two, down to 2^-22 (fp16) or 2^-25 (bf16) of the row's largest magnitude;

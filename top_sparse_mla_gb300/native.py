@@ -406,7 +406,7 @@ def dsa_kv8_params_init(q, k_pool, block_table, max_q_len=None, **overrides) -> 
     """Parameters of dsa_kv8_attn_fwd for these tensors' shapes and type: q bf16 or fp16
     [n_tokens, h_q, d], k_pool uint8 [n_pages, h_kv, page_size, d], block_table
     [n_req, cols]. max_q_len: most query rows of a request (default: n_tokens);
-    overrides: window, softmax_scale."""
+    overrides: window, softmax_scale, flags."""
     where = "dsa_kv8_params_init"
     if torch is None:
         _bind_torch()
