@@ -68,9 +68,9 @@ def _batch(n):
     return Case(n, [(int(a), int(b)) for a, b in zip(rng.integers(0, 3, n), rng.integers(0, 40, n))], h=1, g=2, d=64, page=16)
 
 
-# 2783 requests are the first whose prefix sums and the plan's other shared memory pass 48 KB together, 3072 the first
-# whose prefix sums do so alone.  A kernel keeps a limit that was raised: each size in a process of its own.
-@pytest.mark.parametrize("n", [2782, 2783, 3071, 3072, native.DSA_KV8_MAX_REQ])
+# 2783 requests are the first whose prefix sums and the plan's other shared memory pass 48 KB together; those of 4000 do so
+# alone.  A kernel keeps a limit that was raised: each size in a process of its own.
+@pytest.mark.parametrize("n", [2782, 2783, 3000, 4000, native.DSA_KV8_MAX_REQ])
 def test_large_batches_as_a_process_first_call(n):
     code = f"import test_kv8_attn_edges_gpu as t; t._check(t._batch({n}))"
     here = os.path.dirname(os.path.abspath(__file__))
@@ -83,7 +83,7 @@ def test_large_batches_from_several_host_threads():
     """The C calls of two batch sizes, each from two threads on streams of their own: a smaller batch's call lowered the limit of
     shared memory between a larger one's setting it and its launch, which refused one in a hundred of the larger ones."""
     lib = native.library()
-    cases = [_batch(n) for n in (3072, native.DSA_KV8_MAX_REQ)]
+    cases = [_batch(n) for n in (4000, native.DSA_KV8_MAX_REQ)]
     calls = []
     for c in cases + cases:
         D = c.device()
