@@ -53,6 +53,10 @@ DSA_KV8_MAX_GROUP = 128
 DSA_KV8_MAX_REQ = 8192
 DSA_KV8_FLAG_TEST_WAIT_TIMEOUT = 2
 DSA_STATUS_QUERY_TOO_LONG = 64
+DSA_QK_BF16 = 0
+DSA_QK_FP16 = 1
+DSA_QK_FLAG_INTERLEAVED = 1
+DSA_QK_MAX_HEADS = 4096
 
 EXPORTED = (
     "dsa_params_init",
@@ -70,6 +74,9 @@ EXPORTED = (
     "dsa_kv8_params_init",
     "dsa_kv8_attn_workspace_size",
     "dsa_kv8_attn_fwd",
+    "dsa_qk_params_init",
+    "dsa_qk_norm_rope",
+    "dsa_kv_gather",
 )
 
 
@@ -105,6 +112,21 @@ class DsaKv8Params(ctypes.Structure):
         ("type", ctypes.c_int32),
         ("softmax_scale", ctypes.c_float),
         ("flags", ctypes.c_uint32),
+    ]
+
+
+class DsaQkParams(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32),
+        ("h_q", ctypes.c_int32),
+        ("h_k", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("rotary_start", ctypes.c_int32),
+        ("type", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("rms_eps", ctypes.c_float),
+        ("rope_base", ctypes.c_float),
     ]
 
 
@@ -161,6 +183,13 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_kv8_attn_workspace_size.restype = sz
     lib.dsa_kv8_attn_fwd.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp, i64, i64, vp, p8, vp, sz, vp]
     lib.dsa_kv8_attn_fwd.restype = ctypes.c_int
+    pq = ctypes.POINTER(DsaQkParams)
+    lib.dsa_qk_params_init.argtypes = [pq, i32, i32, i32, i32]
+    lib.dsa_qk_params_init.restype = ctypes.c_int
+    lib.dsa_qk_norm_rope.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, i64, vp, i64, i64, pq, vp]
+    lib.dsa_qk_norm_rope.restype = ctypes.c_int
+    lib.dsa_kv_gather.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i64, i32, vp, vp]
+    lib.dsa_kv_gather.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -464,6 +493,90 @@ def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_
                                     v_scale.data_ptr(), block_table.data_ptr(), table_ld, cu_q.data_ptr(),
                                     kv_lens.data_ptr(), out.data_ptr(), out_ld, out_hd, _ptr(lse), ctypes.byref(p),
                                     workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+
+
+def dsa_qk_params_init(q, k=None, rotary_dim=None, rotary_start: int = 0, interleaved: bool = False,
+                       rms_eps: float = 1e-6, rope_base: float = 10000.0) -> DsaQkParams:
+    """Parameters of dsa_qk_norm_rope for these tensors' shapes and type: q bf16 or fp16 [n_tokens, h_q, d], k
+    [n_tokens, h_k, d] or None. rotary_dim: how many of a head's values turn (default: d), from rotary_start on, in
+    pairs of neighbours if `interleaved`, else with the value half of them further on."""
+    where = "dsa_qk_params_init"
+    if torch is None:
+        _bind_torch()
+    if q.dim() != 3 or q.dtype not in _KV8_TYPES:
+        _refuse(where, "q must be a bfloat16 or float16 tensor [n_tokens, h_q, d]")
+    n, h_q, d = (int(x) for x in q.shape)
+    if k is not None and (k.dim() != 3 or k.dtype is not q.dtype or k.shape[0] != n or k.shape[2] != d):
+        _refuse(where, f"k must be a {q.dtype} tensor [{n}, h_k, {d}]")
+    p = DsaQkParams()
+    rc = library().dsa_qk_params_init(ctypes.byref(p), n, h_q, 0 if k is None else int(k.shape[1]), d)
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+    p.type = _KV8_TYPES[q.dtype]
+    p.rotary_dim = d if rotary_dim is None else int(rotary_dim)
+    p.rotary_start, p.flags = int(rotary_start), DSA_QK_FLAG_INTERLEAVED if interleaved else 0
+    p.rms_eps, p.rope_base = float(rms_eps), float(rope_base)
+    return p
+
+
+def _weights(where: str, dev: int, w, name: str, dtype, d: int) -> None:
+    if w is not None and (w.dtype is not dtype or w.shape != (d,) or not w.is_contiguous() or w.get_device() != dev):
+        _dense(where, dev, (w, name, dtype, (d,)))
+
+
+def dsa_qk_norm_rope(q, k, positions, q_weight, k_weight, q_out, k_out, p: DsaQkParams, stream=None) -> None:
+    """RMS norm and rotation of the heads of queries and keys (include/dsa_qk_norm_rope.h). q, q_out: bf16 or fp16
+    [n_tokens, h_q, d]; k, k_out: [n_tokens, h_k, d], or None where p has no keys (token and head pitches allowed;
+    an output may be its input itself); positions: int32 [n_tokens]; q_weight, k_weight: [d], or None for no norm."""
+    where = "dsa_qk_norm_rope"
+    dev = _device(where, q)
+    n, h_q, h_k, d, dtype = p.n_tokens, p.h_q, p.h_k, p.d, q.dtype
+    if _KV8_TYPES.get(dtype) != p.type:
+        _refuse(where, "q's type is not that of p")
+    q_ld, q_hd = _heads(where, dev, q, "q", dtype, n, h_q, d)
+    qo_ld, qo_hd = _heads(where, dev, q_out, "q_out", dtype, n, h_q, d)
+    if (k is None) != (h_k == 0) or (k_out is None) != (h_k == 0):
+        _refuse(where, "k and k_out must be given where p has keys, and only there")
+    k_ld = k_hd = ko_ld = ko_hd = 0
+    if h_k:
+        k_ld, k_hd = _heads(where, dev, k, "k", dtype, n, h_k, d)
+        ko_ld, ko_hd = _heads(where, dev, k_out, "k_out", dtype, n, h_k, d)
+    if not (positions.dtype is _I32 and positions.shape == (n,) and positions.is_contiguous() and positions.get_device() == dev):
+        _dense(where, dev, (positions, "positions", _I32, (n,)))
+    _weights(where, dev, q_weight, "q_weight", dtype, d)
+    _weights(where, dev, k_weight, "k_weight", dtype, d)
+    rc = library().dsa_qk_norm_rope(q.data_ptr(), q_ld, q_hd, _ptr(k), k_ld, k_hd, positions.data_ptr(), _ptr(q_weight),
+                                    _ptr(k_weight), q_out.data_ptr(), qo_ld, qo_hd, _ptr(k_out), ko_ld, ko_hd,
+                                    ctypes.byref(p), _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+
+
+def dsa_kv_gather(pool, block_table, cu_rows, out, page_size: int, lens=None, status=None, stream=None) -> None:
+    """Latent rows read back from the cache (include/dsa_kv_gather.h). pool: uint8 [n_rows, 656]; block_table: int32
+    [n_req, cols] (a row pitch is allowed); cu_rows: int32 [n_req + 1]; out: bf16 [n_out, ld >= 576]; lens: int32
+    [n_req] or None; status: uint32 or int32 [1] device tensor or None."""
+    where = "dsa_kv_gather"
+    dev = _device(where, pool)
+    if pool.dtype is not _U8 or pool.dim() != 2 or pool.shape[1] != DSA_ROW_BYTES or not pool.is_contiguous():
+        _dense(where, dev, (pool, "pool", _U8, (pool.shape[0], DSA_ROW_BYTES)))
+    n_req, cols = block_table.shape[0], block_table.shape[-1]
+    table_ld = _table_pitch(where, dev, block_table, n_req, cols)
+    _dense(where, dev, (cu_rows, "cu_rows", _I32, (n_req + 1,)))
+    if lens is not None:
+        _dense(where, dev, (lens, "lens", _I32, (n_req,)))
+    n_out, (ld, one) = out.shape[0], out.stride() if out.dim() == 2 else (0, 0)
+    if out.dtype is not torch.bfloat16 or out.dim() != 2 or out.shape[1] < 576 or (n_out > 0 and one != 1) or out.get_device() != dev:
+        _refuse(where, "out must be a bfloat16 tensor [n_out, >= 576] of dense rows on the current CUDA device")
+    if n_out > 1 and ld < 576:
+        _refuse(where, "the rows of out overlap")
+    if status is not None and (status.element_size() != 4 or status.get_device() != dev):
+        _refuse(where, "status must be a 32-bit word on the current CUDA device")
+    rc = library().dsa_kv_gather(pool.data_ptr(), pool.shape[0], block_table.data_ptr(), table_ld, cols, int(page_size),
+                                 cu_rows.data_ptr(), _ptr(lens), n_req, out.data_ptr(), ld if n_out > 1 else 576, n_out,
+                                 _ptr(status), _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
