@@ -57,6 +57,11 @@ DSA_QK_BF16 = 0
 DSA_QK_FP16 = 1
 DSA_QK_FLAG_INTERLEAVED = 1
 DSA_QK_MAX_HEADS = 4096
+DSA_MLA_BF16 = 0
+DSA_MLA_FP16 = 1
+DSA_MLA_MAX_HEADS = 1024
+DSA_MLA_MAX_REQ = 8192
+DSA_MLA_FLAG_TEST_WAIT_TIMEOUT = 2
 
 EXPORTED = (
     "dsa_params_init",
@@ -77,6 +82,9 @@ EXPORTED = (
     "dsa_qk_params_init",
     "dsa_qk_norm_rope",
     "dsa_kv_gather",
+    "dsa_mla_params_init",
+    "dsa_mla_prefill_workspace_size",
+    "dsa_mla_prefill_fwd",
 )
 
 
@@ -127,6 +135,20 @@ class DsaQkParams(ctypes.Structure):
         ("flags", ctypes.c_uint32),
         ("rms_eps", ctypes.c_float),
         ("rope_base", ctypes.c_float),
+    ]
+
+
+class DsaMlaParams(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32),
+        ("n_keys", ctypes.c_int32),
+        ("n_req", ctypes.c_int32),
+        ("h", ctypes.c_int32),
+        ("max_q_len", ctypes.c_int32),
+        ("max_kv_len", ctypes.c_int32),
+        ("type", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
     ]
 
 
@@ -190,6 +212,13 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_qk_norm_rope.restype = ctypes.c_int
     lib.dsa_kv_gather.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i64, i32, vp, vp]
     lib.dsa_kv_gather.restype = ctypes.c_int
+    pm = ctypes.POINTER(DsaMlaParams)
+    lib.dsa_mla_params_init.argtypes = [pm, i32, i32, i32, i32]
+    lib.dsa_mla_params_init.restype = ctypes.c_int
+    lib.dsa_mla_prefill_workspace_size.argtypes = [pm, ctypes.c_int]
+    lib.dsa_mla_prefill_workspace_size.restype = sz
+    lib.dsa_mla_prefill_fwd.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, vp, pm, vp, sz, vp]
+    lib.dsa_mla_prefill_fwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -577,6 +606,73 @@ def dsa_kv_gather(pool, block_table, cu_rows, out, page_size: int, lens=None, st
     rc = library().dsa_kv_gather(pool.data_ptr(), pool.shape[0], block_table.data_ptr(), table_ld, cols, int(page_size),
                                  cu_rows.data_ptr(), _ptr(lens), n_req, out.data_ptr(), ld if n_out > 1 else 576, n_out,
                                  _ptr(status), _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+
+
+def dsa_mla_params_init(q, k_nope, cu_q, max_q_len=None, max_kv_len=None, **overrides) -> DsaMlaParams:
+    """Parameters of dsa_mla_prefill_fwd for these tensors' shapes and type: q bf16 or fp16 [n_tokens, h, 192], k_nope
+    [n_keys, h, 128], cu_q int32 [n_req + 1]. Other fields (softmax_scale, flags) by keyword."""
+    where = "dsa_mla_params_init"
+    if torch is None:
+        _bind_torch()
+    if q.dim() != 3 or q.shape[2] != 192 or q.dtype not in _KV8_TYPES:
+        _refuse(where, "q must be a bfloat16 or float16 tensor [n_tokens, h, 192]")
+    if k_nope.dim() != 3 or k_nope.shape[1:] != (q.shape[1], 128) or k_nope.dtype is not q.dtype:
+        _refuse(where, f"k_nope must be a {q.dtype} tensor [n_keys, {q.shape[1]}, 128]")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        _refuse(where, "cu_q must be [n_req + 1]")
+    p = DsaMlaParams()
+    rc = library().dsa_mla_params_init(ctypes.byref(p), q.shape[0], k_nope.shape[0], cu_q.shape[0] - 1, q.shape[1])
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+    p.type = _KV8_TYPES[q.dtype]
+    if max_q_len is not None:
+        p.max_q_len = int(max_q_len)
+    if max_kv_len is not None:
+        p.max_kv_len = int(max_kv_len)
+    for name, value in overrides.items():
+        if name not in ("softmax_scale", "flags"):
+            _refuse(where, f"unknown parameter {name}")
+        setattr(p, name, value)
+    return p
+
+
+def dsa_mla_prefill_workspace_size(p: DsaMlaParams, num_sms: int = 0) -> int:
+    n = int(library().dsa_mla_prefill_workspace_size(ctypes.byref(p), int(num_sms)))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, "dsa_mla_prefill_workspace_size")
+    return n
+
+
+def dsa_mla_prefill_fwd(q, k_nope, k_rope, v, cu_q, cu_kv, out, p: DsaMlaParams, workspace, lse=None, stream=None) -> None:
+    """Latent attention with expanded keys and values (include/dsa_mla_prefill.h). q: bf16 or fp16 [n_tokens, h, 192];
+    k_nope, v: [n_keys, h, 128]; k_rope: [n_keys, 64] (a row pitch is allowed); out: [n_tokens, h, 128] (token and head
+    pitches allowed); cu_q, cu_kv: int32 [n_req + 1]; lse: fp32 [n_tokens, h] or None; workspace:
+    dsa_mla_prefill_workspace_size(p) bytes on the device."""
+    where = "dsa_mla_prefill_fwd"
+    dev = _device(where, q)
+    n, m, h, n_req, dtype = p.n_tokens, p.n_keys, p.h, p.n_req, q.dtype
+    if _KV8_TYPES.get(dtype) != p.type:
+        _refuse(where, "q's type is not that of p")
+    q_ld, q_hd = _heads(where, dev, q, "q", dtype, n, h, 192)
+    k_ld, k_hd = _heads(where, dev, k_nope, "k_nope", dtype, m, h, 128)
+    v_ld, v_hd = _heads(where, dev, v, "v", dtype, m, h, 128)
+    out_ld, out_hd = _heads(where, dev, out, "out", dtype, n, h, 128)
+    r_ld, one = k_rope.stride() if k_rope.dim() == 2 else (0, 0)
+    if k_rope.dtype is not dtype or k_rope.shape != (m, 64) or (m > 0 and one != 1) or k_rope.get_device() != dev:
+        _refuse(where, f"k_rope must be a {dtype} tensor of shape {(m, 64)} of dense rows on the current CUDA device")
+    if not (cu_q.dtype is cu_kv.dtype is _I32 and cu_q.shape == cu_kv.shape == (n_req + 1,) and cu_q.is_contiguous()
+            and cu_kv.is_contiguous() and cu_q.get_device() == cu_kv.get_device() == dev):
+        _dense(where, dev, (cu_q, "cu_q", _I32, (n_req + 1,)), (cu_kv, "cu_kv", _I32, (n_req + 1,)))
+    if lse is not None:
+        _dense(where, dev, (lse, "lse", _F32, (n, h)))
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(where, "the workspace must be contiguous and on the current CUDA device")
+    rc = library().dsa_mla_prefill_fwd(q.data_ptr(), q_ld, q_hd, k_nope.data_ptr(), k_ld, k_hd, k_rope.data_ptr(), r_ld if m > 1 else 64,
+                                       v.data_ptr(), v_ld, v_hd, cu_q.data_ptr(), cu_kv.data_ptr(), out.data_ptr(), out_ld,
+                                       out_hd, _ptr(lse), ctypes.byref(p), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
