@@ -13,7 +13,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("dsa_sparse_attn.cu", "dsa_kv8_attn.cu", "dsa_kv8_tiles.cu",
                                                       "dsa_kv8_insert.cu", "dsa_topk.cu", "dsa_kv_insert.cu", "dsa_page_map.cu",
-                                                      "dsa_qk_norm_rope.cu", "dsa_kv_gather.cu", "dsa_mla_prefill.cu")]
+                                                      "dsa_qk_norm_rope.cu", "dsa_kv_gather.cu", "dsa_mla_prefill.cu", "dsa_kv8_prefix.cu")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libdsa_sparse_attn.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)

@@ -30,17 +30,25 @@ struct Share {   // where a CTA's share of the steps begins
 };
 
 struct Tile {   // rows [row0, row0 + TILE_ROWS) of a request (query * group + head of the group)
-  int req, row0;
+  int req, row0;     // req: row of the block table
   int q0, rows;      // the request's first query token and its rows
   int pos0;          // position of its first query
   int lo, hi;        // cached tokens that the tile's rows see, lo rounded down to a step
-  int pad;
+  int side;          // PREFIX: which part of its rows' tokens these are, SHARED or OWN
 };
 
 struct Header {
   uint32_t status;
   int n_tiles;
   long long share;   // steps of every CTA
+};
+
+enum { SHARED = 0, OWN = 1 };
+// What the rows of a group, or of a request, see of the cache in one part: tokens [lo, hi) by block table row
+// `req`, and of those the ones up to their own positions, pos0 for the first query.
+struct Part {
+  int q0, q_len, pos0, lo;
+  int hi, req, side, pad;
 };
 
 struct Params {
@@ -63,12 +71,20 @@ struct Params {
   int n_shares, max_tiles, n_ctas;   // n_ctas: of the tiles' kernel
   int has_tiles;    // whether requests may have more rows than rows_kernel takes
   int cluster;      // CTAs that share a tile and KV head; 0: a CTA has several of them
+  // Requests that share a prefix (dsa_kv8_prefix.cu): n_req counts the groups and the requests, whose
+  // parts are in `parts`; the queries' O, m and l of either part go to part_o and part_ml
+  Part* parts;
+  const int32_t *cu_groups, *prefix_lens;
+  float* part_o;
+  float2* part_ml;
+  int n_groups;
   uint32_t test_block;   // block of CTA 0 at which the copies stop (DSA_KV8_FLAG_TEST_WAIT_TIMEOUT)
   float scale_log2;   // softmax_scale * log2 e
 };
 
 struct Request {
   int q0, q_len, kv;
+  int lo, hi, req, side;   // PREFIX
   __device__ __forceinline__ int rows(const Params& P) const { return q_len * P.group; }
 };
 
@@ -79,8 +95,20 @@ __device__ __forceinline__ Request request(const Params& P, int from, int to, in
   a.kv = min(max(kv_len, 0), P.cap);
   return a;
 }
+template <bool PREFIX = false>
 __device__ __forceinline__ Request request(const Params& P, int r) {
-  return request(P, P.cu_q[r], P.cu_q[r + 1], P.kv_lens[r]);
+  if (!PREFIX) return request(P, P.cu_q[r], P.cu_q[r + 1], P.kv_lens[r]);
+  // plain loads: the plan writes them while the kernels that read them are there already
+  const int4* at = reinterpret_cast<const int4*>(P.parts + r);
+  const int4 x = at[0], y = at[1];
+  Request a;
+  a.q0 = x.x; a.q_len = x.y; a.kv = x.z + x.y;
+  a.lo = x.w; a.hi = y.x; a.req = y.y; a.side = y.z;
+  return a;
+}
+// a query row's place in part_o and part_ml
+__device__ __forceinline__ long long part_row(const Params& P, int side, int token, int head) {
+  return ((long long)side * P.n_tokens + token) * P.h_q + head;
 }
 
 // The cached tokens [lo, hi) that the query positions [p0, p1] may see, lo rounded down to
@@ -88,7 +116,12 @@ __device__ __forceinline__ Request request(const Params& P, int r) {
 struct Span {
   int lo, steps;
 };
+template <bool PREFIX = false>
 __device__ __forceinline__ Span span(const Params& P, const Request& a, int i0, int i1) {
+  if (PREFIX) {   // no window, and a part begins at a step
+    const int end = min(a.kv - a.q_len + i1 + 1, a.hi);
+    return Span{a.lo, max((end - a.lo + STEP - 1) / STEP, 1)};
+  }
   const int p0 = a.kv - a.q_len + i0, p1 = a.kv - a.q_len + i1;
   Span s;
   s.lo = P.window > 0 ? max(p0 - P.window + 1, 0) & ~(STEP - 1) : 0;

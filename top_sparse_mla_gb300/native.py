@@ -85,6 +85,8 @@ EXPORTED = (
     "dsa_mla_params_init",
     "dsa_mla_prefill_workspace_size",
     "dsa_mla_prefill_fwd",
+    "dsa_kv8_prefix_workspace_size",
+    "dsa_kv8_prefix_attn_fwd",
 )
 
 
@@ -212,6 +214,10 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_qk_norm_rope.restype = ctypes.c_int
     lib.dsa_kv_gather.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i64, i32, vp, vp]
     lib.dsa_kv_gather.restype = ctypes.c_int
+    lib.dsa_kv8_prefix_workspace_size.argtypes = [p8, i32, ctypes.c_int]
+    lib.dsa_kv8_prefix_workspace_size.restype = sz
+    lib.dsa_kv8_prefix_attn_fwd.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, i32, vp, i64, i64, vp, p8, vp, sz, vp]
+    lib.dsa_kv8_prefix_attn_fwd.restype = ctypes.c_int
     pm = ctypes.POINTER(DsaMlaParams)
     lib.dsa_mla_params_init.argtypes = [pm, i32, i32, i32, i32]
     lib.dsa_mla_params_init.restype = ctypes.c_int
@@ -494,14 +500,8 @@ def dsa_kv8_attn_workspace_size(p: DsaKv8Params, num_sms: int = 0) -> int:
     return n
 
 
-def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, p: DsaKv8Params, workspace,
-                     lse=None, stream=None) -> None:
-    """Attention over the paged 8-bit cache (include/dsa_kv8.h). q, out: bf16 or fp16
-    [n_tokens, h_q, d] (token and head pitches allowed); pools and scales as
-    dsa_kv8_insert; block_table: int32 [n_req, cols]; cu_q: int32 [n_req + 1]; kv_lens:
-    int32 [n_req]; lse: fp32 [n_tokens, h_q] or None; workspace: uint8, 256-byte aligned
-    (dsa_kv8_attn_workspace_size(p) bytes)."""
-    where = "dsa_kv8_attn_fwd"
+def _kv8_attn_args(where, q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, p, workspace, lse):
+    """(device, arguments up to kv_lens, arguments from out to lse) of a call of the attention, checked."""
     dev = _device(where, q)
     if _kv8_pools(where, dev, k_pool, v_pool, k_scale, v_scale) != (p.n_pages, p.h_kv, p.page_size, p.d):
         _refuse(where, "the pools are not those of p")
@@ -518,10 +518,45 @@ def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_
     table_ld = _table_pitch(where, dev, block_table, n_req, p.table_cols)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(where, "the workspace must be contiguous and on the current CUDA device")
-    rc = library().dsa_kv8_attn_fwd(q.data_ptr(), q_ld, q_hd, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
-                                    v_scale.data_ptr(), block_table.data_ptr(), table_ld, cu_q.data_ptr(),
-                                    kv_lens.data_ptr(), out.data_ptr(), out_ld, out_hd, _ptr(lse), ctypes.byref(p),
-                                    workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    return (dev, (q.data_ptr(), q_ld, q_hd, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                  block_table.data_ptr(), table_ld, cu_q.data_ptr(), kv_lens.data_ptr()),
+            (out.data_ptr(), out_ld, out_hd, _ptr(lse)))
+
+
+def dsa_kv8_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, p: DsaKv8Params, workspace,
+                     lse=None, stream=None) -> None:
+    """Attention over the paged 8-bit cache (include/dsa_kv8.h). q, out: bf16 or fp16
+    [n_tokens, h_q, d] (token and head pitches allowed); pools and scales as
+    dsa_kv8_insert; block_table: int32 [n_req, cols]; cu_q: int32 [n_req + 1]; kv_lens:
+    int32 [n_req]; lse: fp32 [n_tokens, h_q] or None; workspace: uint8, 256-byte aligned
+    (dsa_kv8_attn_workspace_size(p) bytes)."""
+    where = "dsa_kv8_attn_fwd"
+    _, front, back = _kv8_attn_args(where, q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, p, workspace, lse)
+    rc = library().dsa_kv8_attn_fwd(*front, *back, ctypes.byref(p), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc != DSA_OK:
+        raise DsaError(rc, where)
+
+
+def dsa_kv8_prefix_workspace_size(p: DsaKv8Params, n_groups: int, num_sms: int = 0) -> int:
+    n = int(library().dsa_kv8_prefix_workspace_size(ctypes.byref(p), int(n_groups), int(num_sms)))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, "dsa_kv8_prefix_workspace_size")
+    return n
+
+
+def dsa_kv8_prefix_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, cu_groups, prefix_lens, out,
+                            p: DsaKv8Params, workspace, lse=None, stream=None) -> None:
+    """dsa_kv8_attn_fwd for a batch whose requests share prefixes, whose pages are read once for all
+    (include/dsa_kv8_prefix.h). cu_groups: int32 [n_groups + 1], the requests of each group; prefix_lens: int32
+    [n_groups]; workspace: dsa_kv8_prefix_workspace_size(p, n_groups) bytes; the others as in dsa_kv8_attn_fwd."""
+    where = "dsa_kv8_prefix_attn_fwd"
+    dev, front, back = _kv8_attn_args(where, q, k_pool, v_pool, k_scale, v_scale, block_table, cu_q, kv_lens, out, p, workspace, lse)
+    n = prefix_lens.shape[0] if prefix_lens.dim() == 1 else -1
+    if not (cu_groups.dtype is prefix_lens.dtype is _I32 and n >= 0 and cu_groups.shape == (n + 1,) and cu_groups.is_contiguous()
+            and prefix_lens.is_contiguous() and cu_groups.get_device() == prefix_lens.get_device() == dev):
+        _dense(where, dev, (prefix_lens, "prefix_lens", _I32, (max(n, 0),)), (cu_groups, "cu_groups", _I32, (n + 1,)))
+    rc = library().dsa_kv8_prefix_attn_fwd(*front, cu_groups.data_ptr(), prefix_lens.data_ptr(), n, *back, ctypes.byref(p),
+                                           workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
@@ -672,7 +707,7 @@ def dsa_mla_prefill_fwd(q, k_nope, k_rope, v, cu_q, cu_kv, out, p: DsaMlaParams,
     rc = library().dsa_mla_prefill_fwd(q.data_ptr(), q_ld, q_hd, k_nope.data_ptr(), k_ld, k_hd, k_rope.data_ptr(), r_ld if m > 1 else 64,
                                        v.data_ptr(), v_ld, v_hd, cu_q.data_ptr(), cu_kv.data_ptr(), out.data_ptr(), out_ld,
                                        out_hd, _ptr(lse), ctypes.byref(p), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), _stream(stream))
+                                       workspace.nbytes, _stream(stream))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
