@@ -9,9 +9,10 @@
 //   - warp 8 copies queries, keys and values into shared memory (TMA, panels of 64 dims x 128
 //     rows in the 128-byte swizzle): four panels for keys, which pass through three at a time
 //     (128 dims of the head, 64 rotary ones), and two blocks of values;
-//   - warp 9 issues the products: S = Q K^T (128 x 128 x 192) and O += P V (128 x 128 x 128, P
-//     in tensor memory).  The two halves alternate, so that one half's softmax runs under the
-//     other half's products.
+//   - a thread of warp 9 issues the products: S = Q K^T (128 x 128 x 192) and O += P V (128 x 128 x
+//     128, P in tensor memory).  The two halves alternate, so that one half's softmax runs under
+//     the other half's products;
+//   - warp 10 clears what a request's last block of values has behind the request's end.
 // A tile with at most 128 rows is a unit of one half, and the halves take such units in turn:
 // one's scores are formed while the other's values are.
 //
@@ -51,20 +52,21 @@ constexpr int K_PANELS = 4, V_BUFS = 2;
 constexpr float MOST = 15.0f;      // largest exponent of a weight by an m that is kept
 constexpr float LAG = 8.0f;        // how far, in powers of two, a running maximum may lag
 constexpr float NOTHING = -FLT_MAX;   // m of a piece in which a row saw nothing
-constexpr int W_COPY = 8, W_MMA = 9, THREADS = 12 * 32;   // warps 10 and 11 only give registers
+constexpr int W_COPY = 8, W_MMA = 9, W_FIX = 10, THREADS = 12 * 32;   // warp 11 only gives registers
 // Registers of a thread of the softmax groups (eight warps) and of the others (four), out of
 // what 12 warps of 168 were launched with.
-constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 208, OTHER_REGS = 88;
+constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 200, OTHER_REGS = 104;
 static_assert(8 * SOFTMAX_REGS + 4 * OTHER_REGS <= 12 * LAUNCH_REGS, "more registers than the CTA has would be waited for");
 constexpr unsigned long long WAIT_LIMIT_CYCLES = 20000000000ull;   // ~10 s at 2 GHz
 constexpr int PLAN_THREADS = 1024;
-constexpr int SPLIT_UNITS = 4;     // units per SM below which they may be split
+constexpr int SPLIT_UNITS = 2;     // units per SM below which they may be split
 
 // barriers
 enum {
   B_KFULL = 0, B_KFREE = 4, B_VFULL = 8, B_VFREE = 10,   // by panel, by buffer
-  B_QFULL = 12, B_QFREE = 14, B_SFULL = 16, B_PFULL = 18, B_OFULL = 20,   // by half
-  B_DRAIN = 22, N_BAR = 23
+  B_QFULL = 12, B_QFREE = 14, B_SFULL = 16, B_OFULL = 18,   // by half
+  B_PFULL = 20,   // by half, and by half of the block
+  B_FIX = 24, B_FIXED = 25, B_DRAIN = 26, N_BAR = 27
 };
 
 struct Smem {
@@ -160,7 +162,7 @@ DSA_DEV T scan(T v, T* s_warp, T& all) {
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params P) {
   extern __shared__ int s_tile[];   // [n_req + 1] exclusive prefix of the requests' tiles
   __shared__ int s_warp[PLAN_THREADS / 32], s_place[PLAN_THREADS];
-  __shared__ long long s_long[PLAN_THREADS / 32];
+  __shared__ long long s_long[PLAN_THREADS / 32], s_before[PLAN_THREADS];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, n = P.n_req;
   for (int r = tid; r < n; r += PLAN_THREADS) s_tile[r] = (rows_of(P, r) + TILE_ROWS - 1) / TILE_ROWS;
@@ -196,21 +198,23 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     if (tid < n_tiles) P.tiles[tid] = t;
     total *= P.h;
     share = max((total + P.n_ctas - 1) / P.n_ctas, 2LL);
+    if (tid < n_tiles) s_before[tid] = t.before;
     __syncthreads();
-    // the shares that begin in this thread's tile
-    for (int b = tid; b < P.n_ctas; b += PLAN_THREADS) P.shares[b].tile = -1;
-    __syncthreads();
-    if (tid < n_tiles) {
-      const long long steps = max(t.steps, 1), from = t.before * P.h, to = from + steps * P.h;
-      for (long long b = (from + share - 1) / share; b * share < to; ++b) {
-        const long long rest = b * share - from;
-        Share s;
-        s.tile = tid;
+    for (int b = tid; b < P.n_ctas; b += PLAN_THREADS) {
+      const long long at_step = b * share;
+      Share s = {-1, 0, 0, 0};
+      if (at_step < total) {
+        int lo = 0, hi = n_tiles;   // the tile with before[lo] * h <= at_step < before[lo + 1] * h
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_before[mid] * P.h <= at_step) lo = mid; else hi = mid;
+        }
+        const long long steps = ((lo + 1 < n_tiles ? s_before[lo + 1] : total / P.h) - s_before[lo]), rest = at_step - s_before[lo] * P.h;
+        s.tile = lo;
         s.head = (int)(rest / steps);
         s.step = (int)(rest - s.head * steps);
-        s.pad = 0;
-        P.shares[b] = s;
       }
+      P.shares[b] = s;
     }
   } else {
     // the longest first (all above PLAN_THREADS - 1 blocks alike): a count of each length, the
@@ -240,7 +244,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 // ------------------------------------------------------------------------------ shared by the roles
 struct Ctx {
   uint32_t sb, bars;
-  volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2]: blocks copied
+  volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2]: blocks copied,
+                        // [3]: buffer of the values to be mended
   uint32_t* status;
 };
 
@@ -263,6 +268,10 @@ DSA_DEV bool wait_slow(uint32_t addr, uint32_t parity, volatile int* misc, uint3
       return false;
     }
   }
+}
+DSA_DEV bool wait_1(const Ctx& c, int b, uint32_t parity) {
+  const uint32_t addr = bar(c, b);
+  return mbar_try(addr, parity) || wait_slow(addr, parity, c.misc, c.status);
 }
 // The whole warp waits and agrees on the outcome.
 DSA_DEV bool wait_w(const Ctx& c, int b, uint32_t parity) {
@@ -473,119 +482,119 @@ DSA_DEV void copies(const Params& P, const Maps& M, const Ctx& c, int n_tiles) {
 }
 
 // ------------------------------------------------------------------------------ products
-// The whole warp runs this role and one elected lane issues each product: with
-// warp-uniform control flow the descriptors stay in uniform registers.
+// One thread runs this role.  (The whole warp with an elected lane to issue, and votes on each wait,
+// took 5700 cycles for a block of both halves, whose products are 2560: the softmax, 1400 a half, was
+// waiting for the next instruction to be issued.)
 template <bool SPLIT>
-DSA_DEV void products(const Params& P, const Ctx& c, uint8_t* sm, uint32_t tmem, int n_tiles) {
+DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles) {
   const uint32_t type = P.bf16 ? (1u << 7) | (1u << 10) : 0u;
   const uint32_t ID_QK = idesc_f16(128, BLOCK, 0, 0) | type, ID_PV = idesc_f16(128, DV, 0, 1) | type;
   const uint64_t d_q = sdesc(c.sb + Smem::Q, 16, 1024);
   const uint64_t d_k = sdesc(c.sb + Smem::K, 16, 1024);
   const uint64_t d_v = sdesc(c.sb + Smem::V, PANEL, 1024);
-  uint32_t g = 0, kp = 0;
-  uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights and units of each half
-  // what is left of the block before
-  bool due[2] = {false, false}, first[2] = {false, false}, last[2] = {false, false};
-  int v_rows = 0;   // its keys that exist
-  bool v_there = false;
-
-  // waits for the values of block i; rows that are not the request's may hold anything, and 0 * NaN is not 0
-  auto values = [&](uint32_t i) {
-    if (v_there) return true;
-    const int buf = i % V_BUFS;
-    if (!wait_w(c, B_VFULL + buf, (i / V_BUFS) & 1)) return false;
-    v_there = true;
-    if (v_rows < BLOCK) {
-      uint8_t* v = sm + Smem::V + buf * Smem::VBUF;
-      const int lane = threadIdx.x & 31;
-      for (int r = v_rows + (lane >> 3); r < BLOCK; r += 4) {
-        *reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(v + PANEL + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async_smem();
-      __syncwarp();
+  // bits of the halves: whether weights are due, the block at hand is its unit's last one in the half, and parities
+  uint32_t g = 0, kp = 0, fixes = 0, due = 0, last = 0, p_parity = 0, q_parity = 0;
+  bool first = false, partial = false;   // of the block whose weights are due; partial: it has rows that are not the request's
+  Walk<SPLIT> walk(P);
+  Unit x;
+  int i = 0, blocks = 0;
+  while (true) {
+    bool more = true;
+    while (i == blocks && more) {
+      more = walk.next(P, n_tiles, x);
+      blocks = more ? max(x.blocks[0], x.blocks[1]) : 0;
+      i = 0;
     }
-    return true;
-  };
-  auto weigh = [&](int h, uint32_t i) {   // O += P V of half h, block i
-    if (!values(i) || !wait_w(c, B_PFULL + h, np[h] & 1)) return false;
-    ++np[h];
-    tc_fence_after();
-    if (elect_one()) {
-#pragma unroll
-      for (int k = 0; k < BLOCK / 16; ++k)
-        mma_ts(tmem + Tmem::O + 128 * h, tmem + Tmem::S + 128 * h + 8 * k,
-               d_v + ((uint32_t)((i % V_BUFS) * Smem::VBUF + k * 2048) >> 4), ID_PV, (!first[h] || k > 0) ? 1u : 0u);
-      if (last[h]) tc_commit(bar(c, B_OFULL + h));
-    }
-    __syncwarp();
-    due[h] = false;
-    return true;
-  };
-  auto score = [&](int h, bool new_q, bool q_done, bool k_done) {   // S of half h, the block at hand
-    if (new_q) {
-      if (!wait_w(c, B_QFULL + h, nq[h] & 1)) return false;
-      ++nq[h];
-    }
-    tc_fence_after();   // the scores before were read
+    if (!more && due == 0) return;
+    const uint32_t now = more ? (i < x.blocks[0] ? 1u : 0u) | (i < x.blocks[1] ? 2u : 0u) : 0u;
+    const uint32_t ends = now & ((i + 1 == x.blocks[0] ? 1u : 0u) | (i + 1 == x.blocks[1] ? 2u : 0u));
+    const uint32_t due_at_first = due;
+    bool v_there = false, k_there = false;
+    // a half's scores follow its weights' product with the block before; a half alone goes first, so that its scores
+    // are under way while the other's weights are waited for
 #pragma unroll 1
-    for (int p = 0; p < 3; ++p) {
-      const int slot = (kp + p) % K_PANELS;
-      if (!wait_w(c, B_KFULL + slot, ((kp + p) / K_PANELS) & 1)) return false;
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + Tmem::S + 128 * h, d_q + ((uint32_t)(h * Smem::QHALF + p * PANEL + k * 32) >> 4),
-                 d_k + ((uint32_t)(slot * PANEL + k * 32) >> 4), ID_QK, (p > 0 || k > 0) ? 1u : 0u);
-        if (k_done) tc_commit(bar(c, B_KFREE + slot));
-        if (p == 2) {
-          if (q_done) tc_commit(bar(c, B_QFREE + h));
-          tc_commit(bar(c, B_SFULL + h));
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t h = now == 2u ? 1 - t : t, bit = 1u << h;
+      if (due & bit) {   // O += P V with block g - 1
+        const uint32_t buf = (g - 1) % V_BUFS;
+        if (!v_there) {
+          if (!wait_1(c, B_VFULL + buf, ((g - 1) / V_BUFS) & 1)) return;
+          if (partial) {
+            c.misc[3] = (int)buf;
+            mbar_arrive(bar(c, B_FIX));
+            if (!wait_1(c, B_FIXED, fixes & 1)) return;
+            ++fixes;
+          }
+          v_there = true;
         }
+        const uint64_t v = d_v + ((buf * Smem::VBUF) >> 4);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (!wait_1(c, B_PFULL + 2 * h + part, (p_parity >> h) & 1)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4 * part; k < 4 * part + 4; ++k)
+            mma_ts(tmem + Tmem::O + 128 * h, tmem + Tmem::S + 128 * h + 8 * k, v + (k * 2048 >> 4), ID_PV, k > 0 || !first ? 1u : 0u);
+        }
+        p_parity ^= bit;
+        if (last & bit) tc_commit(bar(c, B_OFULL + h));
       }
-      __syncwarp();
+      if (now & bit) {   // S of block g
+        if (i == 0) {
+          if (!wait_1(c, B_QFULL + h, (q_parity >> h) & 1)) return;
+          q_parity ^= bit;
+        }
+        tc_fence_after();   // the scores before were read
+        const bool k_last = (now >> 1) == h || now == 1u;   // the last half that reads the keys
+        const uint64_t q = d_q + ((h * Smem::QHALF) >> 4);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const uint32_t slot = (kp + p) % K_PANELS;
+          if (!k_there && !wait_1(c, B_KFULL + slot, ((kp + p) / K_PANELS) & 1)) return;
+          const uint64_t k_at = d_k + ((slot * PANEL) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + Tmem::S + 128 * h, q + ((p * PANEL + k * 32) >> 4), k_at + (k * 32 >> 4), ID_QK, (p > 0 || k > 0) ? 1u : 0u);
+          if (k_last) tc_commit(bar(c, B_KFREE + slot));
+        }
+        k_there = true;
+        if (ends & bit) tc_commit(bar(c, B_QFREE + h));
+        tc_commit(bar(c, B_SFULL + h));
+      }
     }
-    return true;
-  };
+    if (due_at_first) tc_commit(bar(c, B_VFREE + (g - 1) % V_BUFS));
+    if (!more) return;
+    due = now;
+    first = i == 0;
+    last = ends;
+    partial = x.t.kv - (x.s0 + i) * BLOCK < BLOCK;
+    kp += 3;
+    ++i;
+    ++g;
+  }
+}
 
+// The values of a request's last block: rows that are not the request's may hold anything, and 0 * NaN is
+// not 0.  One warp, when the products ask for it.
+template <bool SPLIT>
+DSA_DEV void fix_values(const Params& P, const Ctx& c, uint8_t* sm, int n_tiles) {
+  const int lane = threadIdx.x & 31;
+  uint32_t fixes = 0;
   Walk<SPLIT> walk(P);
   Unit x;
   while (walk.next(P, n_tiles, x)) {
-    const int blocks = max(x.blocks[0], x.blocks[1]);
-    for (int i = 0; i < blocks; ++i, ++g) {
-      const bool now[2] = {i < x.blocks[0], i < x.blocks[1]};
-      const bool any = due[0] || due[1];
-      if (now[0] && !now[1]) {
-        if (due[0] && !weigh(0, g - 1)) return;
-        if (!score(0, i == 0, i + 1 == x.blocks[0], true)) return;
-        if (due[1] && !weigh(1, g - 1)) return;
-      } else if (now[1] && !now[0]) {
-        if (due[1] && !weigh(1, g - 1)) return;
-        if (!score(1, i == 0, i + 1 == x.blocks[1], true)) return;
-        if (due[0] && !weigh(0, g - 1)) return;
-      } else {
-        if (due[0] && !weigh(0, g - 1)) return;
-        if (!score(0, i == 0, i + 1 == x.blocks[0], false)) return;
-        if (due[1] && !weigh(1, g - 1)) return;
-        if (!score(1, i == 0, i + 1 == x.blocks[1], true)) return;
-      }
-      if (any) {
-        if (elect_one()) tc_commit(bar(c, B_VFREE + (g - 1) % V_BUFS));
-        __syncwarp();
-      }
-      kp += 3;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        due[h] = now[h];
-        first[h] = i == 0;
-        last[h] = i + 1 == x.blocks[h];
-      }
-      v_rows = x.t.kv - (x.s0 + i) * BLOCK;
-      v_there = false;
+    const int blocks = max(x.blocks[0], x.blocks[1]), rows = x.t.kv - (x.s0 + blocks - 1) * BLOCK;
+    if (blocks == 0 || rows >= BLOCK) continue;   // only the last block can have fewer
+    if (!wait_w(c, B_FIX, fixes & 1)) return;
+    ++fixes;
+    uint8_t* v = sm + Smem::V + c.misc[3] * Smem::VBUF;
+    for (int r = rows + (lane >> 3); r < BLOCK; r += 4) {
+      *reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(v + PANEL + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
+    fence_async_smem();
+    arrive_w(c, B_FIXED);
   }
-  if (due[0] && !weigh(0, g - 1)) return;
-  if (due[1]) weigh(1, g - 1);
 }
 
 // ------------------------------------------------------------------------------ softmax
@@ -654,89 +663,70 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       if (!wait_w(c, B_SFULL + h, ns & 1)) return;
       ++ns;
       tc_fence_after();
+      uint32_t x2[128];
+#pragma unroll
+      for (int k = 0; k < 128; k += 32) tmem_ld32(ts + k, *reinterpret_cast<uint32_t(*)[32]>(x2 + k));
+      const uint64_t add = pair(-m, -m);
+      tc_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 128; e += 2) fma2(x2[e], x2[e + 1], mul, add);
+      if (base + BLOCK - 1 > pos0 + first) {   // the half's first row sees less
+        const int last = pos - base;
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > last) x2[e] = 0xFF800000u;   // -inf
+      }
+      float t4[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        t4[q] = fmaxf(__uint_as_float(x2[q]), __uint_as_float(x2[q + 4]));
+#pragma unroll
+        for (int e = 8; e < 128; e += 8) t4[q] = max3(t4[q], __uint_as_float(x2[e + q]), __uint_as_float(x2[e + 4 + q]));
+      }
+      const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+      if (__any_sync(0xFFFFFFFFu, fresh || top > MOST)) {
+        const bool up = top > (fresh ? -INFINITY : LAG);
+        // by delta, not by m's rounded step: from 2^23 on m + delta is rounded
+        const float delta = up ? floorf(top) : 0.f;
+        const float f = (up && !fresh) ? ex2(-delta) : 1.0f;
+        if (up) fresh = false;
+        m += delta;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < 128; ++e) x2[e] = __float_as_uint(__uint_as_float(x2[e]) - delta);
+        if (i > 0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+          // the product of the block before is done: these scores were issued after it
 #pragma unroll 1
-      for (int s = 0; s < 2; ++s) {   // 64 keys at a time
-        uint32_t x2[64];
-        tmem_ld32(ts + 64 * s, *reinterpret_cast<uint32_t(*)[32]>(x2));
-        tmem_ld32(ts + 64 * s + 32, *reinterpret_cast<uint32_t(*)[32]>(x2 + 32));
-        const uint64_t add = pair(-m, -m);
-        tc_wait_ld();
+          for (int k = 0; k < DV; k += 8) {
+            uint32_t o[8];
+            tmem_ld8(to + k, o);
+            tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) fma2(x2[e], x2[e + 1], mul, add);
-        const int j0 = base + 64 * s;
-        if (j0 + 63 > pos0 + first) {   // the half's first row sees less
-          const int last = pos - j0;
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e > last) x2[e] = 0xFF800000u;   // -inf
-        }
-        float t4[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          t4[q] = fmaxf(__uint_as_float(x2[q]), __uint_as_float(x2[q + 4]));
-#pragma unroll
-          for (int e = 8; e < 64; e += 8) t4[q] = max3(t4[q], __uint_as_float(x2[e + q]), __uint_as_float(x2[e + 4 + q]));
-        }
-        const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-        if (__any_sync(0xFFFFFFFFu, fresh || top > MOST)) {
-          // what this thread stored last (the weights of the block's first part) is read again
-          // below, and only this wait puts a tensor memory load behind a store
-          tc_wait_st();
-          const bool up = top > (fresh ? -INFINITY : LAG);
-          // by delta, not by m's rounded step: from 2^23 on m + delta is rounded
-          const float delta = up ? floorf(top) : 0.f;
-          const float f = (up && !fresh) ? ex2(-delta) : 1.0f;
-          if (up) fresh = false;
-          m += delta;
-          l *= f;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x2[e] = __float_as_uint(__uint_as_float(x2[e]) - delta);
-          if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
-            if (i > 0) {
-              // the product of the block before is done: these scores were issued after it
-#pragma unroll 1
-              for (int k = 0; k < DV; k += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + k, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(to + k, o);
-              }
-            }
-            if (s == 1) {   // the weights of the block's first part
-#pragma unroll 1
-              for (int k = 0; k < 32; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(ts + k, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float2 y = unpack<BF16>(o[e]);
-                  o[e] = pack<BF16>(y.x * f, y.y * f);
-                }
-                tmem_st16(ts + k, o);
-              }
-            }
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st8(to + k, o);
           }
         }
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {   // the products begin with the first 64 keys
         uint32_t p[32];
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float w0 = ex2(__uint_as_float(x2[2 * e])), w1 = ex2(__uint_as_float(x2[2 * e + 1]));
-          const float w2 = ex2(__uint_as_float(x2[2 * e + 2])), w3 = ex2(__uint_as_float(x2[2 * e + 3]));
+          const uint32_t* u = x2 + 64 * part + 2 * e;
+          const float w0 = ex2(__uint_as_float(u[0])), w1 = ex2(__uint_as_float(u[1]));
+          const float w2 = ex2(__uint_as_float(u[2])), w3 = ex2(__uint_as_float(u[3]));
           add2(s0, s1, w0, w1);
           add2(s2, s3, w2, w3);
           p[e] = pack<BF16>(w0, w1);
           p[e + 1] = pack<BF16>(w2, w3);
         }
         l += (s0 + s1) + (s2 + s3);
-        tmem_st32(ts + 32 * s, p);
+        tmem_st32(ts + 32 * part, p);
+        tc_wait_st();
+        tc_fence_before();
+        arrive_w(c, B_PFULL + 2 * h + part);
       }
-      tc_wait_st();
-      tc_fence_before();
-      arrive_w(c, B_PFULL + h);
     }
     // ---- result
     if (blocks > 0) {
@@ -806,7 +796,7 @@ __global__ void __launch_bounds__(THREADS, 1) mla_kernel(const __grid_constant__
   const int warp = threadIdx.x >> 5;
   if (SPLIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join
   if (threadIdx.x == 0) {
-    for (int i = 0; i < N_BAR; ++i) mbar_init(bar(c, i), i == B_PFULL || i == B_PFULL + 1 ? 4 : 1);
+    for (int i = 0; i < N_BAR; ++i) mbar_init(bar(c, i), i >= B_PFULL && i < B_PFULL + 4 ? 4 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     c.misc[1] = c.misc[2] = 0;
   }
@@ -823,7 +813,8 @@ __global__ void __launch_bounds__(THREADS, 1) mla_kernel(const __grid_constant__
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
     if (warp == W_COPY) copies<SPLIT>(P, M, c, n_tiles);
-    else if (warp == W_MMA) products<SPLIT>(P, c, smem, tmem, n_tiles);
+    else if (warp == W_FIX) fix_values<SPLIT>(P, c, smem, n_tiles);
+    else if (warp == W_MMA && elect_one()) products<SPLIT>(P, c, tmem, n_tiles);
   }
   __syncwarp();
   if (warp == W_MMA) {
@@ -1099,7 +1090,7 @@ int dsa_mla_prefill_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k
        !describe_rope(&M.r, fn, P.bf16, k_rope, P.n_keys, pitch(k_rope_ld, DR, P.n_keys))))
     return DSA_ERR_CUDA;
   const size_t smem = (size_t)(P.n_req + 1) * sizeof(int);
-  static_assert((DSA_MLA_MAX_REQ + 1) * sizeof(int) <= 36 * 1024, "the plan's dynamic shared memory needs no permission");
+  static_assert((DSA_MLA_MAX_REQ + 1) * sizeof(int) <= 34 * 1024, "the plan's dynamic shared memory needs no permission");
   plan_kernel<<<1, PLAN_THREADS, smem, st>>>(P);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (P.bf16) return P.split ? launch<true, true>(P, M, st) : launch<true, false>(P, M, st);
