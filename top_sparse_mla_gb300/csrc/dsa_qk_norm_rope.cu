@@ -1,10 +1,12 @@
 // RMS norm and rotation of the heads of queries and keys (include/dsa_qk_norm_rope.h).
 //
-// What bounds it: memory, each value read and written once.  The rows (token, head) of q and
-// k are numbered token by token, and a CTA has R neighbouring ones.  It forms the cosines and
-// sines of its tokens once, in shared memory, for all their heads, while its first rows are on
-// their way.  A row belongs to G lanes of 8 values each (16-byte loads and stores).  Halves of
-// a head that turn together lie rotary_dim / 16 lanes apart and are exchanged by shuffles.
+// What bounds it: memory, each value read and written once.  A row (token, head) belongs to G lanes of 16
+// values each, two 16-byte parts: of a rotary half and of the other half what turns with it, so that a lane
+// has both values of its pairs; or, interleaved and behind the rotary values, neighbours.  A lane group goes
+// through heads of one token and forms the cosines and sines of its lanes' pairs once, in registers, while
+// its first rows are on their way.  (Kept in shared memory for the CTA's tokens and read with every row, and
+// with a lane's values side by side and their partners exchanged by shuffles, both through one pipe, 16381
+// tokens of 64 + 8 heads of 128 took 198 us against 104.6 now, 5.8 TB/s, 0.85 of a copy.)
 //
 // The angle of pair i is position * turns[i] in 64-bit fixed point, a fraction of a turn that
 // wraps by itself: an fp32 angle would be off by 2^-24 of itself, half a turn at position 2^24.
@@ -21,8 +23,9 @@ namespace dsa_qk {
 
 constexpr int THREADS = 256;
 constexpr int MAX_PAIRS = 128;     // rotary pairs of a head
-constexpr int TABLE = 4096;        // cosines and sines of a CTA: 32 KB
 constexpr int AT_ONCE = 4;         // rows of a lane group in flight
+constexpr int MOST_ROWS = 32;      // heads that a lane group goes through with one token's angles, at most
+constexpr int SPREAD = 4, ANGLE_ROWS = 4;   // see launch()
 
 struct Side {   // queries or keys
   const uint16_t *x, *w;
@@ -34,138 +37,175 @@ struct Params {
   Side q, k;
   const int32_t* positions;
   int n_tokens, h_q, heads, lanes;   // heads: of both; lanes: of a row that hold values
-  int rows;                          // of a CTA
-  int pairs, first, half;            // rotary pairs; first lane of the rotary values; lanes of half of them
+  int rows, q_chunks, chunks;        // heads of a lane group, and lane groups of a token: of its queries, and all
+  int first, half;                   // parts of 8 values: the first rotary one, and half of them
   int interleaved, fp16;
   float inv_d, eps;
   // rotary frequency of pair i as a 64-bit fixed-point fraction of a turn
   unsigned long long turns[MAX_PAIRS];
 };
 
-__device__ __forceinline__ float2 unpack(uint32_t w, int fp16) {
-  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+template <bool FP16>
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  if (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint32_t pack(float a, float b, int fp16) {
-  if (fp16) return dsa::pack_f16x2(a, b);
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack(float2 v) {
+  if (FP16) return dsa::pack_f16x2(v.x, v.y);
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
   return r;
 }
-__device__ __forceinline__ void unpack8(uint4 v, int fp16, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack(w[i], fp16);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
+template <bool FP16>
+__device__ __forceinline__ void unpack8(uint4 v, float2* f) {
+  f[0] = unpack<FP16>(v.x);
+  f[1] = unpack<FP16>(v.y);
+  f[2] = unpack<FP16>(v.z);
+  f[3] = unpack<FP16>(v.w);
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ unsigned long long bits(float2 v) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 floats(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return floats(r);
 }
 
-template <int G, bool INTERLEAVED>
+template <int G, bool INTERLEAVED, bool FP16>
 __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(16) float2 table[];   // [tokens of the CTA][pairs] (cos, sin)
-  constexpr int GROUPS = THREADS / G;
-  const int lane = threadIdx.x & 31, l = lane & (G - 1), group = threadIdx.x / G;
-  const long long row0 = (long long)blockIdx.x * P.rows;
-  const long long token0 = row0 / P.heads;
-  const int head0 = (int)(row0 - token0 * P.heads);
-  const int rows = (int)min((long long)P.rows, (long long)P.n_tokens * P.heads - row0);
-  const int fp16 = P.fp16;
-  const bool holds = l < P.lanes;
+  const int l = threadIdx.x & (G - 1);
+  const long long unit = (long long)blockIdx.x * (THREADS / G) + threadIdx.x / G, at = unit / P.chunks;
+  const bool there = at < P.n_tokens;
+  const int token = there ? (int)at : P.n_tokens - 1, chunk = (int)(unit - at * P.chunks);
+  const bool key = chunk >= P.q_chunks, holds = l < P.lanes;
+  // heads of this lane group, all of the queries or all of the keys
+  const int head0 = (chunk - (key ? P.q_chunks : 0)) * P.rows, heads = key ? P.heads - P.h_q : P.h_q;
+  const int rows = there && holds ? min(P.rows, heads - head0) : 0;
+  const uint16_t* w = key ? P.k.w : P.q.w;
+  const long long hd = key ? P.k.hd : P.q.hd, y_hd = key ? P.k.y_hd : P.q.y_hd;
+  const uint16_t* x_row = (key ? P.k.x : P.q.x) + token * (key ? P.k.ld : P.q.ld) + head0 * hd;
+  uint16_t* y_row = (key ? P.k.y : P.q.y) + token * (key ? P.k.y_ld : P.q.y_ld) + head0 * y_hd;
 
-  struct Row {
-    int token, head;   // counted from token0
-  };
-  auto row = [&](int i) {
-    const unsigned at = (unsigned)(head0 + i);
-    const unsigned t = at / (unsigned)P.heads;
-    return Row{(int)t, (int)(at - t * P.heads)};
-  };
-  auto load = [&](int i) -> uint4 {
-    if (i >= rows || !holds) return make_uint4(0u, 0u, 0u, 0u);
-    const Row r = row(i);
-    const bool key = r.head >= P.h_q;
-    const Side& s = key ? P.k : P.q;
-    return *reinterpret_cast<const uint4*>(s.x + (token0 + r.token) * s.ld + (r.head - (key ? P.h_q : 0)) * s.hd + 8 * l);
-  };
-
-  uint4 v[AT_ONCE];
+  // this lane's parts of 8 values: parts of a head are numbered 0 .. 2 lanes - 1
+  int part[2] = {2 * l, 2 * l + 1};
+  bool turns = false;   // both parts turn; else, interleaved, each may
+  if (!INTERLEAVED) {
+    if (l < P.half) {
+      part[0] = P.first + l;
+      part[1] = P.first + P.half + l;
+      turns = true;
+    } else {   // of the parts in front of the rotary ones and behind them
 #pragma unroll
-  for (int a = 0; a < AT_ONCE; ++a) v[a] = load(group + a * GROUPS);
-
-  const int tokens = row(rows - 1).token + 1;
-  for (int i = threadIdx.x; i < tokens * P.pairs; i += THREADS) {
-    const int t = i / P.pairs, pair = i - t * P.pairs;
-    const unsigned long long turn = (unsigned long long)(long long)__ldg(P.positions + token0 + t) * P.turns[pair];
-    float sn, cs;
-    sincospif((float)(turn >> 40) * 1.1920928955078125e-07f, &sn, &cs);   // 2 * (its 24 highest bits / 2^24)
-    table[i] = make_float2(cs, sn);
+      for (int s = 0; s < 2; ++s) {
+        part[s] -= 2 * P.half;
+        if (part[s] >= P.first) part[s] += 2 * P.half;
+      }
+    }
   }
-  uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
-  if (holds && P.q.w) qw = __ldg(reinterpret_cast<const uint4*>(P.q.w) + l);
-  if (holds && P.k.w) kw = __ldg(reinterpret_cast<const uint4*>(P.k.w) + l);
-  __syncthreads();
+  struct Row {
+    uint4 v[2];
+  };
+  auto load = [&](int i) {
+    Row r;
+    r.v[0] = r.v[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < rows) {
+      const uint16_t* x = x_row + i * hd;
+      r.v[0] = *reinterpret_cast<const uint4*>(x + 8 * part[0]);
+      r.v[1] = *reinterpret_cast<const uint4*>(x + 8 * part[1]);
+    }
+    return r;
+  };
+  const int pos = __ldg(P.positions + token);
+  Row v[AT_ONCE];
+#pragma unroll
+  for (int a = 0; a < AT_ONCE; ++a) v[a] = load(a);
+  const bool norm = w != nullptr;
+  float2 weight[8];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    unpack8<FP16>(holds && norm ? __ldg(reinterpret_cast<const uint4*>(w) + part[s]) : make_uint4(0u, 0u, 0u, 0u), weight + 4 * s);
+  // (cos, sin) of this lane's pairs: of the values e of both parts, or, interleaved, of the pairs of the first part and
+  // of the second
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    int pair = 8 * l + e;
+    bool turn = turns;
+    if (INTERLEAVED) {
+      const int p = part[e >> 2] - P.first;
+      turn = p >= 0 && p < 2 * P.half;
+      pair = 4 * p + (e & 3);
+    }
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+    if (turn) {
+      const unsigned long long t = (unsigned long long)(long long)pos * P.turns[pair];
+      sincospif((float)(t >> 40) * 1.1920928955078125e-07f, &sn[e], &cs[e]);   // 2 * (its 24 highest bits / 2^24)
+    }
+  }
 
-  // this lane's place among the rotary values
-  const int at = l - P.first;
-  const bool turns = at >= 0 && at < 2 * P.half;
-  const int partner = (lane & ~(G - 1)) + (turns ? (at < P.half ? l + P.half : l - P.half) : l);
-  const int pair0 = INTERLEAVED ? 4 * at : 8 * (at < P.half ? at : at - P.half);
-  const float side = at < P.half ? -1.f : 1.f;
-
-  for (int i0 = group; i0 < rows + group; i0 += AT_ONCE * GROUPS) {   // the same trips for every group: shuffles
+  // every lane group of a warp makes the same trips: shuffles
+  for (int i0 = 0; i0 < P.rows; i0 += AT_ONCE) {
 #pragma unroll
     for (int a = 0; a < AT_ONCE; ++a) {
-      const int i = i0 + a * GROUPS;
-      const bool live = i < rows;
-      const Row r = row(min(i, rows - 1));
-      const bool key = r.head >= P.h_q;
-      float x[8];
-      unpack8(v[a], fp16, x);
-      v[a] = load(i + AT_ONCE * GROUPS);
-      const bool norm = (key ? P.k.w : P.q.w) != nullptr;
-      float ss = 0.f;
+      const int i = i0 + a;
+      if (i >= P.rows) break;
+      float2 x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int s = 0; s < 2; ++s) unpack8<FP16>(v[a].v[s], x + 4 * s);
+      v[a] = load(i + AT_ONCE);
+      float2 ss = mul2(x[0], x[0]);
 #pragma unroll
-      for (int o = G / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      for (int e = 1; e < 8; ++e) ss = fma2(x[e], x[e], ss);
+      float sum = ss.x + ss.y;
+#pragma unroll
+      for (int o = G / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
       if (norm) {
-        const float inv = 1.0f / sqrtf(fmaf(ss, P.inv_d, P.eps));
-        float w[8];
-        unpack8(key ? kw : qw, fp16, w);
+        const float inv = __frsqrt_rn(fmaf(sum, P.inv_d, P.eps));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+        for (int e = 0; e < 8; ++e) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), weight[e]);
       }
-      const float2* cs = table + (turns ? r.token * P.pairs + pair0 : 0);
+      // values that do not turn are left as they are: 0 * infinity is not 0
       if (INTERLEAVED) {
-        if (turns) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = cs[e];
-            const float b = x[2 * e + 1];
-            x[2 * e + 1] = fmaf(x[2 * e], f.y, b * f.x);
-            x[2 * e] = fmaf(x[2 * e], f.x, -b * f.y);
+        for (int s = 0; s < 2; ++s) {
+          const int p = part[s] - P.first;
+          if (p >= 0 && p < 2 * P.half) {
+#pragma unroll
+            for (int e = 4 * s; e < 4 * s + 4; ++e)
+              x[e] = make_float2(fmaf(x[e].x, cs[e], -x[e].y * sn[e]), fmaf(x[e].x, sn[e], x[e].y * cs[e]));
           }
         }
-      } else if (P.pairs > 0) {
+      } else if (turns) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = __shfl_sync(0xFFFFFFFFu, x[e], partner);
-          if (turns) {
-            const float2 f = cs[e];
-            x[e] = fmaf(x[e], f.x, side * other * f.y);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]), n = make_float2(sn[2 * e], sn[2 * e + 1]);
+          const float2 b = x[4 + e];
+          x[4 + e] = fma2(x[e], n, mul2(b, c));
+          x[e] = fma2(x[e], c, mul2(b, make_float2(-n.x, -n.y)));
         }
       }
-      if (live && holds) {
-        const Side& s = key ? P.k : P.q;
-        uint4 o;
-        o.x = pack(x[0], x[1], fp16);
-        o.y = pack(x[2], x[3], fp16);
-        o.z = pack(x[4], x[5], fp16);
-        o.w = pack(x[6], x[7], fp16);
-        *reinterpret_cast<uint4*>(s.y + (token0 + r.token) * s.y_ld + (r.head - (key ? P.h_q : 0)) * s.y_hd + 8 * l) = o;
+      if (i < rows) {
+        uint16_t* y = y_row + i * y_hd;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          *reinterpret_cast<uint4*>(y + 8 * part[s]) =
+              make_uint4(pack<FP16>(x[4 * s]), pack<FP16>(x[4 * s + 1]), pack<FP16>(x[4 * s + 2]), pack<FP16>(x[4 * s + 3]));
       }
     }
   }
@@ -203,24 +243,31 @@ static void turn_table(float base, int dim, unsigned long long* out) {
 }
 
 template <int G>
-static int launch(const Params& P, long long total, int sms, cudaStream_t st) {
+static int launch(const Params& P, int sms, cudaStream_t st) {
   Params Q = P;
   constexpr int groups = THREADS / G;
-  // as many rows as give every SM its CTAs, at most what AT_ONCE loads of every group bring at
-  // four rounds, and no more tokens than the table has room for
-  long long rows = (total + 4LL * sms - 1) / (4LL * sms);
-  const long long most = 4LL * AT_ONCE * groups;
-  if (rows > most) rows = most;
-  rows = (rows + groups - 1) / groups * groups;
-  // rows that begin anywhere touch at most (rows - 2) / heads + 2 tokens
-  const long long tokens = P.pairs > 0 ? TABLE / P.pairs : rows + 1;
-  if ((rows - 2) / P.heads + 2 > tokens) rows = (tokens - 2) * P.heads + 1;
-  Q.rows = (int)rows;
-  const long long grid = (total + rows - 1) / rows;
+  // As many rows of a lane group as leave every SM SPREAD CTAs or fewer, and of those the number that costs a
+  // token least: groups take as long as the fullest one, and a group's angles as long as some rows.  us, SPREAD
+  // 4 and 8: 2123 tokens of 16 heads of 192 10.4 and 14.4; 64 of 64 + 8 of 128 10.5 and 10.7.  (With AT_ONCE 2
+  // in place of 4, 16381 of these 118.8 against 104.6.)
+  const long long total = (long long)P.n_tokens * P.heads, spread = (long long)SPREAD * sms * groups;
+  const long long most = (total + spread - 1) / spread < MOST_ROWS ? (total + spread - 1) / spread : MOST_ROWS;
+  long long least = 1LL << 60;
+  for (int rows = 1; rows <= most; ++rows) {
+    const int q_chunks = (P.h_q + rows - 1) / rows, chunks = q_chunks + (P.heads - P.h_q + rows - 1) / rows;
+    const long long cost = (long long)chunks * (rows + ANGLE_ROWS);
+    if (cost <= least) {
+      least = cost;
+      Q.rows = rows;
+      Q.q_chunks = q_chunks;
+      Q.chunks = chunks;
+    }
+  }
+  const long long grid = ((long long)P.n_tokens * Q.chunks + groups - 1) / groups;
   if (grid > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
-  const size_t smem = (size_t)((rows - 2) / P.heads + 2) * P.pairs * sizeof(float2);
-  if (P.interleaved) norm_rope_kernel<G, true><<<(unsigned)grid, THREADS, smem, st>>>(Q);
-  else norm_rope_kernel<G, false><<<(unsigned)grid, THREADS, smem, st>>>(Q);
+  auto run = [&](auto kernel) { kernel<<<(unsigned)grid, THREADS, 0, st>>>(Q); };
+  if (P.fp16) P.interleaved ? run(norm_rope_kernel<G, true, true>) : run(norm_rope_kernel<G, false, true>);
+  else P.interleaved ? run(norm_rope_kernel<G, true, false>) : run(norm_rope_kernel<G, false, false>);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
@@ -277,9 +324,8 @@ extern "C" int dsa_qk_norm_rope(const void* q, int64_t q_ld, int64_t q_hd, const
   P.n_tokens = p->n_tokens;
   P.h_q = p->h_q;
   P.heads = p->h_q + p->h_k;
-  P.lanes = p->d / 8;
-  P.rows = 0;
-  P.pairs = p->rotary_dim / 2;
+  P.lanes = p->d / 16;
+  P.rows = P.q_chunks = P.chunks = 0;
   P.first = p->rotary_start / 8;
   P.half = p->rotary_dim / 16;
   P.interleaved = (p->flags & DSA_QK_FLAG_INTERLEAVED) != 0;
@@ -287,7 +333,6 @@ extern "C" int dsa_qk_norm_rope(const void* q, int64_t q_ld, int64_t q_hd, const
   P.inv_d = 1.0f / (float)p->d;
   P.eps = p->rms_eps;
   turn_table(p->rope_base, p->rotary_dim, P.turns);
-  const long long total = (long long)p->n_tokens * P.heads;
   const cudaStream_t st = (cudaStream_t)stream;
-  return p->d <= 64 ? launch<8>(P, total, sms, st) : p->d <= 128 ? launch<16>(P, total, sms, st) : launch<32>(P, total, sms, st);
+  return p->d <= 64 ? launch<4>(P, sms, st) : p->d <= 128 ? launch<8>(P, sms, st) : launch<16>(P, sms, st);
 }
