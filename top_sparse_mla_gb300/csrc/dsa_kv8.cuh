@@ -14,6 +14,7 @@ namespace dsa_kv8 {
 
 constexpr int STEP = 16;          // cached tokens of one step of a warp; every page size is a multiple
 constexpr int TILE_ROWS = 256;    // query rows of a tile
+constexpr int TILE_BLOCK = 128;   // cached tokens of a tile's block
 constexpr int MAX_CLUSTER = 16;
 // The softmax's sum is that of w / v_scale, but where pages' value scales are so far apart that a w may
 // be too small for fp32: there it is that of 2^(score - maximum).  rows_kernel goes by each page's
@@ -48,7 +49,8 @@ enum { SHARED = 0, OWN = 1 };
 // `req`, and of those the ones up to their own positions, pos0 for the first query.
 struct Part {
   int q0, q_len, pos0, lo;
-  int hi, req, side, pad;
+  int hi, req, side, group;   // group: of a request's own part, or -1
+  int tile0, pad[3];          // the first of its tiles, where it has some
 };
 
 struct Params {
@@ -77,7 +79,14 @@ struct Params {
   const int32_t *cu_groups, *prefix_lens;
   float* part_o;
   float2* part_ml;
-  int n_groups;
+  // Tiles whose blocks are shared out (PREFIX and SPLIT): all blocks, of all heads of all tiles, lie in a row.  The ones in
+  // front of each tile, by head; where each CTA's begin, with the unit that is there; and the first and last CTA of each unit.
+  // m, l and O of a CTA's two pieces: of a unit that it continued (0), and of one that it began (1)
+  long long *tile_steps, *tile_cuts;
+  int* cut_units;
+  int2* unit_ctas;
+  float* pieces;
+  int n_groups, tile_shares;
   uint32_t test_block;   // block of CTA 0 at which the copies stop (DSA_KV8_FLAG_TEST_WAIT_TIMEOUT)
   float scale_log2;   // softmax_scale * log2 e
 };
@@ -106,6 +115,8 @@ __device__ __forceinline__ Request request(const Params& P, int r) {
   a.lo = x.w; a.hi = y.x; a.req = y.y; a.side = y.z;
   return a;
 }
+// floats of a piece: O in the order [d / 4][row][4], m, l
+__device__ __host__ __forceinline__ size_t piece_size(int d) { return (size_t)TILE_ROWS * (d + 2); }
 // a query row's place in part_o and part_ml
 __device__ __forceinline__ long long part_row(const Params& P, int side, int token, int head) {
   return ((long long)side * P.n_tokens + token) * P.h_q + head;

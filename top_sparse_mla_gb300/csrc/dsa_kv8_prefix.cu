@@ -20,56 +20,72 @@ constexpr int LAUNCH_REGS = 128;   // of a thread of the tiles' kernel
 namespace dsa_kv8 {
 
 // ------------------------------------------------------------------------------ join
-// CTAs (x, r) have the query rows of request r; a thread takes 8 dims of a row at a time.
-constexpr int JOIN_THREADS = 256, JOIN_TRIPS = 4;
+// CTAs (x, r) have the query rows of request r; a thread takes 8 dims of a row at a time.  The pieces of
+// a part are joined in their order, and then the parts.
+constexpr int JOIN_THREADS = 256;
+
+struct Sum {   // of a row: O and l in units of 2^m
+  float m, l, o[8];
+  __device__ __forceinline__ void add(float m1, float l1, float4 a, float4 b) {
+    const float top = fmaxf(m, m1), f0 = ex2(m - top), f1 = ex2(m1 - top);
+    l = scaled(l, m - top) + scaled(l1, m1 - top);
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e], f1, o[e] * f0);
+    m = top;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void add_part(const Params& P, const Part& a, int token, int head, int k, Sum& sum) {
+  if (a.q_len * P.group > P.small_rows && P.tile_shares) {
+    const int row = (token - a.q0) * P.group + head % P.group, tile = a.tile0 + row / TILE_ROWS, r = row % TILE_ROWS;
+    const int2 by = P.unit_ctas[tile * P.h_kv + head / P.group];
+    const int b0 = by.x, b1 = by.y;
+    if (b0 != b1) {
+#pragma unroll 4
+      for (int b = b0; b <= b1; ++b) {
+        const float* piece = P.pieces + (2LL * b + (b == b0 ? 1 : 0)) * piece_size(D);
+        const float m = piece[TILE_ROWS * D + r];
+        if (m == NOTHING) continue;   // O is not written
+        const float4* o = reinterpret_cast<const float4*>(piece + (k / 4 * TILE_ROWS + r) * 4);
+        sum.add(m, piece[TILE_ROWS * (D + 1) + r], o[0], o[TILE_ROWS]);
+      }
+      return;
+    }
+  }
+  const long long at = part_row(P, a.side, token, head);
+  const float2 ml = P.part_ml[at];
+  const float4* o = reinterpret_cast<const float4*>(P.part_o + at * D + k);
+  sum.add(ml.x, ml.y, o[0], o[1]);
+}
+
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Request a = request<true>(P, P.n_groups + blockIdx.y);
-  const bool both = a.lo > 0;
-  const long long items = (long long)a.q_len * P.h_q * (D / 8);
+  const Part own = P.parts[P.n_groups + blockIdx.y];
+  const Part shared = P.parts[own.lo > 0 ? own.group : P.n_groups + blockIdx.y];
+  const long long items = (long long)own.q_len * P.h_q * (D / 8);
   for (long long u = (long long)blockIdx.x * JOIN_THREADS + threadIdx.x; u < items; u += (long long)gridDim.x * JOIN_THREADS) {
-    const int k = (int)(u % (D / 8)) * 8;
-    const long long row = u / (D / 8);
-    const int i = (int)(row / P.h_q), head = (int)(row - (long long)i * P.h_q), token = a.q0 + i;
-    float m = 0.f, l = 0.f, o[8];
-    float2 ml[2];
-    float4 v[2][2];
+    // the heads of a KV head side by side, as their rows are in a piece
+    const long long v = u / P.group, row = v / (D / 8);
+    const int k = (int)(v % (D / 8)) * 8, i = (int)(row / P.h_kv);
+    const int head = (int)(row - (long long)i * P.h_kv) * P.group + (int)(u - v * P.group), token = own.q0 + i;
+    Sum s;
+    s.m = M_INIT;
+    s.l = 0.f;
 #pragma unroll
-    for (int side = SHARED; side <= OWN; ++side) {
-      ml[side] = make_float2(M_INIT, 0.f);
-      v[side][0] = v[side][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (side == OWN || both) {
-        const long long at = part_row(P, side, token, head);
-        ml[side] = P.part_ml[at];
-        const float4* from = reinterpret_cast<const float4*>(P.part_o + at * D + k);
-        v[side][0] = from[0];
-        v[side][1] = from[1];
-      }
-    }
-    m = fmaxf(ml[0].x, ml[1].x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = 0.f;
-#pragma unroll
-    for (int side = SHARED; side <= OWN; ++side) {
-      const float f = ex2(ml[side].x - m);
-      l += scaled(ml[side].y, ml[side].x - m);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        o[4 * q] = fmaf(v[side][q].x, f, o[4 * q]);
-        o[4 * q + 1] = fmaf(v[side][q].y, f, o[4 * q + 1]);
-        o[4 * q + 2] = fmaf(v[side][q].z, f, o[4 * q + 2]);
-        o[4 * q + 3] = fmaf(v[side][q].w, f, o[4 * q + 3]);
-      }
-    }
-    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // a NaN sum stays one
+    for (int e = 0; e < 8; ++e) s.o[e] = 0.f;
+    if (own.lo > 0) add_part<D>(P, shared, token, head, k, s);
+    add_part<D>(P, own, token, head, k, s);
+    const float inv = s.l > 0.f ? 1.0f / s.l : (s.l == 0.f ? 0.f : s.l);   // a NaN sum stays one
     uint4 w;
-    w.x = pack(o[0] * inv, o[1] * inv, P.fp16);
-    w.y = pack(o[2] * inv, o[3] * inv, P.fp16);
-    w.z = pack(o[4] * inv, o[5] * inv, P.fp16);
-    w.w = pack(o[6] * inv, o[7] * inv, P.fp16);
+    w.x = pack(s.o[0] * inv, s.o[1] * inv, P.fp16);
+    w.y = pack(s.o[2] * inv, s.o[3] * inv, P.fp16);
+    w.z = pack(s.o[4] * inv, s.o[5] * inv, P.fp16);
+    w.w = pack(s.o[6] * inv, s.o[7] * inv, P.fp16);
     *reinterpret_cast<uint4*>(P.out + token * P.out_ld + head * P.out_hd + k) = w;
-    if (k == 0 && P.lse) P.lse[(long long)token * P.h_q + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+    if (k == 0 && P.lse) P.lse[(long long)token * P.h_q + head] = s.l == 0.f ? -INFINITY : 0.6931471805599453f * (s.m + log2f(s.l));
   }
 }
 
@@ -83,17 +99,34 @@ static int check_prefix(const dsa_kv8_params* p, int n_groups) {
 
 struct PrefixLayout {
   Layout base;
-  size_t parts, part_o, part_ml, bytes;
+  bool tile_shares;
+  size_t parts, part_o, part_ml, tile_steps, tile_cuts, cut_units, unit_ctas, pieces, bytes;
 };
+
+// Tiles and heads of an SM below which the tiles' blocks are shared out to all SMs alike, whatever their
+// lengths; with more of them, whole ones keep the SMs as busy.
+constexpr int SHARE_UNITS = 2;
+constexpr int MOST_SHARED_TILES = 1024;   // for the plan's shared memory
+
+// All query rows of the batch by KV head, where rows_kernel can take them: no tiles then
+static int batch_rows(const dsa_kv8_params* p) {
+  const long long rows = (long long)p->n_tokens * (p->h_q / p->h_kv);
+  return rows <= MAX_ROWS ? (int)rows : 0;
+}
+static int prefix_row_tiles(const dsa_kv8_params* p) {
+  const int rows = batch_rows(p);
+  return rows == 0 ? row_tiles(p) : rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
 
 static PrefixLayout prefix_layout(const dsa_kv8_params* p, int n_groups, int sms) {
   PrefixLayout L;
-  const size_t group = p->h_q / p->h_kv, rows = 8 * (size_t)row_tiles(p), queries = (size_t)p->n_tokens * p->h_q;
+  const size_t group = p->h_q / p->h_kv, rows = 8 * (size_t)prefix_row_tiles(p), queries = (size_t)p->n_tokens * p->h_q;
   Layout& b = L.base;
-  b.n_shares = ctas_per_sm(p->d, row_tiles(p)) * sms;
+  b.n_shares = ctas_per_sm(p->d, prefix_row_tiles(p)) * sms;
   // ascending cu_q and cu_groups cannot give more
   b.max_tiles = (int)((p->n_tokens * group + (TILE_ROWS - 1) * (size_t)n_groups) / TILE_ROWS);
-  if (has_tiles(p)) b.max_tiles += (int)((p->n_tokens * group + (TILE_ROWS - 1) * (size_t)p->n_req) / TILE_ROWS);
+  if (batch_rows(p) > 0 || n_groups + p->n_req == 0) b.max_tiles = 0;
+  else if (has_tiles(p)) b.max_tiles += (int)((p->n_tokens * group + (TILE_ROWS - 1) * (size_t)p->n_req) / TILE_ROWS);
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -107,19 +140,25 @@ static PrefixLayout prefix_layout(const dsa_kv8_params* p, int n_groups, int sms
   L.parts = take((size_t)(p->n_req + n_groups) * sizeof(Part));
   L.part_o = take(2 * queries * p->d * sizeof(float));
   L.part_ml = take(2 * queries * sizeof(float2));
+  L.tile_shares = b.max_tiles > 0 && b.max_tiles < MOST_SHARED_TILES && (long long)b.max_tiles * p->h_kv < SHARE_UNITS * (long long)sms;
+  L.tile_steps = take(L.tile_shares ? (b.max_tiles + 1) * sizeof(long long) : 0);
+  L.tile_cuts = take(L.tile_shares ? (sms + 1) * sizeof(long long) : 0);
+  L.cut_units = take(L.tile_shares ? sms * sizeof(int) : 0);
+  L.unit_ctas = take(L.tile_shares ? (size_t)b.max_tiles * p->h_kv * sizeof(int2) : 0);
+  L.pieces = take(L.tile_shares ? 2 * (size_t)sms * piece_size(p->d) * sizeof(float) : 0);
   L.bytes = b.bytes = at;
   return L;
 }
 
 template <int D>
 static int launch_prefix(const dsa_kv8_params* p, const Params& P, cudaStream_t st) {
-  const int nt = row_tiles(p);
+  const int nt = prefix_row_tiles(p);
   int rc = nt == 1 ? launch_rows<D, 1, true>(P, false, st) : nt == 2 ? launch_rows<D, 2, true>(P, false, st) : launch_rows<D, 4, true>(P, false, st);
   if (rc == DSA_OK && P.has_tiles) rc = launch_tiles_of<true>(D, P, st);
   if (rc != DSA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  const long long items = (long long)p->max_q_len * p->h_q * (D / 8), trip = JOIN_THREADS * JOIN_TRIPS;
-  const long long most = 2LL * P.n_shares, x = (items + trip - 1) / trip;
+  const long long items = (long long)p->max_q_len * p->h_q * (D / 8);
+  const long long most = 2LL * P.n_shares, x = (items + JOIN_THREADS - 1) / JOIN_THREADS;
   cfg.gridDim = dim3((unsigned)(x < 1 ? 1 : x > most ? most : x), (unsigned)p->n_req);
   cfg.blockDim = dim3(JOIN_THREADS);
   cfg.stream = st;
@@ -170,10 +209,22 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   P.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   P.n_groups = n_groups;
   P.own_plan = 0;
+  P.small_rows = 8 * prefix_row_tiles(p);
   P.has_tiles = L.base.max_tiles > 0;
-  set_clusters(P, p, L.base.max_tiles, sms);
-  const size_t smem = (size_t)(P.n_req + 1) * 2 * sizeof(long long) + 2 * (size_t)n_groups * sizeof(int);
-  const size_t most = (size_t)(DSA_KV8_MAX_REQ + 1) * 2 * sizeof(long long) + 2 * (size_t)DSA_KV8_MAX_REQ * sizeof(int);
+  P.cluster = 0;
+  P.n_ctas = sms;
+  P.tile_shares = L.tile_shares;
+  P.tile_steps = reinterpret_cast<long long*>(ws + L.tile_steps);
+  P.tile_cuts = reinterpret_cast<long long*>(ws + L.tile_cuts);
+  P.cut_units = reinterpret_cast<int*>(ws + L.cut_units);
+  P.unit_ctas = reinterpret_cast<int2*>(ws + L.unit_ctas);
+  P.pieces = reinterpret_cast<float*>(ws + L.pieces);
+  // the plan's lists of parts, and the groups' (find_parts) or the shared out tiles'
+  const auto plan_smem = [](size_t parts, size_t groups, size_t tiles) {
+    return (parts + 1) * 2 * sizeof(long long) + (groups > 2 * tiles ? groups : 2 * tiles) * sizeof(long long);
+  };
+  const size_t smem = plan_smem(P.n_req, n_groups, L.tile_shares ? L.base.max_tiles + 1 : 0);
+  const size_t most = plan_smem(DSA_KV8_MAX_REQ, DSA_KV8_MAX_REQ, MOST_SHARED_TILES);
   static_assert((DSA_KV8_MAX_REQ + 1) * 16 + DSA_KV8_MAX_REQ * 8 + 8 * 1024 <= 227 * 1024, "shared memory of the plan");
   const int rc1 = P.n_req <= 2 * FEW_THREADS ? launch(plan_kernel<FEW_THREADS, true>, 1, FEW_THREADS, smem, most, st, P, false)
                                              : launch(plan_kernel<PLAN_THREADS, true>, 1, PLAN_THREADS, smem, most, st, P, false);

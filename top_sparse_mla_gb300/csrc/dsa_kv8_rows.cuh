@@ -20,6 +20,7 @@ constexpr int PLAN_THREADS = 1024;
 // tokens, 16/2 heads, us, own shares and the plan's: 500 requests 19.9 and 23.5, 1024 32.7
 // and 35.4, 1500 47.4 and 50.8, 2048 (16 a thread) 63.3 and 63.6, 4096 124.7 and 111.3.
 constexpr int OWN_PLAN = 12;
+constexpr int PIECE_BLOCKS = 2;   // blocks that take a CTA of the tiles' kernel as long as a piece's beginning and end
 constexpr int FEW_THREADS = 256;  // of the plan, where rows_kernel's CTAs find their shares
 // rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
@@ -43,6 +44,28 @@ __device__ __forceinline__ Share share_at(const Params& P, int r, long long rest
   s.head = (int)(rest / steps);
   s.step = rest - s.head * steps - P.unit_steps;
   return s;
+}
+
+// Exclusive sum of a value of each thread over the CTA; `all` becomes the sum.
+template <int THREADS>
+__device__ __forceinline__ long long scan(long long v, long long* s_warp, long long& all) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long long in = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, in, o);
+    if (lane >= o) in += x;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[w] = in;
+  __syncthreads();
+  long long before = in - v;
+  all = 0;
+  for (int u = 0; u < THREADS / 32; ++u) {
+    if (u < w) before += s_warp[u];
+    all += s_warp[u];
+  }
+  return before;
 }
 
 // ------------------------------------------------------------------------------ parts
@@ -81,7 +104,7 @@ __device__ __forceinline__ void find_parts(const Params& P, int* s_shared, uint3
   __syncthreads();
   for (int g = tid; g < P.n_groups; g += blockDim.x) {
     const int shared = s_shared[g] >> P.page_shift << P.page_shift, first = s_first[g];
-    Part x{0, 0, shared - 1, 0, shared, first, SHARED, 0};
+    Part x{0, 0, shared - 1, 0, shared, first, SHARED, -1, 0, {}};
     if (first < n && shared > 0) {
       x.q0 = min(max(P.cu_q[begin(g)], 0), P.n_tokens);
       x.q_len = max(min(max(P.cu_q[begin(g + 1)], 0), P.n_tokens) - x.q0, 0);
@@ -94,7 +117,7 @@ __device__ __forceinline__ void find_parts(const Params& P, int* s_shared, uint3
     const Request a = request(P, r);
     const int g = group_of(r);
     P.parts[P.n_groups + r] =
-        Part{a.q0, a.q_len <= P.max_q_len ? a.q_len : 0, a.kv - a.q_len, g >= 0 ? s_shared[g] : 0, a.kv, r, OWN, 0};
+        Part{a.q0, a.q_len <= P.max_q_len ? a.q_len : 0, a.kv - a.q_len, g >= 0 ? s_shared[g] : 0, a.kv, r, OWN, g, 0, {}};
   }
   __syncthreads();
 }
@@ -114,6 +137,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   __shared__ long long s_step_warp[THREADS / 32], s_tile_warp[THREADS / 32];
   __shared__ int s_place[THREADS];
   __shared__ uint32_t s_bad;
+  __shared__ int s_longest;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = P.n_req;
   if (tid == 0) s_bad = 0;
@@ -226,6 +250,85 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       t.side = PREFIX ? a.side : 0;
       return t;
     };
+    if (PREFIX && P.tile_shares) {
+      // no order, and every CTA an equal share of the blocks of all heads of all tiles
+      for (int r = tid; r < n; r += THREADS) P.parts[r].tile0 = (int)s_tile[r];
+      auto steps = [&](const Tile& t) { return max((t.hi - t.lo + TILE_BLOCK - 1) / TILE_BLOCK, 1); };
+      const int some = (n_tiles + THREADS - 1) / THREADS, i0 = min(tid * some, n_tiles), i1 = min(i0 + some, n_tiles);
+      long long sum = 0;
+      for (int i = i0; i < i1; ++i) {
+        const Tile t = tile(i);
+        P.tiles[i] = t;
+        sum += steps(t);
+      }
+      long long every = 0, before = scan<THREADS>(sum, s_step_warp, every);
+      const long long total = every * P.h_kv;
+      long long* s_before = s_tile + n + 1;   // [n_tiles + 1]
+      for (int i = i0; i < i1; ++i) {
+        P.tile_steps[i] = s_before[i] = before;
+        before += steps(P.tiles[i]);
+      }
+      if (tid == 0) P.tile_steps[n_tiles] = s_before[n_tiles] = every;
+      __syncthreads();
+      // Every CTA as many blocks; or, where no CTA gets PIECE_BLOCKS more than that, a number of CTAs for each unit, so
+      // that each CTA has one piece to begin and to leave.
+      const long long each = max((total + P.n_ctas - 1) / P.n_ctas, 2LL);
+      auto length = [&](int i) { return s_before[i + 1] - s_before[i]; };
+      // of a unit of tile i: none without blocks
+      auto ctas = [&](int i) { return (int)max(min(length(i) * P.n_ctas / total, length(i) / 2), 1LL); };
+      if (tid == 0) s_longest = 0;
+      __syncthreads();
+      for (int i = tid; i < n_tiles; i += THREADS) atomicMax(&s_longest, (int)min((length(i) + ctas(i) - 1) / ctas(i), 1LL << 30));
+      __syncthreads();
+      const bool whole = (long long)n_tiles * P.h_kv <= P.n_ctas && s_longest <= each + PIECE_BLOCKS;
+      long long* s_front = s_before + n_tiles + 1;   // CTAs in front of each tile's, [n_tiles + 1]
+      if (whole) {
+        long long some_ctas = 0, used = 0;
+        for (int i = i0; i < i1; ++i) some_ctas += (long long)ctas(i) * P.h_kv;
+        long long front = scan<THREADS>(some_ctas, s_step_warp, used);
+        for (int i = i0; i < i1; ++i) {
+          s_front[i] = front;
+          front += (long long)ctas(i) * P.h_kv;
+        }
+        if (tid == 0) s_front[n_tiles] = used;
+        __syncthreads();
+      }
+      for (int b = tid; b <= P.n_ctas; b += THREADS) {
+        const long long* front = whole ? s_front : s_before;
+        const long long at = whole ? b : b * each, scale = whole ? 1 : P.h_kv;
+        long long cut = total;
+        int u = n_tiles * P.h_kv;
+        if (at < front[n_tiles] * scale) {
+          int lo = 0, hi = n_tiles;   // the tile with front[lo] * scale <= at < front[lo + 1] * scale
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (front[mid] * scale <= at) lo = mid; else hi = mid;
+          }
+          const long long rest = at - front[lo] * scale, len = length(lo);
+          const int head = (int)(whole ? rest / ctas(lo) : rest / len);
+          u = lo * P.h_kv + head;
+          cut = whole ? s_before[lo] * P.h_kv + head * len + len * (rest - (long long)head * ctas(lo)) / ctas(lo) : at;
+        }
+        P.tile_cuts[b] = cut;
+        if (b < P.n_ctas) P.cut_units[b] = u;
+      }
+      for (int u = tid; u < n_tiles * P.h_kv; u += THREADS) {
+        const int i = u / P.h_kv, head = u - i * P.h_kv;
+        if (whole) {
+          const int b = (int)s_front[i] + head * ctas(i);
+          P.unit_ctas[u] = make_int2(b, b + ctas(i) - 1);
+        } else {
+          const long long from = s_before[i] * P.h_kv + head * length(i);
+          P.unit_ctas[u] = make_int2((int)(from / each), (int)((from + length(i) - 1) / each));
+        }
+      }
+      if (tid == 0) {
+        P.header->status = s_bad;
+        P.header->n_tiles = n_tiles;
+        P.header->share = share;
+      }
+      return;
+    }
     auto length = [](const Tile& t) { return THREADS - 1 - min(max(t.hi - t.lo, 0) / 128, THREADS - 1); };
     s_place[tid] = 0;
     __syncthreads();

@@ -46,7 +46,7 @@ namespace dsa_kv8 {
 
 using namespace dsa;
 
-constexpr int BLOCK = 128;       // cached tokens of a block
+constexpr int BLOCK = TILE_BLOCK;   // cached tokens of a block
 constexpr float MOST = 15.0f;   // largest exponent of a weight by an m that is kept
 constexpr int W_DQ = 8, W_MMA = 12, W_COPY = 13, TILE_THREADS = 16 * 32;   // warps 14 and 15 only give registers
 // Registers of a thread of the softmax groups and of the others: eight warps of each, which
@@ -178,7 +178,10 @@ template <bool SPLIT, bool PREFIX>
 DSA_DEV bool unit(const Params& P, uint32_t round, int n_tiles, Unit& x) {
   // below 2^32: a unit that is not a request's last has 256 rows of q, 32 KB or more
   uint32_t u = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-  if (SPLIT) {
+  if (SPLIT && PREFIX) {
+    if (n_tiles == 0) return false;
+    u = (uint32_t)P.cut_units[blockIdx.x] + round;
+  } else if (SPLIT) {
     u = blockIdx.x / P.cluster;
     x.piece = blockIdx.x % P.cluster;
     if (round > 0) return false;
@@ -202,6 +205,19 @@ DSA_DEV bool unit(const Params& P, uint32_t round, int n_tiles, Unit& x) {
   }
   if (!SPLIT) return true;
   const int all = max(x.blocks[0], x.blocks[1]);
+  if (PREFIX) {
+    const long long before = P.tile_steps[i] * P.h_kv + (long long)x.head * all;
+    const long long from = P.tile_cuts[blockIdx.x] - before, to = P.tile_cuts[blockIdx.x + 1] - before;
+    if (to <= 0) return false;   // the unit begins behind this CTA's share
+    const int s0 = (int)max(from, 0LL), s1 = (int)min((long long)all, to);
+    const int2 by = P.unit_ctas[u];
+    x.pieces = by.y - by.x + 1;
+    x.piece = 2 * blockIdx.x + (from <= 0 ? 1 : 0);   // the buffer
+    x.t.lo += s0 * BLOCK;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x.blocks[h] = min(max(x.blocks[h] - s0, 0), s1 - s0);
+    return true;
+  }
   x.pieces = max(min(P.cluster, all / 2), 1);
   const int b0 = (int)((long long)all * x.piece / x.pieces), b1 = (int)((long long)all * (x.piece + 1) / x.pieces);
   x.t.lo += b0 * BLOCK;
@@ -609,9 +625,9 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
   Unit x;
   for (uint32_t u = 0; unit<SPLIT, PREFIX>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]), mine = h == 0 ? x.blocks[0] : x.blocks[1];
-    if (!(h == 0 ? x.rows[0] : x.rows[1]) || (SPLIT && x.piece >= x.pieces)) {
+    if (!(h == 0 ? x.rows[0] : x.rows[1]) || (SPLIT && !PREFIX && x.piece >= x.pieces)) {
       g += blocks;
-      if (!SPLIT && !wait_unit(c, u + 1)) return met;
+      if ((!SPLIT || PREFIX) && !wait_unit(c, u + 1)) return met;
       continue;
     }
     const int first = x.t.row0 + 128 * h, row = first + row_in;
@@ -764,7 +780,28 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       *reinterpret_cast<uint4*>(dst + k) = v;
     };
     auto inverse = [](float sum) { return sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum); };   // a NaN sum stays one
-    if (!SPLIT || x.pieces == 1) {
+    if (SPLIT && PREFIX && x.pieces > 1) {
+      float* piece = P.pieces + x.piece * piece_size(D);
+      const int r = row - x.t.row0;
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        if (mine == 0) break;
+        uint32_t o[32];
+        tmem_ld32(to + k, o);
+        tc_wait_ld();
+        if (live)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(piece + ((k + e) / 4 * TILE_ROWS + r) * 4) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      if (live) {
+        piece[TILE_ROWS * D + r] = fresh && l == 0.f ? NOTHING : m;
+        piece[TILE_ROWS * (D + 1) + r] = l;
+      }
+      g += blocks;
+      continue;
+    }
+    if (!SPLIT || PREFIX || x.pieces == 1) {
       const float inv = inverse(l);
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
@@ -822,7 +859,7 @@ DSA_DEV bool softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
         write(8 * k, o, inv);
       }
     }
-    if (PREFIX && live && (!SPLIT || x.piece == 0)) P.part_ml[at] = make_float2(SPLIT && x.pieces > 1 ? m : fresh ? NOTHING : m, l);
+    if (PREFIX && live) P.part_ml[at] = make_float2(fresh && l == 0.f ? NOTHING : m, l);
     if (!PREFIX && live && P.lse && (!SPLIT || x.piece == 0))
       P.lse[(long long)(x.t.q0 + qi) * P.h_q + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
     g += blocks;
@@ -877,7 +914,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
     else if (warp == W_MMA) products<D, SPLIT, PREFIX>(P, c, tmem, n_tiles);
     else if (warp == W_COPY) copies<D, SPLIT, PREFIX>(P, c, n_tiles);
   }
-  if (SPLIT) {   // every thread twice: the pieces are there; and they have been read
+  if (SPLIT && !PREFIX) {   // every thread twice: the pieces are there; and they have been read
     if (!met) cluster_meet();
     cluster_meet();
   }
@@ -906,7 +943,7 @@ static int configure(const Params& P, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
   if (cudaFuncGetAttributes(&a, tiles_kernel<D, SPLIT, PREFIX>) != cudaSuccess || a.numRegs != LAUNCH_REGS) return DSA_ERR_CUDA;
   if (cudaFuncSetAttribute(tiles_kernel<D, SPLIT, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return DSA_ERR_CUDA;
-  if (SPLIT && cudaFuncSetAttribute(tiles_kernel<D, SPLIT, PREFIX>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (SPLIT && !PREFIX && cudaFuncSetAttribute(tiles_kernel<D, SPLIT, PREFIX>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return DSA_ERR_CUDA;
   cfg = {};
   cfg.gridDim = dim3((unsigned)P.n_ctas);
@@ -919,7 +956,7 @@ static int configure(const Params& P, cudaLaunchConfig_t& cfg, cudaLaunchAttribu
   attr[1].val.clusterDim.x = (unsigned)max(P.cluster, 1);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = SPLIT ? 2 : 1;
+  cfg.numAttrs = SPLIT && !PREFIX ? 2 : 1;
   return DSA_OK;
 }
 
@@ -936,7 +973,7 @@ static int launch_one(const Params& P, cudaStream_t st) {
 // other one's loops took a tenth longer.
 template <bool PREFIX>
 static int launch_tiles_of(int d, const Params& P, cudaStream_t st) {
-  if (P.cluster) return d == 128 ? launch_one<128, true, PREFIX>(P, st) : launch_one<64, true, PREFIX>(P, st);
+  if (PREFIX ? P.tile_shares : P.cluster) return d == 128 ? launch_one<128, true, PREFIX>(P, st) : launch_one<64, true, PREFIX>(P, st);
   return d == 128 ? launch_one<128, false, PREFIX>(P, st) : launch_one<64, false, PREFIX>(P, st);
 }
 
