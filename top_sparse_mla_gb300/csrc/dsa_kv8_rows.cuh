@@ -974,6 +974,8 @@ __device__ __forceinline__ void rows_share(const Params& P, RowSmem<D, NT, NW>& 
 template <int D, int NT, int NW, bool PREFIX = false>
 __global__ void __launch_bounds__(32 * NW, NW > ROW_WARPS ? 1 : ctas_per_sm(D, NT)) rows_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
+  // PREFIX: the tiles' kernel begins with the plan, and so behind it
+  if (PREFIX) wait_for_plan();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the tiles' kernel, if there is one
   rows_share<D, NT, NW, PREFIX>(P, *reinterpret_cast<RowSmem<D, NT, NW>*>(smem_raw));
   wait_for_plan();   // what waits for this kernel needs the plan

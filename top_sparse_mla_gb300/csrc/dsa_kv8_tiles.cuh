@@ -901,8 +901,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)c.misc[0];
-  // launched as a programmatic dependent of rows_kernel, which waited for the plan
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Launched as a programmatic dependent of rows_kernel, which waited for the plan.  PREFIX: rows_kernel's CTAs allow this
+  // kernel's only behind that wait, and it needs nothing else of theirs; what comes behind this kernel does.
+  if (!PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
+  else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join
   const int n_tiles = P.header->n_tiles;
   bool met = false;
   if (warp < W_DQ) {
@@ -933,6 +935,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
     tc_fence_after();
     tmem_dealloc(tmem, Tmem<D>::COLS);
   }
+  if (PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");   // done when rows_kernel is
 }
 
 template <int D, bool SPLIT, bool PREFIX>
