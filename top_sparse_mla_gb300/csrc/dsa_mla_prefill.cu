@@ -305,8 +305,14 @@ struct Unit {
   int first[2];    // first row of each half
   bool rows[2];    // whether a half has rows
   int blocks[2];   // blocks of each half in this piece
+  bool two;        // SPLIT: the same rows in both halves, which take the piece's blocks in turn
   int s0;          // the piece's first block
   int pieces, part;   // CTAs that share the unit; this piece's partial result
+
+  // whether block i of the piece is half h's, and whether it is the first and the last of these
+  DSA_DEV bool has(int h, int i) const { return i < (h == 0 ? blocks[0] : blocks[1]) && (!two || (i & 1) == h); }
+  DSA_DEV bool begins(int i) const { return i < (two ? 2 : 1); }
+  DSA_DEV bool ends(int h, int i) const { return i + (two ? 2 : 1) >= (h == 0 ? blocks[0] : blocks[1]); }
 };
 
 // The units of a CTA, in order.  All roles walk them alike.
@@ -348,37 +354,33 @@ struct Walk {
     const int4 a = at[0], b = at[1];
     x.t.q0 = a.x; x.t.rows = a.y; x.t.row0 = a.z; x.t.kv = a.w;
     x.t.k0 = b.x; x.t.steps = b.y;
-    const int left_rows = x.t.rows - x.t.row0;
-    if (left_rows > 128) {
-      x.rows[0] = x.rows[1] = true;
-      x.first[0] = x.t.row0;
-      x.first[1] = x.t.row0 + 128;
-    } else {
-      const bool second = one++ & 1;
-      x.rows[0] = !second;
-      x.rows[1] = second;
-      x.first[0] = x.first[1] = x.t.row0;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int seen = x.t.kv - x.t.rows + min(x.first[h] + 128, x.t.rows);   // by the half's last row
-      x.blocks[h] = x.rows[h] ? (max(seen, 0) + BLOCK - 1) / BLOCK : 0;
-    }
     x.s0 = 0;
     x.pieces = 1;
     x.part = 0;
+    int s1 = x.t.steps;
     if (SPLIT) {
       const int steps = max(x.t.steps, 1);
       const long long before = (((long long)(uint32_t)b.w << 32) | (uint32_t)b.z) * P.h + (long long)x.head * steps;
-      const int s1 = (int)min((long long)steps, step + left);
+      s1 = (int)min((long long)steps, step + left);
       x.s0 = step;
       x.part = 2 * blockIdx.x + (step == 0 ? 1 : 0);
       x.pieces = (int)((before + steps - 1) / share - before / share) + 1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) x.blocks[h] = min(max(x.blocks[h] - x.s0, 0), s1 - x.s0);
       left -= s1 - step;
       step = 0;
       ++head;
+    }
+    const int left_rows = x.t.rows - x.t.row0;
+    x.two = SPLIT && left_rows <= 128 && x.pieces > 1;
+    const bool second = left_rows <= 128 && !x.two && (one++ & 1);
+    const bool both = left_rows > 128 || x.two;
+    x.rows[0] = both || !second;
+    x.rows[1] = both || second;
+    x.first[0] = x.t.row0;
+    x.first[1] = x.t.row0 + (left_rows > 128 ? 128 : 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int seen = x.t.kv - x.t.rows + min(x.first[h] + 128, x.t.rows);   // by the half's last row
+      x.blocks[h] = x.rows[h] ? min(max((max(seen, 0) + BLOCK - 1) / BLOCK - x.s0, 0), s1 - x.s0) : 0;
     }
     return true;
   }
@@ -433,7 +435,7 @@ DSA_DEV void copies(const Params& P, const Maps& M, const Ctx& c, int n_tiles) {
       if (i == 0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (ok && x.blocks[h] > 0) {
+          if (ok && x.has(h, x.two ? h : 0)) {
             ok = wait_w(c, B_QFREE + h, (nq[h] & 1) ^ 1);
             if (!ok) break;
             ++nq[h];
@@ -506,8 +508,8 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
       i = 0;
     }
     if (!more && due == 0) return;
-    const uint32_t now = more ? (i < x.blocks[0] ? 1u : 0u) | (i < x.blocks[1] ? 2u : 0u) : 0u;
-    const uint32_t ends = now & ((i + 1 == x.blocks[0] ? 1u : 0u) | (i + 1 == x.blocks[1] ? 2u : 0u));
+    const uint32_t now = more ? (x.has(0, i) ? 1u : 0u) | (x.has(1, i) ? 2u : 0u) : 0u;
+    const uint32_t ends = more ? now & ((x.ends(0, i) ? 1u : 0u) | (x.ends(1, i) ? 2u : 0u)) : 0u;
     const uint32_t due_at_first = due;
     bool v_there = false, k_there = false;
     // a half's scores follow its weights' product with the block before; a half alone goes first, so that its scores
@@ -540,7 +542,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
         if (last & bit) tc_commit(bar(c, B_OFULL + h));
       }
       if (now & bit) {   // S of block g
-        if (i == 0) {
+        if (x.begins(i)) {
           if (!wait_1(c, B_QFULL + h, (q_parity >> h) & 1)) return;
           q_parity ^= bit;
         }
@@ -565,7 +567,7 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
     if (due_at_first) tc_commit(bar(c, B_VFREE + (g - 1) % V_BUFS));
     if (!more) return;
     due = now;
-    first = i == 0;
+    first = x.begins(i);
     last = ends;
     partial = x.t.kv - (x.s0 + i) * BLOCK < BLOCK;
     kp += 3;
@@ -647,22 +649,28 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;   // the warp's 32 lanes of tensor memory
   const uint32_t ts = tmem + lanes + Tmem::S + 128 * h, to = tmem + lanes + Tmem::O + 128 * h;
   uint32_t ns = 0, no = 0;
+  bool dry = true;
   Walk<SPLIT> walk(P);
   Unit x;
   while (walk.next(P, n_tiles, x)) {
     if (!(h == 0 ? x.rows[0] : x.rows[1])) continue;
     const int blocks = h == 0 ? x.blocks[0] : x.blocks[1], first = h == 0 ? x.first[0] : x.first[1];
+    const int begin = x.two ? h : 0, stride = x.two ? 2 : 1;
     const int row = first + row_in;
     const bool live = row < x.t.rows;
     const int pos0 = x.t.kv - x.t.rows, pos = pos0 + min(row, x.t.rows - 1);
     const uint64_t mul = pair(P.scale_log2, P.scale_log2);
     float m = 0.f, l = 0.f;
     bool fresh = true;   // m is not set: every score so far was masked
-    for (int i = 0; i < blocks; ++i) {
-      const int base = (x.s0 + i) * BLOCK;
-      if (!wait_w(c, B_SFULL + h, ns & 1)) return;
-      ++ns;
-      tc_fence_after();
+    // Before its first scores a CTA goes through this once on what tensor memory holds, for its instructions: fetched when
+    // the scores are there, they take some thousand cycles.
+    for (int i = dry ? begin - stride : begin; i < blocks || dry; i += stride) {
+      const int base = dry ? 1 << 30 : (x.s0 + i) * BLOCK;   // dry: as if nothing were seen
+      if (!dry) {
+        if (!wait_w(c, B_SFULL + h, ns & 1)) return;
+        ++ns;
+        tc_fence_after();
+      }
       uint32_t x2[128];
 #pragma unroll
       for (int k = 0; k < 128; k += 32) tmem_ld32(ts + k, *reinterpret_cast<uint32_t(*)[32]>(x2 + k));
@@ -694,7 +702,7 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
         l *= f;
 #pragma unroll
         for (int e = 0; e < 128; ++e) x2[e] = __float_as_uint(__uint_as_float(x2[e]) - delta);
-        if (i > 0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+        if (i > begin && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
           // the product of the block before is done: these scores were issued after it
 #pragma unroll 1
           for (int k = 0; k < DV; k += 8) {
@@ -722,14 +730,21 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
           p[e + 1] = pack<BF16>(w2, w3);
         }
         l += (s0 + s1) + (s2 + s3);
+        if (dry) continue;
         tmem_st32(ts + 32 * part, p);
         tc_wait_st();
         tc_fence_before();
         arrive_w(c, B_PFULL + 2 * h + part);
       }
+      if (dry) {
+        m = l = 0.f;
+        fresh = true;
+        dry = false;
+      }
     }
     // ---- result
-    if (blocks > 0) {
+    const bool some = blocks > begin;
+    if (some) {
       if (!wait_w(c, B_OFULL + h, no & 1)) return;
       ++no;
       tc_fence_after();
@@ -737,33 +752,39 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
     const long long token = (long long)x.t.q0 + row;
     if (!SPLIT || x.pieces == 1) {
       uint16_t* dst = P.out + token * P.out_ld + x.head * P.out_hd;
+      const bool wide = ((uintptr_t)dst & 31) == 0;
       const float inv = inverse(l);
 #pragma unroll 1
       for (int k = 0; k < DV; k += 32) {
         uint32_t o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
-        if (blocks > 0) {
+        if (some) {
           tmem_ld32(to + k, o);
           tc_wait_ld();
         }
         if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 v;
-            v.x = pack<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-            v.y = pack<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            v.z = pack<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            v.w = pack<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            *reinterpret_cast<uint4*>(dst + k + e) = v;
+          for (int e = 0; e < 32; e += 16) {
+            uint32_t v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              v[q] = pack<BF16>(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv);
+            // a lane for a row touches 32 lines with every store: the fewer the better
+            if (wide) {
+              stg256(dst + k + e, v);
+            } else {
+              *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(dst + k + e + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
           }
         }
       }
       if (live && P.lse) P.lse[token * P.h + x.head] = lse_of(m, l);
     } else {
       float* at = P.partial + (long long)x.part * PARTIAL;
-      const int r = row - x.t.row0;
-      if (blocks > 0) {
+      const int r = row - x.t.row0 + (x.two ? 128 * h : 0);
+      if (some) {
 #pragma unroll 1
         for (int k = 0; k < DV; k += 32) {
           uint32_t o[32];
@@ -837,53 +858,67 @@ __global__ void __launch_bounds__(THREADS, 1) mla_kernel(const __grid_constant__
 }
 
 // ------------------------------------------------------------------------------ join
-// Units in several pieces, 32 rows at a time: a warp has 16 dims of them, a lane a row.  The
-// pieces are joined in their order.
-constexpr int JOIN_THREADS = 256;
+// Units in several pieces, 32 rows and 32 dims at a time: a warp has 4 of the dims, a lane a row.  The
+// pieces are joined in their order, AT_ONCE of them on their way together.
+constexpr int JOIN_THREADS = 256, AT_ONCE = 8;
 template <bool BF16>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int ROWS = TILE_ROWS / 32, PARTS = ROWS * (DV / 32);
   const int n_tiles = P.header->n_tiles, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long share = P.header->share;
-  const int items = n_tiles * P.h * (TILE_ROWS / 32);
+  const int items = n_tiles * P.h * PARTS;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int unit = item / (TILE_ROWS / 32), i = unit / P.h, head = unit - i * P.h;
+    const int unit = item / PARTS, i = unit / P.h, head = unit - i * P.h;
     const Tile t = P.tiles[i];
     const long long steps = max(t.steps, 1), before = t.before * P.h + head * steps;
     const int b0 = (int)(before / share), b1 = (int)((before + steps - 1) / share);
-    const int r = (item % (TILE_ROWS / 32)) * 32 + lane, row = t.row0 + r;
+    const int r = (item % ROWS) * 32 + lane, row = t.row0 + r, chunk = item % PARTS / ROWS * 8 + w;
     if (b0 == b1 || row >= t.rows) continue;
-    auto part = [&](int b) { return P.partial + (2LL * b + (b == b0 ? 1 : 0)) * PARTIAL; };
-    float m = NOTHING, l = 0.f;
-    for (int b = b0; b <= b1; ++b) m = fmaxf(m, part(b)[TILE_ROWS * DV + r]);
-    float o[16];
+    const int halves = t.rows - t.row0 <= 128 ? 2 : 1;   // 2: both halves had these rows
+    const int n = (b1 - b0 + 1) * halves;
+    float m = NOTHING, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < n; j0 += AT_ONCE) {
+      float pm[AT_ONCE], pl[AT_ONCE];
+      float4 po[AT_ONCE];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = 0.f;
-#pragma unroll 2
-    for (int b = b0; b <= b1; ++b) {
-      const float* at = part(b);
-      const float pm = at[TILE_ROWS * DV + r];
-      if (pm == NOTHING) continue;
-      const float f = ex2(pm - m);
-      l = fmaf(at[TILE_ROWS * (DV + 1) + r], f, l);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 v = *reinterpret_cast<const float4*>(at + ((4 * w + q) * TILE_ROWS + r) * 4);
-        o[4 * q] = fmaf(v.x, f, o[4 * q]);
-        o[4 * q + 1] = fmaf(v.y, f, o[4 * q + 1]);
-        o[4 * q + 2] = fmaf(v.z, f, o[4 * q + 2]);
-        o[4 * q + 3] = fmaf(v.w, f, o[4 * q + 3]);
+      for (int j = 0; j < AT_ONCE; ++j) {
+        pm[j] = NOTHING;
+        pl[j] = 0.f;
+        po[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + j < n) {
+          const int b = b0 + (j0 + j) / halves;
+          const int at_row = r + (j0 + j) % halves * 128;
+          const float* at = P.partial + (2LL * b + (b == b0 ? 1 : 0)) * PARTIAL;
+          pm[j] = at[TILE_ROWS * DV + at_row];
+          pl[j] = at[TILE_ROWS * (DV + 1) + at_row];
+          po[j] = *reinterpret_cast<const float4*>(at + (chunk * TILE_ROWS + at_row) * 4);
+        }
       }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) top = fmaxf(top, pm[j]);
+      const float f0 = ex2(m - top);
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= f0;
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) {
+        if (pm[j] == NOTHING) continue;   // O is not written
+        const float f = ex2(pm[j] - top);
+        l = fmaf(pl[j], f, l);
+        o[0] = fmaf(po[j].x, f, o[0]);
+        o[1] = fmaf(po[j].y, f, o[1]);
+        o[2] = fmaf(po[j].z, f, o[2]);
+        o[3] = fmaf(po[j].w, f, o[3]);
+      }
+      m = top;
     }
     const long long token = (long long)t.q0 + row;
     const float inv = inverse(l);
-    uint32_t p[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = pack<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    uint4* dst = reinterpret_cast<uint4*>(P.out + token * P.out_ld + head * P.out_hd + 16 * w);
-    dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
-    dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
-    if (w == 0 && P.lse) P.lse[token * P.h + head] = lse_of(m, l);
+    *reinterpret_cast<uint2*>(P.out + token * P.out_ld + head * P.out_hd + 4 * chunk) =
+        make_uint2(pack<BF16>(o[0] * inv, o[1] * inv), pack<BF16>(o[2] * inv, o[3] * inv));
+    if (chunk == 0 && P.lse) P.lse[token * P.h + head] = lse_of(m, l);
   }
 }
 
@@ -992,7 +1027,7 @@ static int launch(const Params& P, const Maps& M, cudaStream_t st) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, mla_kernel<BF16, SPLIT>, P, M) != cudaSuccess) return DSA_ERR_CUDA;
   if (!SPLIT) return DSA_OK;
-  cfg.gridDim = dim3((unsigned)P.n_ctas * 2);
+  cfg.gridDim = dim3((unsigned)P.n_ctas * 4);
   cfg.blockDim = dim3(JOIN_THREADS);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<BF16>, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;

@@ -177,6 +177,12 @@ DSA_DEV uint32_t ldg_nc_u8(const void* p) {
   asm volatile("ld.global.nc.u8 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
+// 32 bytes to a 32-byte aligned place
+DSA_DEV void stg256(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // L2 prefetch of the 128-byte line holding p (no ordering with other memory accesses)
 DSA_DEV void prefetch_line_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 DSA_DEV void sts128(uint32_t addr, uint4 v) {
