@@ -42,6 +42,8 @@ struct Header {
   uint32_t status;
   int n_tiles;
   long long share;   // steps of every CTA
+  int row_units;     // PREFIX: units that rows_kernel's CTAs take whole, one after the other; 0 where they have shares
+  int next_unit;     // how many were taken beside each CTA's first
 };
 
 enum { SHARED = 0, OWN = 1 };
@@ -86,6 +88,7 @@ struct Params {
   int* cut_units;
   int2* unit_ctas;
   float* pieces;
+  int* row_parts;   // parts of rows_kernel whose units are taken whole
   int n_groups, tile_shares;
   uint32_t test_block;   // block of CTA 0 at which the copies stop (DSA_KV8_FLAG_TEST_WAIT_TIMEOUT)
   float scale_log2;   // softmax_scale * log2 e

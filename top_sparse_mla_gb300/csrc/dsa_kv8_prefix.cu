@@ -24,14 +24,32 @@ namespace dsa_kv8 {
 // a part are joined in their order, and then the parts.
 constexpr int JOIN_THREADS = 256;
 
+constexpr int AT_ONCE = 4;   // pieces on their way together
+
 struct Sum {   // of a row: O and l in units of 2^m
   float m, l, o[8];
-  __device__ __forceinline__ void add(float m1, float l1, float4 a, float4 b) {
-    const float top = fmaxf(m, m1), f0 = ex2(m - top), f1 = ex2(m1 - top);
-    l = scaled(l, m - top) + scaled(l1, m1 - top);
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  template <int N>
+  __device__ __forceinline__ void add(const float (&m1)[N], const float (&l1)[N], const float4 (&v)[N][2]) {
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e], f1, o[e] * f0);
+    for (int j = 0; j < N; ++j) top = fmaxf(top, m1[j]);
+    l = scaled(l, m - top);
+    const float f0 = ex2(m - top);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (m1[j] == NOTHING && l1[j] == 0.f) continue;   // O is not written
+      const float f = ex2(m1[j] - top);
+      l += scaled(l1[j], m1[j] - top);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        o[4 * h] = fmaf(v[j][h].x, f, o[4 * h]);
+        o[4 * h + 1] = fmaf(v[j][h].y, f, o[4 * h + 1]);
+        o[4 * h + 2] = fmaf(v[j][h].z, f, o[4 * h + 2]);
+        o[4 * h + 3] = fmaf(v[j][h].w, f, o[4 * h + 3]);
+      }
+    }
     m = top;
   }
 };
@@ -41,15 +59,25 @@ __device__ __forceinline__ void add_part(const Params& P, const Part& a, int tok
   if (a.q_len * P.group > P.small_rows && P.tile_shares) {
     const int row = (token - a.q0) * P.group + head % P.group, tile = a.tile0 + row / TILE_ROWS, r = row % TILE_ROWS;
     const int2 by = P.unit_ctas[tile * P.h_kv + head / P.group];
-    const int b0 = by.x, b1 = by.y;
-    if (b0 != b1) {
-#pragma unroll 4
-      for (int b = b0; b <= b1; ++b) {
-        const float* piece = P.pieces + (2LL * b + (b == b0 ? 1 : 0)) * piece_size(D);
-        const float m = piece[TILE_ROWS * D + r];
-        if (m == NOTHING) continue;   // O is not written
-        const float4* o = reinterpret_cast<const float4*>(piece + (k / 4 * TILE_ROWS + r) * 4);
-        sum.add(m, piece[TILE_ROWS * (D + 1) + r], o[0], o[TILE_ROWS]);
+    if (by.x != by.y) {
+      for (int b0 = by.x; b0 <= by.y; b0 += AT_ONCE) {
+        float m[AT_ONCE], l[AT_ONCE];
+        float4 v[AT_ONCE][2];
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+          m[j] = NOTHING;
+          l[j] = 0.f;
+          v[j][0] = v[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (b0 + j <= by.y) {
+            const float* piece = P.pieces + (2LL * (b0 + j) + (b0 + j == by.x ? 1 : 0)) * piece_size(D);
+            m[j] = piece[TILE_ROWS * D + r];
+            l[j] = piece[TILE_ROWS * (D + 1) + r];
+            const float4* o = reinterpret_cast<const float4*>(piece + (k / 4 * TILE_ROWS + r) * 4);
+            v[j][0] = o[0];
+            v[j][1] = o[TILE_ROWS];
+          }
+        }
+        sum.add(m, l, v);
       }
       return;
     }
@@ -57,7 +85,9 @@ __device__ __forceinline__ void add_part(const Params& P, const Part& a, int tok
   const long long at = part_row(P, a.side, token, head);
   const float2 ml = P.part_ml[at];
   const float4* o = reinterpret_cast<const float4*>(P.part_o + at * D + k);
-  sum.add(ml.x, ml.y, o[0], o[1]);
+  const float m[1] = {ml.x}, l[1] = {ml.y};
+  const float4 v[1][2] = {{o[0], o[1]}};
+  sum.add(m, l, v);
 }
 
 template <int D>
@@ -100,7 +130,7 @@ static int check_prefix(const dsa_kv8_params* p, int n_groups) {
 struct PrefixLayout {
   Layout base;
   bool tile_shares;
-  size_t parts, part_o, part_ml, tile_steps, tile_cuts, cut_units, unit_ctas, pieces, bytes;
+  size_t parts, row_parts, part_o, part_ml, tile_steps, tile_cuts, cut_units, unit_ctas, pieces, bytes;
 };
 
 // Tiles and heads of an SM below which the tiles' blocks are shared out to all SMs alike, whatever their
@@ -138,6 +168,7 @@ static PrefixLayout prefix_layout(const dsa_kv8_params* p, int n_groups, int sms
   b.tiles = take((size_t)b.max_tiles * sizeof(Tile));
   b.partial = take((size_t)b.n_shares * 4 * (rows * p->d + 2 * rows) * sizeof(float));
   L.parts = take((size_t)(p->n_req + n_groups) * sizeof(Part));
+  L.row_parts = take((size_t)(p->n_req + n_groups) * sizeof(int));
   L.part_o = take(2 * queries * p->d * sizeof(float));
   L.part_ml = take(2 * queries * sizeof(float2));
   L.tile_shares = b.max_tiles > 0 && b.max_tiles < MOST_SHARED_TILES && (long long)b.max_tiles * p->h_kv < SHARE_UNITS * (long long)sms;
@@ -203,6 +234,7 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   Params P = params_of(c, p, L.base, sms, false);
   P.n_req = p->n_req + n_groups;
   P.parts = reinterpret_cast<Part*>(ws + L.parts);
+  P.row_parts = reinterpret_cast<int*>(ws + L.row_parts);
   P.cu_groups = cu_groups;
   P.prefix_lens = prefix_lens;
   P.part_o = reinterpret_cast<float*>(ws + L.part_o);

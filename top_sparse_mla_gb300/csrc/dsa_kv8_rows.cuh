@@ -20,6 +20,7 @@ constexpr int PLAN_THREADS = 1024;
 // tokens, 16/2 heads, us, own shares and the plan's: 500 requests 19.9 and 23.5, 1024 32.7
 // and 35.4, 1500 47.4 and 50.8, 2048 (16 a thread) 63.3 and 63.6, 4096 124.7 and 111.3.
 constexpr int OWN_PLAN = 12;
+constexpr int WHOLE_SHARES = 3;  // see plan_kernel
 constexpr int PIECE_BLOCKS = 2;   // blocks that take a CTA of the tiles' kernel as long as a piece's beginning and end
 constexpr int FEW_THREADS = 256;  // of the plan, where rows_kernel's CTAs find their shares
 // rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
@@ -137,10 +138,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   __shared__ long long s_step_warp[THREADS / 32], s_tile_warp[THREADS / 32];
   __shared__ int s_place[THREADS];
   __shared__ uint32_t s_bad;
-  __shared__ int s_longest;
+  __shared__ int s_longest, s_longest_row;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, n = P.n_req;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_longest_row = 0;
   for (int b = tid; b < 3 * P.n_shares; b += THREADS) P.arrived[b] = 0;
   __syncthreads();
   if (PREFIX) find_parts(P, reinterpret_cast<int*>(s_tile + P.n_req + 1), &s_bad);
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     if (!PREFIX && a.q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
     else if (rows > P.small_rows) tiles = (rows + TILE_ROWS - 1) / TILE_ROWS;
     s_step[r] = unit_steps<PREFIX>(P, a);
+    if (PREFIX) atomicMax(&s_longest_row, (int)s_step[r]);
     s_tile[r] = tiles;
   }
   __syncthreads();
@@ -210,8 +212,19 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
 
   const long long total = all * P.h_kv;
   const long long share = share_of(P, total);
+  // PREFIX: units as a whole, where the longest is not much longer than a share: a CTA with a part of two units
+  // begins, leaves and joins twice
+  int row_units = 0;
+  if (PREFIX && s_longest_row <= WHOLE_SHARES * share) {
+    long long count = 0;
+    for (int r = r0; r < r1; ++r) count += s_step[r + 1] > s_step[r];
+    long long rows = 0, at = scan<THREADS>(count, s_step_warp, rows);
+    for (int r = r0; r < r1; ++r)
+      if (s_step[r + 1] > s_step[r]) P.row_parts[at++] = r;
+    row_units = (int)rows * P.h_kv;
+  }
   // few requests: the CTAs find them for themselves
-  for (int b = tid; b < (P.own_plan ? 0 : P.n_shares); b += THREADS) {
+  for (int b = tid; b < (P.own_plan || row_units > 0 ? 0 : P.n_shares); b += THREADS) {
     Share s{-1, 0, 0};
     const long long f = b * share;
     if (f < total) {
@@ -326,6 +339,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
         P.header->status = s_bad;
         P.header->n_tiles = n_tiles;
         P.header->share = share;
+        P.header->row_units = row_units;
+        P.header->next_unit = 0;
       }
       return;
     }
@@ -356,6 +371,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     P.header->status = s_bad;
     P.header->n_tiles = n_tiles;
     P.header->share = share;
+    P.header->row_units = row_units;
+    P.header->next_unit = 0;
   }
 }
 
@@ -933,6 +950,19 @@ __device__ __forceinline__ void rows_share(const Params& P, RowSmem<D, NT, NW>& 
     share = S.share_steps;
   } else {
     wait_for_plan();
+    if (PREFIX && P.header->row_units > 0) {
+      const int units = P.header->row_units;
+      for (int u = b; u < units;) {
+        if (threadIdx.x == 0) S.last = P.n_shares + atomicAdd(&P.header->next_unit, 1);
+        const int i = u / P.h_kv;
+        const Request a = request<PREFIX>(P, P.row_parts[i]);
+        const Span sp = span<PREFIX>(P, a, 0, a.q_len - 1);
+        rows_unit<D, NT, NW, PREFIX>(P, S, a.req, a, u - i * P.h_kv, 0, sp, 0, sp.steps, 1, b, 0);
+        u = S.last;
+        __syncthreads();
+      }
+      return;
+    }
     at = P.shares[b];
     share = P.header->share;
   }
