@@ -14,7 +14,7 @@
  *   cu_groups    int32 [n_groups + 1], ascending, within [0, n_req] (values outside are taken
  *                as the nearest bound)
  *   prefix_lens  int32 [n_groups] (negative: 0)
- *   n_groups >= 0 (0: neither array is read); n_req + n_groups <= DSA_KV8_MAX_REQ
+ *   n_groups     0 (neither array is read) to DSA_KV8_MAX_GROUPS; n_req + n_groups <= DSA_KV8_MAX_REQ
  *   window has to be 0
  * All other arguments, the status word of the workspace, what is left unwritten, and the rules
  * for streams and graphs are those of dsa_kv8_attn_fwd.  Beside its error, O and the sums of
@@ -34,6 +34,8 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+#define DSA_KV8_MAX_GROUPS 4096
 
 /* Bytes of device workspace for `p` and n_groups on a GPU with `num_sms` SMs (num_sms <= 0: the
  * current device); 0 for invalid parameters. */

@@ -124,7 +124,7 @@ static int check_prefix(const dsa_kv8_params* p, int n_groups) {
   const int rc = check(p);
   if (rc != DSA_OK) return rc;
   if (n_groups < 0) return DSA_ERR_INVALID_ARG;
-  return p->window > 0 || n_groups > DSA_KV8_MAX_REQ - p->n_req ? DSA_ERR_UNSUPPORTED_SHAPE : DSA_OK;
+  return p->window > 0 || n_groups > DSA_KV8_MAX_GROUPS || n_groups > DSA_KV8_MAX_REQ - p->n_req ? DSA_ERR_UNSUPPORTED_SHAPE : DSA_OK;
 }
 
 struct PrefixLayout {
@@ -253,11 +253,12 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   P.pieces = reinterpret_cast<float*>(ws + L.pieces);
   // the plan's lists of parts, and the groups' (find_parts) or the shared out tiles'
   const auto plan_smem = [](size_t parts, size_t groups, size_t tiles) {
-    return (parts + 1) * 2 * sizeof(long long) + (groups > 2 * tiles ? groups : 2 * tiles) * sizeof(long long);
+    const size_t g = (3 * groups + 1) * sizeof(int), t = tiles * (2 * sizeof(long long) + sizeof(int));
+    return (parts + 1) * 2 * sizeof(long long) + (g > t ? g : t);
   };
   const size_t smem = plan_smem(P.n_req, n_groups, L.tile_shares ? L.base.max_tiles + 1 : 0);
-  const size_t most = plan_smem(DSA_KV8_MAX_REQ, DSA_KV8_MAX_REQ, MOST_SHARED_TILES);
-  static_assert((DSA_KV8_MAX_REQ + 1) * 16 + DSA_KV8_MAX_REQ * 8 + 8 * 1024 <= 227 * 1024, "shared memory of the plan");
+  const size_t most = plan_smem(DSA_KV8_MAX_REQ, DSA_KV8_MAX_GROUPS, MOST_SHARED_TILES + 1);
+  static_assert((DSA_KV8_MAX_REQ + 1) * 16 + (3 * DSA_KV8_MAX_GROUPS + 1) * 4 + 8 * 1024 <= 227 * 1024, "shared memory of the plan");
   const int rc1 = P.n_req <= 2 * FEW_THREADS ? launch(plan_kernel<FEW_THREADS, true>, 1, FEW_THREADS, smem, most, st, P, false)
                                              : launch(plan_kernel<PLAN_THREADS, true>, 1, PLAN_THREADS, smem, most, st, P, false);
   if (rc1 != DSA_OK) return rc1;

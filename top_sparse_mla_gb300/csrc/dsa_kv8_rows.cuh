@@ -6,6 +6,7 @@
 #pragma once
 
 #include <float.h>
+#include <limits.h>
 
 #include "dsa_kv8.cuh"
 
@@ -70,56 +71,96 @@ __device__ __forceinline__ long long scan(long long v, long long* s_warp, long l
 }
 
 // ------------------------------------------------------------------------------ parts
+// steps and tiles of a request or a part, for one of the two kernels
+struct Load {
+  int steps, tiles;
+};
+template <bool PREFIX>
+__device__ __forceinline__ Load load_of(const Params& P, const Request& a) {
+  const int rows = a.rows(P);
+  const bool skipped = !PREFIX && a.q_len > P.max_q_len;
+  return Load{unit_steps<PREFIX>(P, a), !skipped && rows > P.small_rows ? (rows + TILE_ROWS - 1) / TILE_ROWS : 0};
+}
+
 // The tokens that a group shares are the pages that prefix_lens names as far as every query of its requests
-// sees them all; what a request sees behind them is its own.  s_shared: [2 * n_groups].
-__device__ __forceinline__ void find_parts(const Params& P, int* s_shared, uint32_t* s_bad) {
-  int* s_first = s_shared + P.n_groups;   // a group's first request with queries
-  const int tid = threadIdx.x, n = P.n_req - P.n_groups;
-  auto begin = [&](int g) { return min(max(P.cu_groups[g], 0), n); };
-  // the group with begin(g) <= r < begin(g + 1), or -1
+// sees them all; what a request sees behind them is its own.  s_groups: [3 * n_groups + 1].  The parts' steps
+// and tiles go to s_step and s_tile.
+template <int THREADS>
+__device__ __forceinline__ void find_parts(const Params& P, int* s_groups, long long* s_step, long long* s_tile, uint32_t* s_bad,
+                                           int* s_longest) {
+  int* s_shared = s_groups;                 // shared tokens of a group
+  int* s_first = s_groups + P.n_groups;     // its first request with queries
+  int* s_begin = s_first + P.n_groups;      // its first request
+  const int tid = threadIdx.x, lane = tid & 31, n = P.n_req - P.n_groups;
+  // the group with s_begin[g] <= r < s_begin[g + 1], or -1
   auto group_of = [&](int r) {
     int lo = 0, hi = P.n_groups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (begin(mid) <= r) lo = mid; else hi = mid;
+      if (s_begin[mid] <= r) lo = mid; else hi = mid;
     }
-    return P.n_groups > 0 && begin(lo) <= r && r < begin(lo + 1) ? lo : -1;
+    return P.n_groups > 0 && s_begin[lo] <= r && r < s_begin[lo + 1] ? lo : -1;
   };
-  for (int g = tid; g < P.n_groups; g += blockDim.x) {
-    s_shared[g] = max(P.prefix_lens[g], 0);
-    s_first[g] = n;
+  auto add = [&](int i, const Part& x, int& longest) {
+    P.parts[i] = x;
+    const Load load = load_of<true>(P, Request{x.q0, x.q_len, x.pos0 + x.q_len, x.lo, x.hi, x.req, x.side});
+    s_step[i] = load.steps;
+    s_tile[i] = load.tiles;
+    longest = max(longest, load.steps);
+  };
+  // all that is in global memory on its way together, for the first requests and groups
+  Request a = request(P, min(tid, n - 1));
+  for (int g = tid; g <= P.n_groups; g += THREADS) {
+    const int begin = P.n_groups > 0 ? P.cu_groups[g] : 0, prefix = g < P.n_groups ? P.prefix_lens[g] : 0;
+    if (g < P.n_groups) {
+      s_shared[g] = max(prefix, 0);
+      s_first[g] = n;
+    }
+    s_begin[g] = min(max(begin, 0), n);
   }
   __syncthreads();
-  for (int r = tid; r < n; r += blockDim.x) {
-    const Request a = request(P, r);
-    if (a.q_len > P.max_q_len) {
+  for (int r = tid; r - lane < n; r += THREADS) {   // whole warps
+    if (r >= THREADS) a = request(P, min(r, n - 1));
+    int g = -1, most = INT_MAX, first = INT_MAX;
+    if (r < n && a.q_len > P.max_q_len) {
       atomicOr(s_bad, DSA_STATUS_QUERY_TOO_LONG);
-    } else if (a.q_len > 0) {
-      const int g = group_of(r);
-      if (g >= 0) {
-        atomicMin(&s_shared[g], max(a.kv - a.q_len + 1, 0));
-        atomicMin(&s_first[g], r);
-      }
+    } else if (r < n && a.q_len > 0) {
+      g = group_of(r);
+      most = max(a.kv - a.q_len + 1, 0);
+      first = r;
+    }
+    const int one = __reduce_max_sync(0xFFFFFFFFu, g);
+    if (__all_sync(0xFFFFFFFFu, g == one || first == INT_MAX)) {   // one group: one lane for all
+      most = __reduce_min_sync(0xFFFFFFFFu, most);
+      first = __reduce_min_sync(0xFFFFFFFFu, first);
+      g = lane == 0 ? one : -1;
+    }
+    if (g >= 0) {
+      atomicMin(&s_shared[g], most);
+      atomicMin(&s_first[g], first);
     }
   }
   __syncthreads();
-  for (int g = tid; g < P.n_groups; g += blockDim.x) {
+  int longest = 0;
+  for (int g = tid; g < P.n_groups; g += THREADS) {
     const int shared = s_shared[g] >> P.page_shift << P.page_shift, first = s_first[g];
     Part x{0, 0, shared - 1, 0, shared, first, SHARED, -1, 0, {}};
     if (first < n && shared > 0) {
-      x.q0 = min(max(P.cu_q[begin(g)], 0), P.n_tokens);
-      x.q_len = max(min(max(P.cu_q[begin(g + 1)], 0), P.n_tokens) - x.q0, 0);
+      x.q0 = min(max(P.cu_q[s_begin[g]], 0), P.n_tokens);
+      x.q_len = max(min(max(P.cu_q[s_begin[g + 1]], 0), P.n_tokens) - x.q0, 0);
     }
-    P.parts[g] = x;
+    add(g, x, longest);
     s_shared[g] = first < n ? shared : 0;
   }
   __syncthreads();
-  for (int r = tid; r < n; r += blockDim.x) {
-    const Request a = request(P, r);
+  for (int r = tid; r < n; r += THREADS) {
+    if (THREADS < n) a = request(P, r);
     const int g = group_of(r);
-    P.parts[P.n_groups + r] =
-        Part{a.q0, a.q_len <= P.max_q_len ? a.q_len : 0, a.kv - a.q_len, g >= 0 ? s_shared[g] : 0, a.kv, r, OWN, g, 0, {}};
+    add(P.n_groups + r,
+        Part{a.q0, a.q_len <= P.max_q_len ? a.q_len : 0, a.kv - a.q_len, g >= 0 ? s_shared[g] : 0, a.kv, r, OWN, g, 0, {}}, longest);
   }
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  if (lane == 0) atomicMax(s_longest, longest);
   __syncthreads();
 }
 
@@ -144,7 +185,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   if (tid == 0) s_bad = s_longest_row = 0;
   for (int b = tid; b < 3 * P.n_shares; b += THREADS) P.arrived[b] = 0;
   __syncthreads();
-  if (PREFIX) find_parts(P, reinterpret_cast<int*>(s_tile + P.n_req + 1), &s_bad);
+  if (PREFIX) find_parts<THREADS>(P, reinterpret_cast<int*>(s_tile + P.n_req + 1), s_step, s_tile, &s_bad, &s_longest_row);
   if (P.own_plan && !P.has_tiles) {   // no shares and no tiles to find
     for (int r = tid; r < n; r += THREADS)
       if (request(P, r).q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
@@ -155,15 +196,12 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     }
     return;
   }
-  for (int r = tid; r < n; r += THREADS) {
-    const Request a = request<PREFIX>(P, r);
-    const int rows = a.rows(P);
-    int tiles = 0;
-    if (!PREFIX && a.q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
-    else if (rows > P.small_rows) tiles = (rows + TILE_ROWS - 1) / TILE_ROWS;
-    s_step[r] = unit_steps<PREFIX>(P, a);
-    if (PREFIX) atomicMax(&s_longest_row, (int)s_step[r]);
-    s_tile[r] = tiles;
+  for (int r = tid; r < (PREFIX ? 0 : n); r += THREADS) {
+    const Request a = request(P, r);
+    const Load load = load_of<false>(P, a);
+    if (a.q_len > P.max_q_len) atomicOr(&s_bad, DSA_STATUS_QUERY_TOO_LONG);
+    s_step[r] = load.steps;
+    s_tile[r] = load.tiles;
   }
   __syncthreads();
   const int per = ((n + THREADS - 1) / THREADS) | 1;   // odd: no bank conflicts
@@ -216,12 +254,22 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   // begins, leaves and joins twice
   int row_units = 0;
   if (PREFIX && s_longest_row <= WHOLE_SHARES * share) {
-    long long count = 0;
-    for (int r = r0; r < r1; ++r) count += s_step[r + 1] > s_step[r];
-    long long rows = 0, at = scan<THREADS>(count, s_step_warp, rows);
+    // about the longest first, in four classes of length, whose counts share a word (at most 8192 parts)
+    auto place = [&](int r) { return 16 * (3 - min((int)((s_step[r + 1] - s_step[r]) * 4 / (s_longest_row + 1)), 3)); };
+    long long count = 0, every = 0;
     for (int r = r0; r < r1; ++r)
-      if (s_step[r + 1] > s_step[r]) P.row_parts[at++] = r;
-    row_units = (int)rows * P.h_kv;
+      if (s_step[r + 1] > s_step[r]) count += 1LL << place(r);
+    long long at = scan<THREADS>(count, s_step_warp, every);
+    auto of = [](long long packed, int shift) { return (int)((unsigned long long)packed >> shift & 0xFFFF); };
+    const int begin[4] = {0, of(every, 0), of(every, 0) + of(every, 16), of(every, 0) + of(every, 16) + of(every, 32)};
+    const int rows = begin[3] + of(every, 48);
+    for (int r = r0; r < r1; ++r)
+      if (s_step[r + 1] > s_step[r]) {
+        const int k = place(r);
+        P.row_parts[(k == 0 ? 0 : k == 16 ? begin[1] : k == 32 ? begin[2] : begin[3]) + of(at, k)] = r;
+        at += 1LL << k;
+      }
+    row_units = rows * P.h_kv;
   }
   // few requests: the CTAs find them for themselves
   for (int b = tid; b < (P.own_plan || row_units > 0 ? 0 : P.n_shares); b += THREADS) {
@@ -266,46 +314,44 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     if (PREFIX && P.tile_shares) {
       // no order, and every CTA an equal share of the blocks of all heads of all tiles
       for (int r = tid; r < n; r += THREADS) P.parts[r].tile0 = (int)s_tile[r];
-      auto steps = [&](const Tile& t) { return max((t.hi - t.lo + TILE_BLOCK - 1) / TILE_BLOCK, 1); };
+      long long* s_before = s_tile + n + 1;          // blocks of a head in front of each tile, [n_tiles + 1]
+      long long* s_front = s_before + n_tiles + 1;   // CTAs in front of each tile's, [n_tiles + 1]
+      int* s_ctas = reinterpret_cast<int*>(s_front + n_tiles + 1);   // of a unit of each tile, [n_tiles]
       const int some = (n_tiles + THREADS - 1) / THREADS, i0 = min(tid * some, n_tiles), i1 = min(i0 + some, n_tiles);
-      long long sum = 0;
+      long long sum = 0, every = 0;
       for (int i = i0; i < i1; ++i) {
         const Tile t = tile(i);
         P.tiles[i] = t;
-        sum += steps(t);
+        const int len = max((t.hi - t.lo + TILE_BLOCK - 1) / TILE_BLOCK, 1);
+        s_front[i] = len;
+        sum += len;
       }
-      long long every = 0, before = scan<THREADS>(sum, s_step_warp, every);
+      long long before = scan<THREADS>(sum, s_step_warp, every);
       const long long total = every * P.h_kv;
-      long long* s_before = s_tile + n + 1;   // [n_tiles + 1]
-      for (int i = i0; i < i1; ++i) {
-        P.tile_steps[i] = s_before[i] = before;
-        before += steps(P.tiles[i]);
-      }
-      if (tid == 0) P.tile_steps[n_tiles] = s_before[n_tiles] = every;
-      __syncthreads();
       // Every CTA as many blocks; or, where no CTA gets PIECE_BLOCKS more than that, a number of CTAs for each unit, so
       // that each CTA has one piece to begin and to leave.
       const long long each = max((total + P.n_ctas - 1) / P.n_ctas, 2LL);
-      auto length = [&](int i) { return s_before[i + 1] - s_before[i]; };
-      // of a unit of tile i: none without blocks
-      auto ctas = [&](int i) { return (int)max(min(length(i) * P.n_ctas / total, length(i) / 2), 1LL); };
       if (tid == 0) s_longest = 0;
       __syncthreads();
-      for (int i = tid; i < n_tiles; i += THREADS) atomicMax(&s_longest, (int)min((length(i) + ctas(i) - 1) / ctas(i), 1LL << 30));
+      long long some_ctas = 0, used = 0;
+      for (int i = i0; i < i1; ++i) {
+        const int len = (int)s_front[i], k = max((int)min((long long)len * P.n_ctas / total, (long long)(len / 2)), 1);
+        P.tile_steps[i] = s_before[i] = before;
+        before += len;
+        s_ctas[i] = k;
+        some_ctas += (long long)k * P.h_kv;
+        atomicMax(&s_longest, (len + k - 1) / k);
+      }
+      if (tid == 0) P.tile_steps[n_tiles] = s_before[n_tiles] = every;
+      long long front = scan<THREADS>(some_ctas, s_step_warp, used);
+      for (int i = i0; i < i1; ++i) {
+        s_front[i] = front;
+        front += (long long)s_ctas[i] * P.h_kv;
+      }
+      if (tid == 0) s_front[n_tiles] = used;
       __syncthreads();
       const bool whole = (long long)n_tiles * P.h_kv <= P.n_ctas && s_longest <= each + PIECE_BLOCKS;
-      long long* s_front = s_before + n_tiles + 1;   // CTAs in front of each tile's, [n_tiles + 1]
-      if (whole) {
-        long long some_ctas = 0, used = 0;
-        for (int i = i0; i < i1; ++i) some_ctas += (long long)ctas(i) * P.h_kv;
-        long long front = scan<THREADS>(some_ctas, s_step_warp, used);
-        for (int i = i0; i < i1; ++i) {
-          s_front[i] = front;
-          front += (long long)ctas(i) * P.h_kv;
-        }
-        if (tid == 0) s_front[n_tiles] = used;
-        __syncthreads();
-      }
+      auto length = [&](int i) { return s_before[i + 1] - s_before[i]; };
       for (int b = tid; b <= P.n_ctas; b += THREADS) {
         const long long* front = whole ? s_front : s_before;
         const long long at = whole ? b : b * each, scale = whole ? 1 : P.h_kv;
@@ -318,9 +364,9 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
             if (front[mid] * scale <= at) lo = mid; else hi = mid;
           }
           const long long rest = at - front[lo] * scale, len = length(lo);
-          const int head = (int)(whole ? rest / ctas(lo) : rest / len);
+          const int head = (int)(whole ? rest / s_ctas[lo] : rest / len);
           u = lo * P.h_kv + head;
-          cut = whole ? s_before[lo] * P.h_kv + head * len + len * (rest - (long long)head * ctas(lo)) / ctas(lo) : at;
+          cut = whole ? s_before[lo] * P.h_kv + head * len + len * (rest - (long long)head * s_ctas[lo]) / s_ctas[lo] : at;
         }
         P.tile_cuts[b] = cut;
         if (b < P.n_ctas) P.cut_units[b] = u;
@@ -328,8 +374,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       for (int u = tid; u < n_tiles * P.h_kv; u += THREADS) {
         const int i = u / P.h_kv, head = u - i * P.h_kv;
         if (whole) {
-          const int b = (int)s_front[i] + head * ctas(i);
-          P.unit_ctas[u] = make_int2(b, b + ctas(i) - 1);
+          const int b = (int)s_front[i] + head * s_ctas[i];
+          P.unit_ctas[u] = make_int2(b, b + s_ctas[i] - 1);
         } else {
           const long long from = s_before[i] * P.h_kv + head * length(i);
           P.unit_ctas[u] = make_int2((int)(from / each), (int)((from + length(i) - 1) / each));

@@ -649,7 +649,6 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
   const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;   // the warp's 32 lanes of tensor memory
   const uint32_t ts = tmem + lanes + Tmem::S + 128 * h, to = tmem + lanes + Tmem::O + 128 * h;
   uint32_t ns = 0, no = 0;
-  bool dry = true;
   Walk<SPLIT> walk(P);
   Unit x;
   while (walk.next(P, n_tiles, x)) {
@@ -662,15 +661,11 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
     const uint64_t mul = pair(P.scale_log2, P.scale_log2);
     float m = 0.f, l = 0.f;
     bool fresh = true;   // m is not set: every score so far was masked
-    // Before its first scores a CTA goes through this once on what tensor memory holds, for its instructions: fetched when
-    // the scores are there, they take some thousand cycles.
-    for (int i = dry ? begin - stride : begin; i < blocks || dry; i += stride) {
-      const int base = dry ? 1 << 30 : (x.s0 + i) * BLOCK;   // dry: as if nothing were seen
-      if (!dry) {
-        if (!wait_w(c, B_SFULL + h, ns & 1)) return;
-        ++ns;
-        tc_fence_after();
-      }
+    for (int i = begin; i < blocks; i += stride) {
+      const int base = (x.s0 + i) * BLOCK;
+      if (!wait_w(c, B_SFULL + h, ns & 1)) return;
+      ++ns;
+      tc_fence_after();
       uint32_t x2[128];
 #pragma unroll
       for (int k = 0; k < 128; k += 32) tmem_ld32(ts + k, *reinterpret_cast<uint32_t(*)[32]>(x2 + k));
@@ -730,16 +725,10 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
           p[e + 1] = pack<BF16>(w2, w3);
         }
         l += (s0 + s1) + (s2 + s3);
-        if (dry) continue;
         tmem_st32(ts + 32 * part, p);
         tc_wait_st();
         tc_fence_before();
         arrive_w(c, B_PFULL + 2 * h + part);
-      }
-      if (dry) {
-        m = l = 0.f;
-        fresh = true;
-        dry = false;
       }
     }
     // ---- result

@@ -51,6 +51,7 @@ DSA_KV8_FP16 = 1
 DSA_KV8_MAX_HEADS = 1024
 DSA_KV8_MAX_GROUP = 128
 DSA_KV8_MAX_REQ = 8192
+DSA_KV8_MAX_GROUPS = 4096
 DSA_KV8_FLAG_TEST_WAIT_TIMEOUT = 2
 DSA_STATUS_QUERY_TOO_LONG = 64
 DSA_QK_BF16 = 0
