@@ -171,7 +171,9 @@ static PrefixLayout prefix_layout(const dsa_kv8_params* p, int n_groups, int sms
   L.row_parts = take((size_t)(p->n_req + n_groups) * sizeof(int));
   L.part_o = take(2 * queries * p->d * sizeof(float));
   L.part_ml = take(2 * queries * sizeof(float2));
-  L.tile_shares = b.max_tiles > 0 && b.max_tiles < MOST_SHARED_TILES && (long long)b.max_tiles * p->h_kv < SHARE_UNITS * (long long)sms;
+  const long long blocks = ((long long)p->table_cols * p->page_size + TILE_BLOCK - 1) / TILE_BLOCK + 1;   // of a tile at most
+  L.tile_shares = b.max_tiles > 0 && b.max_tiles < MOST_SHARED_TILES && (long long)b.max_tiles * p->h_kv < SHARE_UNITS * (long long)sms &&
+                  sms < 256 && blocks <= (1 << 24) && blocks * b.max_tiles * p->h_kv < (1 << 30);   // the plan's 32 bits
   L.tile_steps = take(L.tile_shares ? (b.max_tiles + 1) * sizeof(long long) : 0);
   L.tile_cuts = take(L.tile_shares ? (sms + 1) * sizeof(long long) : 0);
   L.cut_units = take(L.tile_shares ? sms * sizeof(int) : 0);
@@ -253,7 +255,7 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   P.pieces = reinterpret_cast<float*>(ws + L.pieces);
   // the plan's lists of parts, and the groups' (find_parts) or the shared out tiles'
   const auto plan_smem = [](size_t parts, size_t groups, size_t tiles) {
-    const size_t g = (3 * groups + 1) * sizeof(int), t = tiles * (2 * sizeof(long long) + sizeof(int));
+    const size_t g = (3 * groups + 1) * sizeof(int), t = 3 * tiles * sizeof(int);
     return (parts + 1) * 2 * sizeof(long long) + (g > t ? g : t);
   };
   const size_t smem = plan_smem(P.n_req, n_groups, L.tile_shares ? L.base.max_tiles + 1 : 0);

@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   int row_units = 0;
   if (PREFIX && s_longest_row <= WHOLE_SHARES * share) {
     // about the longest first, in four classes of length, whose counts share a word (at most 8192 parts)
-    auto place = [&](int r) { return 16 * (3 - min((int)((s_step[r + 1] - s_step[r]) * 4 / (s_longest_row + 1)), 3)); };
+    auto place = [&](int r) {
+      const long long four = 4 * (s_step[r + 1] - s_step[r]), most = s_longest_row;
+      return four > 3 * most ? 0 : four > 2 * most ? 16 : four > most ? 32 : 48;
+    };
     long long count = 0, every = 0;
     for (int r = r0; r < r1; ++r)
       if (s_step[r + 1] > s_step[r]) count += 1LL << place(r);
@@ -314,72 +317,70 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     if (PREFIX && P.tile_shares) {
       // no order, and every CTA an equal share of the blocks of all heads of all tiles
       for (int r = tid; r < n; r += THREADS) P.parts[r].tile0 = (int)s_tile[r];
-      long long* s_before = s_tile + n + 1;          // blocks of a head in front of each tile, [n_tiles + 1]
-      long long* s_front = s_before + n_tiles + 1;   // CTAs in front of each tile's, [n_tiles + 1]
-      int* s_ctas = reinterpret_cast<int*>(s_front + n_tiles + 1);   // of a unit of each tile, [n_tiles]
+      // (all blocks of all heads are below 2^30: the 64-bit divisions of this kernel's beginning take 600 cycles each)
+      unsigned* s_before = reinterpret_cast<unsigned*>(s_tile + n + 1);   // blocks of a head in front of each tile, [n_tiles + 1]
+      unsigned* s_front = s_before + n_tiles + 1;                         // CTAs in front of each tile's, [n_tiles + 1]
+      unsigned* s_ctas = s_front + n_tiles + 1;                           // of a unit of each tile, [n_tiles]
+      const unsigned h_kv = P.h_kv, n_ctas = P.n_ctas;
       const int some = (n_tiles + THREADS - 1) / THREADS, i0 = min(tid * some, n_tiles), i1 = min(i0 + some, n_tiles);
-      long long sum = 0, every = 0;
+      unsigned sum = 0;
       for (int i = i0; i < i1; ++i) {
         const Tile t = tile(i);
         P.tiles[i] = t;
-        const int len = max((t.hi - t.lo + TILE_BLOCK - 1) / TILE_BLOCK, 1);
-        s_front[i] = len;
-        sum += len;
+        s_front[i] = max((t.hi - t.lo + TILE_BLOCK - 1) / TILE_BLOCK, 1);
+        sum += s_front[i];
       }
-      long long before = scan<THREADS>(sum, s_step_warp, every);
-      const long long total = every * P.h_kv;
+      long long all_blocks = 0, all_ctas = 0;
+      unsigned before = (unsigned)scan<THREADS>(sum, s_step_warp, all_blocks);
+      const unsigned every = (unsigned)all_blocks, total = every * h_kv;
       // Every CTA as many blocks; or, where no CTA gets PIECE_BLOCKS more than that, a number of CTAs for each unit, so
       // that each CTA has one piece to begin and to leave.
-      const long long each = max((total + P.n_ctas - 1) / P.n_ctas, 2LL);
+      const unsigned each = max((total + n_ctas - 1) / n_ctas, 2u);
       if (tid == 0) s_longest = 0;
       __syncthreads();
-      long long some_ctas = 0, used = 0;
+      unsigned some_ctas = 0;
       for (int i = i0; i < i1; ++i) {
-        const int len = (int)s_front[i], k = max((int)min((long long)len * P.n_ctas / total, (long long)(len / 2)), 1);
-        P.tile_steps[i] = s_before[i] = before;
+        // below 2^24 blocks, and fewer than 256 SMs
+        const unsigned len = s_front[i], k = max(min(len * n_ctas / total, len / 2), 1u);
+        s_before[i] = before;
+        P.tile_steps[i] = before;
         before += len;
         s_ctas[i] = k;
-        some_ctas += (long long)k * P.h_kv;
-        atomicMax(&s_longest, (len + k - 1) / k);
+        some_ctas += k * h_kv;
+        atomicMax(&s_longest, (int)((len + k - 1) / k));
       }
       if (tid == 0) P.tile_steps[n_tiles] = s_before[n_tiles] = every;
-      long long front = scan<THREADS>(some_ctas, s_step_warp, used);
+      unsigned front = (unsigned)scan<THREADS>(some_ctas, s_step_warp, all_ctas);
       for (int i = i0; i < i1; ++i) {
         s_front[i] = front;
-        front += (long long)s_ctas[i] * P.h_kv;
+        front += s_ctas[i] * h_kv;
       }
-      if (tid == 0) s_front[n_tiles] = used;
+      if (tid == 0) s_front[n_tiles] = (unsigned)all_ctas;
       __syncthreads();
-      const bool whole = (long long)n_tiles * P.h_kv <= P.n_ctas && s_longest <= each + PIECE_BLOCKS;
-      auto length = [&](int i) { return s_before[i + 1] - s_before[i]; };
-      for (int b = tid; b <= P.n_ctas; b += THREADS) {
-        const long long* front = whole ? s_front : s_before;
-        const long long at = whole ? b : b * each, scale = whole ? 1 : P.h_kv;
-        long long cut = total;
-        int u = n_tiles * P.h_kv;
-        if (at < front[n_tiles] * scale) {
-          int lo = 0, hi = n_tiles;   // the tile with front[lo] * scale <= at < front[lo + 1] * scale
+      const bool whole = n_tiles * h_kv <= n_ctas && s_longest <= each + PIECE_BLOCKS;
+      const unsigned* starts = whole ? s_front : s_before;
+      const unsigned scale = whole ? 1 : h_kv;
+      for (unsigned b = tid; b <= n_ctas; b += THREADS) {
+        const unsigned at = whole ? b : b * each;
+        unsigned cut = total, u = n_tiles * h_kv;
+        if (at < starts[n_tiles] * scale) {
+          int lo = 0, hi = n_tiles;   // the tile with starts[lo] * scale <= at < starts[lo + 1] * scale
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (front[mid] * scale <= at) lo = mid; else hi = mid;
+            if (starts[mid] * scale <= at) lo = mid; else hi = mid;
           }
-          const long long rest = at - front[lo] * scale, len = length(lo);
-          const int head = (int)(whole ? rest / s_ctas[lo] : rest / len);
-          u = lo * P.h_kv + head;
-          cut = whole ? s_before[lo] * P.h_kv + head * len + len * (rest - (long long)head * s_ctas[lo]) / s_ctas[lo] : at;
+          const unsigned rest = at - starts[lo] * scale, len = s_before[lo + 1] - s_before[lo], k = s_ctas[lo];
+          const unsigned head = rest / (whole ? k : len);
+          u = lo * h_kv + head;
+          cut = whole ? s_before[lo] * h_kv + head * len + len * (rest - head * k) / k : at;
         }
         P.tile_cuts[b] = cut;
-        if (b < P.n_ctas) P.cut_units[b] = u;
+        if (b < n_ctas) P.cut_units[b] = (int)u;
       }
-      for (int u = tid; u < n_tiles * P.h_kv; u += THREADS) {
-        const int i = u / P.h_kv, head = u - i * P.h_kv;
-        if (whole) {
-          const int b = (int)s_front[i] + head * s_ctas[i];
-          P.unit_ctas[u] = make_int2(b, b + s_ctas[i] - 1);
-        } else {
-          const long long from = s_before[i] * P.h_kv + head * length(i);
-          P.unit_ctas[u] = make_int2((int)(from / each), (int)((from + length(i) - 1) / each));
-        }
+      for (unsigned u = tid; u < n_tiles * h_kv; u += THREADS) {
+        const unsigned i = u / h_kv, head = u - i * h_kv, len = s_before[i + 1] - s_before[i];
+        const unsigned from = s_before[i] * h_kv + head * len, first = s_front[i] + head * s_ctas[i];
+        P.unit_ctas[u] = whole ? make_int2((int)first, (int)(first + s_ctas[i] - 1)) : make_int2((int)(from / each), (int)((from + len - 1) / each));
       }
       if (tid == 0) {
         P.header->status = s_bad;
