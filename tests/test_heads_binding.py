@@ -18,7 +18,7 @@ def device(request, monkeypatch):
     if request.param == "cpu":
         native._bind_torch()
         monkeypatch.setattr(native, "_device", lambda where, x: -1)
-        monkeypatch.setattr(native, "_stream", lambda stream: 0)
+        monkeypatch.setattr(native, "_stream", lambda stream, dev: 0)
         real = native.library()
 
         class Library:

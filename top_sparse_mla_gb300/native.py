@@ -281,8 +281,10 @@ def _bind_torch() -> None:
     torch = module
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
+        if dev is not None and _raw_stream is not None:   # the current device, as _device found it
+            return _raw_stream(dev)
         if torch is None:
             _bind_torch()
         if _raw_stream is not None:
@@ -389,12 +391,13 @@ def _table_pitch(where: str, dev: int, x, n_req: int, cols: int) -> int:
 
 def _heads(where: str, dev: int, x, name: str, dtype, n: int, h: int, d: int):
     """(token pitch, head pitch) of a [n, h, d] tensor whose last dimension is dense."""
-    ld, hd, one = x.stride() if x.dim() == 3 else (0, 0, 0)
-    if x.dtype is not dtype or x.shape != (n, h, d) or (n > 0 and one != 1) or x.get_device() != dev:
-        _refuse(where, f"{name} must be a {dtype} tensor of shape {(n, h, d)} with a dense last dimension on the "
-                f"current CUDA device, got {x.dtype} {tuple(x.shape)} on {x.device}")
-    # a pitch that no second row uses may be anything: give the dense one
-    return (ld if n > 1 else h * d), (hd if h > 1 else d)
+    if x.shape == (n, h, d) and x.dtype is dtype and x.get_device() == dev:
+        ld, hd, one = x.stride()
+        if one == 1 or n == 0:
+            # a pitch that no second row uses may be anything: give the dense one
+            return (ld if n > 1 else h * d), (hd if h > 1 else d)
+    _refuse(where, f"{name} must be a {dtype} tensor of shape {(n, h, d)} with a dense last dimension on the "
+            f"current CUDA device, got {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
 def dsa_page_map(ctx_lens, new_lens, block_table, free_pages, page_size: int, cu_new, kv_lens, positions, slots,
@@ -557,7 +560,7 @@ def dsa_kv8_prefix_attn_fwd(q, k_pool, v_pool, k_scale, v_scale, block_table, cu
             and prefix_lens.is_contiguous() and cu_groups.get_device() == prefix_lens.get_device() == dev):
         _dense(where, dev, (prefix_lens, "prefix_lens", _I32, (max(n, 0),)), (cu_groups, "cu_groups", _I32, (n + 1,)))
     rc = library().dsa_kv8_prefix_attn_fwd(*front, cu_groups.data_ptr(), prefix_lens.data_ptr(), n, *back, ctypes.byref(p),
-                                           workspace.data_ptr(), workspace.nbytes, _stream(stream))
+                                           workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
@@ -614,7 +617,7 @@ def dsa_qk_norm_rope(q, k, positions, q_weight, k_weight, q_out, k_out, p: DsaQk
     _weights(where, dev, k_weight, "k_weight", dtype, d)
     rc = library().dsa_qk_norm_rope(q.data_ptr(), q_ld, q_hd, _ptr(k), k_ld, k_hd, positions.data_ptr(), _ptr(q_weight),
                                     _ptr(k_weight), q_out.data_ptr(), qo_ld, qo_hd, _ptr(k_out), ko_ld, ko_hd,
-                                    ctypes.byref(p), _stream(stream))
+                                    ctypes.byref(p), _stream(stream, dev))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
@@ -641,7 +644,7 @@ def dsa_kv_gather(pool, block_table, cu_rows, out, page_size: int, lens=None, st
         _refuse(where, "status must be a 32-bit word on the current CUDA device")
     rc = library().dsa_kv_gather(pool.data_ptr(), pool.shape[0], block_table.data_ptr(), table_ld, cols, int(page_size),
                                  cu_rows.data_ptr(), _ptr(lens), n_req, out.data_ptr(), ld if n_out > 1 else 576, n_out,
-                                 _ptr(status), _stream(stream))
+                                 _ptr(status), _stream(stream, dev))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
@@ -708,7 +711,7 @@ def dsa_mla_prefill_fwd(q, k_nope, k_rope, v, cu_q, cu_kv, out, p: DsaMlaParams,
     rc = library().dsa_mla_prefill_fwd(q.data_ptr(), q_ld, q_hd, k_nope.data_ptr(), k_ld, k_hd, k_rope.data_ptr(), r_ld if m > 1 else 64,
                                        v.data_ptr(), v_ld, v_hd, cu_q.data_ptr(), cu_kv.data_ptr(), out.data_ptr(), out_ld,
                                        out_hd, _ptr(lse), ctypes.byref(p), workspace.data_ptr(),
-                                       workspace.nbytes, _stream(stream))
+                                       workspace.nbytes, _stream(stream, dev))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
