@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
 struct Ctx {
   uint32_t sb, bars;
   volatile int* misc;   // [0]: tensor memory address, [1]: abort, [2]: blocks copied,
-                        // [3]: buffer of the values to be mended
+                        // [3]: block whose values are to be mended
   uint32_t* status;
 };
 
@@ -520,12 +520,11 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
       if (due & bit) {   // O += P V with block g - 1
         const uint32_t buf = (g - 1) % V_BUFS;
         if (!v_there) {
-          if (!wait_1(c, B_VFULL + buf, ((g - 1) / V_BUFS) & 1)) return;
           if (partial) {
-            c.misc[3] = (int)buf;
-            mbar_arrive(bar(c, B_FIX));
             if (!wait_1(c, B_FIXED, fixes & 1)) return;
             ++fixes;
+          } else if (!wait_1(c, B_VFULL + buf, ((g - 1) / V_BUFS) & 1)) {
+            return;
           }
           v_there = true;
         }
@@ -570,6 +569,10 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
     first = x.begins(i);
     last = ends;
     partial = x.t.kv - (x.s0 + i) * BLOCK < BLOCK;
+    if (partial) {   // its values are mended while its weights are formed
+      c.misc[3] = (int)g;
+      mbar_arrive(bar(c, B_FIX));
+    }
     kp += 3;
     ++i;
     ++g;
@@ -577,7 +580,8 @@ DSA_DEV void products(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles)
 }
 
 // The values of a request's last block: rows that are not the request's may hold anything, and 0 * NaN is
-// not 0.  One warp, when the products ask for it.
+// not 0.  One warp, for each block that the products name: those of the blocks two before it were used by
+// then, so that its wait for them is for the phase that comes next.
 template <bool SPLIT>
 DSA_DEV void fix_values(const Params& P, const Ctx& c, uint8_t* sm, int n_tiles) {
   const int lane = threadIdx.x & 31;
@@ -589,7 +593,9 @@ DSA_DEV void fix_values(const Params& P, const Ctx& c, uint8_t* sm, int n_tiles)
     if (blocks == 0 || rows >= BLOCK) continue;   // only the last block can have fewer
     if (!wait_w(c, B_FIX, fixes & 1)) return;
     ++fixes;
-    uint8_t* v = sm + Smem::V + c.misc[3] * Smem::VBUF;
+    const uint32_t g = (uint32_t)c.misc[3];
+    if (!wait_w(c, B_VFULL + g % V_BUFS, (g / V_BUFS) & 1)) return;
+    uint8_t* v = sm + Smem::V + g % V_BUFS * Smem::VBUF;
     for (int r = rows + (lane >> 3); r < BLOCK; r += 4) {
       *reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(v + PANEL + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
