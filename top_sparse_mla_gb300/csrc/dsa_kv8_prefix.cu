@@ -55,9 +55,10 @@ struct Sum {   // of a row: O and l in units of 2^m
 };
 
 template <int D>
-__device__ __forceinline__ void add_part(const Params& P, const Part& a, int token, int head, int k, Sum& sum) {
+__device__ __forceinline__ void add_part(const Params& P, const Part& a, int n_tiles, int token, int head, int k, Sum& sum) {
   if (a.q_len * P.group > P.small_rows && P.tile_shares) {
     const int row = (token - a.q0) * P.group + head % P.group, tile = a.tile0 + row / TILE_ROWS, r = row % TILE_ROWS;
+    if (tile >= n_tiles) return;   // lists that do not ascend may give more tiles than there is room for
     const int2 by = P.unit_ctas[tile * P.h_kv + head / P.group];
     if (by.x != by.y) {
       for (int b0 = by.x; b0 <= by.y; b0 += AT_ONCE) {
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Part own = P.parts[P.n_groups + blockIdx.y];
   const Part shared = P.parts[own.lo > 0 ? own.group : P.n_groups + blockIdx.y];
+  const int n_tiles = P.header->n_tiles;
   const long long items = (long long)own.q_len * P.h_q * (D / 8);
   for (long long u = (long long)blockIdx.x * JOIN_THREADS + threadIdx.x; u < items; u += (long long)gridDim.x * JOIN_THREADS) {
     // the heads of a KV head side by side, as their rows are in a piece
@@ -106,8 +108,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     s.l = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) s.o[e] = 0.f;
-    if (own.lo > 0) add_part<D>(P, shared, token, head, k, s);
-    add_part<D>(P, own, token, head, k, s);
+    if (own.lo > 0) add_part<D>(P, shared, n_tiles, token, head, k, s);
+    add_part<D>(P, own, n_tiles, token, head, k, s);
     const float inv = s.l > 0.f ? 1.0f / s.l : (s.l == 0.f ? 0.f : s.l);   // a NaN sum stays one
     uint4 w;
     w.x = pack(s.o[0] * inv, s.o[1] * inv, P.fp16);
