@@ -7,6 +7,7 @@
 // (dsa_kv8_rows.cuh, dsa_kv8_tiles.cuh) and leave each row's O, m and l of either part in the
 // workspace; a last kernel joins the two.
 
+#include "device.cuh"
 #include "dsa_kv8_prefix.h"
 
 #include "dsa_kv8_rows.cuh"
@@ -227,7 +228,7 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   if (bad_call(c, p)) return DSA_ERR_INVALID_ARG;
   if (n_groups > 0 && (!cu_groups || !prefix_lens || !aligned(cu_groups, 4) || !aligned(prefix_lens, 4))) return DSA_ERR_INVALID_ARG;
   int sms = 0;
-  const int rc0 = gb300_sms(&sms);
+  const int rc0 = dsa::gb300_sms(&sms);
   if (rc0 != DSA_OK) return rc0;
   const PrefixLayout L = prefix_layout(p, n_groups, sms);
   if (workspace_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "device.cuh"
 #include "dsa_kv_gather.h"
 #include "ptx_sm103.cuh"
 
@@ -117,11 +118,9 @@ extern "C" int dsa_kv_gather(const void* pool, int64_t n_rows, const int32_t* bl
       (n_rows > 0 && (!pool || !aligned(pool, 16))) ||
       (table_cols > 0 && (!block_table || !aligned(block_table, 4) || (n_req > 1 && table_ld < table_cols))))
     return DSA_ERR_INVALID_ARG;
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED_DEVICE;
+  int sms = 0;
+  const int device_rc = dsa::gb300_sms(&sms);
+  if (device_rc != DSA_OK) return device_rc;
   Params P;
   P.pool = static_cast<const uint8_t*>(pool);
   P.n_rows = (long long)n_rows;

@@ -37,6 +37,7 @@
 
 #include <atomic>
 
+#include "device.cuh"
 #include "dsa_mla_prefill.h"
 #include "ptx_sm103.cuh"
 
@@ -1074,12 +1075,9 @@ int dsa_mla_prefill_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k
                           (p->n_keys > 1 && k_rope_ld < DR)))
       return DSA_ERR_INVALID_ARG;
   }
-  int dev = 0, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED_DEVICE;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSA_ERR_CUDA;
+  int sms = 0;
+  const int device_rc = dsa::gb300_sms(&sms);
+  if (device_rc != DSA_OK) return device_rc;
   const Layout L = layout(p, sms);
   if (workspace_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -16,6 +16,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "device.cuh"
 #include "dsa_qk_norm_rope.h"
 #include "ptx_sm103.cuh"
 
@@ -307,12 +308,9 @@ extern "C" int dsa_qk_norm_rope(const void* q, int64_t q_ld, int64_t q_hd, const
   if ((q_out == q && (q_out_ld != q_ld || q_out_hd != q_hd)) || (p->h_k > 0 && k_out == k && (k_out_ld != k_ld || k_out_hd != k_hd)))
     return DSA_ERR_INVALID_ARG;
   if (!positions || !aligned(positions, 4)) return DSA_ERR_INVALID_ARG;
-  int dev = 0, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED_DEVICE;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSA_ERR_CUDA;
+  int sms = 0;
+  const int device_rc = dsa::gb300_sms(&sms);
+  if (device_rc != DSA_OK) return device_rc;
   Params P;
   auto side = [](const void* x, int64_t ld, int64_t hd, const void* w, void* y, int64_t y_ld, int64_t y_hd) {
     return Side{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), static_cast<uint16_t*>(y), (long long)ld,

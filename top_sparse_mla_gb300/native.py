@@ -589,11 +589,6 @@ def dsa_qk_params_init(q, k=None, rotary_dim=None, rotary_start: int = 0, interl
     return p
 
 
-def _weights(where: str, dev: int, w, name: str, dtype, d: int) -> None:
-    if w is not None and (w.dtype is not dtype or w.shape != (d,) or not w.is_contiguous() or w.get_device() != dev):
-        _dense(where, dev, (w, name, dtype, (d,)))
-
-
 def dsa_qk_norm_rope(q, k, positions, q_weight, k_weight, q_out, k_out, p: DsaQkParams, stream=None) -> None:
     """RMS norm and rotation of the heads of queries and keys (include/dsa_qk_norm_rope.h). q, q_out: bf16 or fp16
     [n_tokens, h_q, d]; k, k_out: [n_tokens, h_k, d], or None where p has no keys (token and head pitches allowed;
@@ -604,20 +599,29 @@ def dsa_qk_norm_rope(q, k, positions, q_weight, k_weight, q_out, k_out, p: DsaQk
     if _KV8_TYPES.get(dtype) != p.type:
         _refuse(where, "q's type is not that of p")
     q_ld, q_hd = _heads(where, dev, q, "q", dtype, n, h_q, d)
-    qo_ld, qo_hd = _heads(where, dev, q_out, "q_out", dtype, n, h_q, d)
-    if (k is None) != (h_k == 0) or (k_out is None) != (h_k == 0):
-        _refuse(where, "k and k_out must be given where p has keys, and only there")
+    qo_ld, qo_hd = (q_ld, q_hd) if q_out is q else _heads(where, dev, q_out, "q_out", dtype, n, h_q, d)
+    k_at = ko_at = kw_at = qw_at = None
     k_ld = k_hd = ko_ld = ko_hd = 0
     if h_k:
+        if k is None or k_out is None:
+            _refuse(where, "k and k_out must be given where p has keys")
         k_ld, k_hd = _heads(where, dev, k, "k", dtype, n, h_k, d)
-        ko_ld, ko_hd = _heads(where, dev, k_out, "k_out", dtype, n, h_k, d)
+        ko_ld, ko_hd = (k_ld, k_hd) if k_out is k else _heads(where, dev, k_out, "k_out", dtype, n, h_k, d)
+        k_at, ko_at = k.data_ptr(), k_out.data_ptr()
+    elif k is not None or k_out is not None:
+        _refuse(where, "k and k_out must be None where p has no keys")
     if not (positions.dtype is _I32 and positions.shape == (n,) and positions.is_contiguous() and positions.get_device() == dev):
         _dense(where, dev, (positions, "positions", _I32, (n,)))
-    _weights(where, dev, q_weight, "q_weight", dtype, d)
-    _weights(where, dev, k_weight, "k_weight", dtype, d)
-    rc = library().dsa_qk_norm_rope(q.data_ptr(), q_ld, q_hd, _ptr(k), k_ld, k_hd, positions.data_ptr(), _ptr(q_weight),
-                                    _ptr(k_weight), q_out.data_ptr(), qo_ld, qo_hd, _ptr(k_out), ko_ld, ko_hd,
-                                    ctypes.byref(p), _stream(stream, dev))
+    if q_weight is not None:
+        if not (q_weight.dtype is dtype and q_weight.shape == (d,) and q_weight.is_contiguous() and q_weight.get_device() == dev):
+            _dense(where, dev, (q_weight, "q_weight", dtype, (d,)))
+        qw_at = q_weight.data_ptr()
+    if k_weight is not None:
+        if not (k_weight.dtype is dtype and k_weight.shape == (d,) and k_weight.is_contiguous() and k_weight.get_device() == dev):
+            _dense(where, dev, (k_weight, "k_weight", dtype, (d,)))
+        kw_at = k_weight.data_ptr()
+    rc = library().dsa_qk_norm_rope(q.data_ptr(), q_ld, q_hd, k_at, k_ld, k_hd, positions.data_ptr(), qw_at, kw_at,
+                                    q_out.data_ptr(), qo_ld, qo_hd, ko_at, ko_ld, ko_hd, ctypes.byref(p), _stream(stream, dev))
     if rc != DSA_OK:
         raise DsaError(rc, where)
 
@@ -628,11 +632,13 @@ def dsa_kv_gather(pool, block_table, cu_rows, out, page_size: int, lens=None, st
     [n_req] or None; status: uint32 or int32 [1] device tensor or None."""
     where = "dsa_kv_gather"
     dev = _device(where, pool)
-    if pool.dtype is not _U8 or pool.dim() != 2 or pool.shape[1] != DSA_ROW_BYTES or not pool.is_contiguous():
-        _dense(where, dev, (pool, "pool", _U8, (pool.shape[0], DSA_ROW_BYTES)))
+    rows = pool.shape[0] if pool.dim() == 2 else 0
+    if not (pool.dtype is _U8 and pool.shape == (rows, DSA_ROW_BYTES) and pool.is_contiguous()):
+        _dense(where, dev, (pool, "pool", _U8, (rows, DSA_ROW_BYTES)))
     n_req, cols = block_table.shape[0], block_table.shape[-1]
     table_ld = _table_pitch(where, dev, block_table, n_req, cols)
-    _dense(where, dev, (cu_rows, "cu_rows", _I32, (n_req + 1,)))
+    if not (cu_rows.dtype is _I32 and cu_rows.shape == (n_req + 1,) and cu_rows.is_contiguous() and cu_rows.get_device() == dev):
+        _dense(where, dev, (cu_rows, "cu_rows", _I32, (n_req + 1,)))
     if lens is not None:
         _dense(where, dev, (lens, "lens", _I32, (n_req,)))
     n_out, (ld, one) = out.shape[0], out.stride() if out.dim() == 2 else (0, 0)
@@ -642,7 +648,7 @@ def dsa_kv_gather(pool, block_table, cu_rows, out, page_size: int, lens=None, st
         _refuse(where, "the rows of out overlap")
     if status is not None and (status.element_size() != 4 or status.get_device() != dev):
         _refuse(where, "status must be a 32-bit word on the current CUDA device")
-    rc = library().dsa_kv_gather(pool.data_ptr(), pool.shape[0], block_table.data_ptr(), table_ld, cols, int(page_size),
+    rc = library().dsa_kv_gather(pool.data_ptr(), rows, block_table.data_ptr(), table_ld, cols, int(page_size),
                                  cu_rows.data_ptr(), _ptr(lens), n_req, out.data_ptr(), ld if n_out > 1 else 576, n_out,
                                  _ptr(status), _stream(stream, dev))
     if rc != DSA_OK:
