@@ -23,12 +23,14 @@
 // kernel joins.  A 2123-token prefill of 64 heads, 3.8 units an SM, took 185 us in shares and 118 in whole
 // units.
 //
-// What bounds it.  6 chunks of up to 2048 queries on up to 8k keys, 32 heads: 820 us, 1320 TFLOP/s, 0.70 of a
-// large bf16 product's rate.  A block of both halves takes 3400 cycles there, its products 2560.  What
-// is missing are the keys of the next block: beside 96 KB of queries shared memory holds 1.6 blocks, so
-// that a copy has 1300 cycles of products to arrive in, and takes 2000.  (Sent for to L2 two to five blocks
-// ahead, they come no sooner: 850.)  64 queries on 32k keys, 16 heads: 66 us, memory's part 40; the rest is the
-// beginning, and the join of 10 pieces a unit.
+// What bounds it.  6 chunks of up to 2048 queries on up to 8k keys, 32 heads: 763 us in a burst, 810 to 840 in
+// a row (1320 TFLOP/s, 0.77 of a large bf16 product's sustained rate), at 1.35 kW, which holds the clock at
+// 1.66 GHz.  A block of both halves takes 3400 cycles, its products 2560.  What is missing are the keys of the
+// next block: beside 96 KB of queries shared memory holds 1.6 blocks, so that a copy has 1300 cycles of
+// products to arrive in, and takes 2000.  (Sent for to L2 two to five blocks ahead they come no sooner, and
+// five panels of keys beside one and a half blocks of values, 1500 cycles, change nothing: 849 us, and 72
+// against 66 below.)  64 queries on 32k keys, 16 heads: 66 us, memory's part 40; the rest is the beginning, and
+// the join of 10 pieces a unit.
 //
 // Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
 // and the CTA's roles stop, drain the tensor core and free its memory.
