@@ -29,7 +29,7 @@
 // next block: beside 96 KB of queries shared memory holds 1.6 blocks, so that a copy has 1300 cycles of
 // products to arrive in, and takes 2000.  (Sent for to L2 two to five blocks ahead they come no sooner, and
 // five panels of keys beside one and a half blocks of values, 1500 cycles, change nothing: 849 us, and 72
-// against 66 below.)  64 queries on 32k keys, 16 heads: 66 us, memory's part 40; the rest is the beginning, and
+// against 66 below.)  64 queries on 32k keys, 16 heads: 64 us, memory's part 40; the rest is the beginning, and
 // the join of 10 pieces a unit.
 //
 // Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
@@ -71,6 +71,9 @@ constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 200, OTHER_REGS = 104;
 static_assert(8 * SOFTMAX_REGS + 4 * OTHER_REGS <= 12 * LAUNCH_REGS, "more registers than the CTA has would be waited for");
 constexpr unsigned long long WAIT_LIMIT_CYCLES = 20000000000ull;   // ~10 s at 2 GHz
 constexpr int PLAN_THREADS = 1024;
+// Of the plan for at most as many tiles and twice as many requests, whose barriers cost less: us with it and with 1024,
+// 64 short prompts 23.2 and 24.8, a 2123-token one 90.6 and 91.8, 64 queries on 32k 63.0 and 65.1.
+constexpr int FEW_THREADS = 256;
 constexpr int SPLIT_UNITS = 2;     // units per SM below which they may be split
 
 // barriers
@@ -171,15 +174,16 @@ DSA_DEV T scan(T v, T* s_warp, T& all) {
   return before;
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ Params P) {
+template <int N>   // threads
+__global__ void __launch_bounds__(N) plan_kernel(const __grid_constant__ Params P) {
   extern __shared__ int s_tile[];   // [n_req + 1] exclusive prefix of the requests' tiles
-  __shared__ int s_warp[PLAN_THREADS / 32], s_place[PLAN_THREADS];
-  __shared__ long long s_long[PLAN_THREADS / 32], s_before[PLAN_THREADS];
+  __shared__ int s_warp[N / 32], s_place[N];
+  __shared__ long long s_long[N / 32], s_before[N];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, n = P.n_req;
-  for (int r = tid; r < n; r += PLAN_THREADS) s_tile[r] = (rows_of(P, r) + TILE_ROWS - 1) / TILE_ROWS;
+  for (int r = tid; r < n; r += N) s_tile[r] = (rows_of(P, r) + TILE_ROWS - 1) / TILE_ROWS;
   __syncthreads();
-  const int per = ((n + PLAN_THREADS - 1) / PLAN_THREADS) | 1;   // odd: no bank conflicts
+  const int per = ((n + N - 1) / N) | 1;   // odd: no bank conflicts
   const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
   int mine = 0, all = 0;
   for (int r = r0; r < r1; ++r) mine += s_tile[r];
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
     share = max((total + P.n_ctas - 1) / P.n_ctas, 2LL);
     if (tid < n_tiles) s_before[tid] = t.before;
     __syncthreads();
-    for (int b = tid; b < P.n_ctas; b += PLAN_THREADS) {
+    for (int b = tid; b < P.n_ctas; b += N) {
       const long long at_step = b * share;
       Share s = {-1, 0, 0, 0};
       if (at_step < total) {
@@ -229,19 +233,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constan
       P.shares[b] = s;
     }
   } else {
-    // the longest first (all above PLAN_THREADS - 1 blocks alike): a count of each length, the
+    // the longest first (all of N - 1 blocks and more alike): a count of each length, the
     // places behind the longer ones, then the tiles.  The order among equal ones changes no result.
-    auto place = [](const Tile& t) { return PLAN_THREADS - 1 - min(t.steps, PLAN_THREADS - 1); };
+    auto place = [](const Tile& t) { return N - 1 - min(t.steps, N - 1); };
     s_place[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < n_tiles; i += PLAN_THREADS) atomicAdd(&s_place[place(tile(i))], 1);
+    for (int i = tid; i < n_tiles; i += N) atomicAdd(&s_place[place(tile(i))], 1);
     __syncthreads();
     int total = 0;
     const int before = scan(s_place[tid], s_warp, total);
     __syncthreads();
     s_place[tid] = before;
     __syncthreads();
-    for (int i = tid; i < n_tiles; i += PLAN_THREADS) {
+    for (int i = tid; i < n_tiles; i += N) {
       const Tile t = tile(i);
       P.tiles[atomicAdd(&s_place[place(t)], 1)] = t;
     }
@@ -1130,7 +1134,8 @@ int dsa_mla_prefill_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k
     return DSA_ERR_CUDA;
   const size_t smem = (size_t)(P.n_req + 1) * sizeof(int);
   static_assert((DSA_MLA_MAX_REQ + 1) * sizeof(int) <= 34 * 1024, "the plan's dynamic shared memory needs no permission");
-  plan_kernel<<<1, PLAN_THREADS, smem, st>>>(P);
+  if (P.max_tiles <= FEW_THREADS && P.n_req <= 2 * FEW_THREADS) plan_kernel<FEW_THREADS><<<1, FEW_THREADS, smem, st>>>(P);
+  else plan_kernel<PLAN_THREADS><<<1, PLAN_THREADS, smem, st>>>(P);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (P.bf16) return P.split ? launch<true, true>(P, M, st) : launch<true, false>(P, M, st);
   return P.split ? launch<false, true>(P, M, st) : launch<false, false>(P, M, st);
