@@ -130,6 +130,12 @@ def test_many_requests(d):
     _check(PrefixCase(6, lens, [(500, 32), (3, 40), (997, 48)], page=16, h=1, g=2, d=d))
 
 
+@pytest.mark.parametrize("n,groups", [(4096, [(1, 16)] * 4096), (8191, [(8191, 16)]), (6000, [(3, 16)] * 2000)])
+def test_as_many_requests_and_groups_as_there_may_be(n, groups):
+    assert n + len(groups) <= native.DSA_KV8_MAX_REQ and len(groups) <= native.DSA_KV8_MAX_GROUPS
+    _check(PrefixCase(21, [(1, 18 + i % 3) for i in range(n)], groups, page=16, h=1, g=2, d=64))
+
+
 def test_without_groups_and_with_groups_of_one():
     lens = [(1, 300), (9, 70), (1, 1), (0, 0), (2, 513)]
     c = PrefixCase(7, lens, [(5, None)], h=2, g=4)
