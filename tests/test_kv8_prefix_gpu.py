@@ -118,8 +118,8 @@ def test_group_sizes(g):
 
 
 def test_large_groups_and_long_prefixes():
-    _check(PrefixCase(3, [(1, 9000 + 3 * i) for i in range(70)], [(70, 8999)], page=64, h=1, g=8))
-    _check(PrefixCase(4, [(2, 3000 + i) for i in range(300)], [(100, 2990), (200, 2990)], page=128, h=2, g=2, d=64, dtype="fp16"))
+    _check(PrefixCase(3, [(1, 6000 + 3 * i) for i in range(40)], [(40, 5999)], page=64, h=1, g=8))
+    _check(PrefixCase(4, [(2, 1500 + i) for i in range(200)], [(70, 1490), (130, 1490)], page=128, h=2, g=2, d=64, dtype="fp16"))
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -250,7 +250,7 @@ def test_captured_as_a_first_call_and_replayed_on_another_batch(n):
 
 
 def test_a_wait_that_runs_out_is_reported_and_recovered_from():
-    c = PrefixCase(20, [(1, 4000 + i) for i in range(300)], [(300, 3990)], page=128, h=8, g=8, d=64)
+    c = PrefixCase(20, [(1, 4000 + i) for i in range(300)], [(300, 3990)], page=128, h=2, g=8, d=64)
     D = c.device()
     want, want_l, status = c.run(D)
     assert status == 0
