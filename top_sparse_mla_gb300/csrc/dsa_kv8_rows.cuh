@@ -9,6 +9,7 @@
 #include <limits.h>
 
 #include "dsa_kv8.cuh"
+#include "dsa_kv8_cuts.h"
 
 namespace dsa_kv8 {
 
@@ -22,7 +23,6 @@ constexpr int PLAN_THREADS = 1024;
 // and 35.4, 1500 47.4 and 50.8, 2048 (16 a thread) 63.3 and 63.6, 4096 124.7 and 111.3.
 constexpr int OWN_PLAN = 12;
 constexpr int WHOLE_SHARES = 3;  // see plan_kernel
-constexpr int PIECE_BLOCKS = 2;   // blocks that take a CTA of the tiles' kernel as long as a piece's beginning and end
 constexpr int FEW_THREADS = 256;  // of the plan, where rows_kernel's CTAs find their shares
 // rows_kernel's CTAs per SM, by head dimension and tiles of 8 query rows: what its registers leave room for.
 // Every CTA has to be resident at once, since the plan gives each an equal share.
@@ -333,15 +333,14 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       long long all_blocks = 0, all_ctas = 0;
       unsigned before = (unsigned)scan<THREADS>(sum, s_step_warp, all_blocks);
       const unsigned every = (unsigned)all_blocks, total = every * h_kv;
-      // Every CTA as many blocks; or, where no CTA gets PIECE_BLOCKS more than that, a number of CTAs for each unit, so
-      // that each CTA has one piece to begin and to leave.
-      const unsigned each = max((total + n_ctas - 1) / n_ctas, 2u);
+      // Every CTA as many blocks, or each unit CTAs of its own (own_pieces())
+      const unsigned each = equal_blocks(total, n_ctas);
       if (tid == 0) s_longest = 0;
       __syncthreads();
       unsigned some_ctas = 0;
       for (int i = i0; i < i1; ++i) {
         // below 2^24 blocks, and fewer than 256 SMs
-        const unsigned len = s_front[i], k = max(min(len * n_ctas / total, len / 2), 1u);
+        const unsigned len = s_front[i], k = own_ctas(len, total, n_ctas);
         s_before[i] = before;
         P.tile_steps[i] = before;
         before += len;
@@ -357,30 +356,17 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       }
       if (tid == 0) s_front[n_tiles] = (unsigned)all_ctas;
       __syncthreads();
-      const bool whole = n_tiles * h_kv <= n_ctas && s_longest <= each + PIECE_BLOCKS;
-      const unsigned* starts = whole ? s_front : s_before;
-      const unsigned scale = whole ? 1 : h_kv;
+      const Cuts cuts{s_before, s_front, s_ctas, (unsigned)n_tiles, h_kv, each,
+                      own_pieces((unsigned long long)all_ctas, n_ctas, (unsigned)s_longest, each)};
       for (unsigned b = tid; b <= n_ctas; b += THREADS) {
-        const unsigned at = whole ? b : b * each;
-        unsigned cut = total, u = n_tiles * h_kv;
-        if (at < starts[n_tiles] * scale) {
-          int lo = 0, hi = n_tiles;   // the tile with starts[lo] * scale <= at < starts[lo + 1] * scale
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (starts[mid] * scale <= at) lo = mid; else hi = mid;
-          }
-          const unsigned rest = at - starts[lo] * scale, len = s_before[lo + 1] - s_before[lo], k = s_ctas[lo];
-          const unsigned head = rest / (whole ? k : len);
-          u = lo * h_kv + head;
-          cut = whole ? s_before[lo] * h_kv + head * len + len * (rest - head * k) / k : at;
-        }
-        P.tile_cuts[b] = cut;
+        unsigned u;
+        P.tile_cuts[b] = cuts.cut(b, u);
         if (b < n_ctas) P.cut_units[b] = (int)u;
       }
       for (unsigned u = tid; u < n_tiles * h_kv; u += THREADS) {
-        const unsigned i = u / h_kv, head = u - i * h_kv, len = s_before[i + 1] - s_before[i];
-        const unsigned from = s_before[i] * h_kv + head * len, first = s_front[i] + head * s_ctas[i];
-        P.unit_ctas[u] = whole ? make_int2((int)first, (int)(first + s_ctas[i] - 1)) : make_int2((int)(from / each), (int)((from + len - 1) / each));
+        int2 by;
+        cuts.ctas_of(u, by.x, by.y);
+        P.unit_ctas[u] = by;
       }
       if (tid == 0) {
         P.header->status = s_bad;
