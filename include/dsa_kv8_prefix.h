@@ -7,8 +7,9 @@
  * same pages for the whole pages among their first prefix_lens[g] tokens.  The call takes what
  * the group shares from the table of one of its requests that has queries, as far as every
  * query of the group sees it: the least of prefix_lens[g] and of kv_len - q_len + 1 over the
- * group's requests with queries, in whole pages.  So a prefix length may be too large by what
- * is not seen, but not by pages that differ, and it is right, if slower, to give less.
+ * group's requests with queries, in whole pages, and at most 2^31 - 1024 - n_tokens tokens.  So
+ * a prefix length may be too large by what is not seen, but not by pages that differ, and it is
+ * right, if slower, to give less.
  * Requests outside every group share nothing.
  *
  *   cu_groups    int32 [n_groups + 1], ascending, within [0, n_req] (values outside are taken

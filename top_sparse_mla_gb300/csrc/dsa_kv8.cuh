@@ -90,6 +90,7 @@ struct Params {
   float* pieces;
   int* row_parts;   // parts of rows_kernel whose units are taken whole
   int n_groups, tile_shares;
+  int most_shared;   // tokens of a group: its rows' positions go on from the last one, and stay as far below 2^31 as others
   uint32_t test_block;   // block of CTA 0 at which the copies stop (DSA_KV8_FLAG_TEST_WAIT_TIMEOUT)
   float scale_log2;   // softmax_scale * log2 e
 };

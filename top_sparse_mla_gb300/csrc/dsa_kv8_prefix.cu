@@ -245,6 +245,7 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   P.part_o = reinterpret_cast<float*>(ws + L.part_o);
   P.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   P.n_groups = n_groups;
+  P.most_shared = (int)(MOST_TOKENS - p->n_tokens);
   P.own_plan = 0;
   P.small_rows = 8 * prefix_row_tiles(p);
   P.has_tiles = L.base.max_tiles > 0;

@@ -113,7 +113,7 @@ __device__ __forceinline__ void find_parts(const Params& P, int* s_groups, long 
   for (int g = tid; g <= P.n_groups; g += THREADS) {
     const int begin = P.n_groups > 0 ? P.cu_groups[g] : 0, prefix = g < P.n_groups ? P.prefix_lens[g] : 0;
     if (g < P.n_groups) {
-      s_shared[g] = max(prefix, 0);
+      s_shared[g] = min(max(prefix, 0), P.most_shared);
       s_first[g] = n;
     }
     s_begin[g] = min(max(begin, 0), n);
@@ -1144,6 +1144,9 @@ static int launch_rows(const Params& P, bool wide, cudaStream_t st) {
               : launch(rows_kernel<D, NT, W, PREFIX>, P.n_shares, 32 * W, smem, smem, st, P, true);
 }
 
+// positions stay below 2^31 with room for a step and a tile behind the last one
+constexpr long long MOST_TOKENS = (1LL << 31) - 1024;
+
 static int current_sms(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
@@ -1227,9 +1230,8 @@ static Params params_of(const Call& c, const dsa_kv8_params* p, const Layout& L,
   P.group = p->h_q / p->h_kv;
   P.n_pages = p->n_pages;
   P.page_shift = __builtin_ctz(p->page_size);
-  // positions stay below 2^31 with room for a step and a tile behind the last one
-  const long long cap = (long long)p->table_cols * p->page_size, most = (1LL << 31) - 1024;
-  P.cap = (int)(cap < most ? cap : most);
+  const long long cap = (long long)p->table_cols * p->page_size;
+  P.cap = (int)(cap < MOST_TOKENS ? cap : MOST_TOKENS);
   P.max_q_len = p->max_q_len;
   // a window that nothing passes is none; others stay where a position minus the window
   // (at least -2^30 minus 2^30) is an int
