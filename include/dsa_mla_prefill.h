@@ -12,7 +12,8 @@
  *               sees nothing)
  * Rows of q and out that belong to no request are neither used nor written.  Keys and values
  * that some query row of the request sees are finite; every other row may hold anything.  A
- * query that is not finite makes its own row NaN and no other.
+ * query that is not finite, or whose largest score is not in fp32, makes its own row NaN and no
+ * other.
  *
  *   q        bf16 or fp16 (`type`), [n_tokens][h][192]: 128 dims against k_nope, then 64 against k_rope
  *   k_nope   the same type, [n_keys][h][128]

@@ -661,6 +661,9 @@ DSA_DEV float2 unpack(uint32_t w) {
   if (!BF16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
+// The sum of a row at position pos.  Weights are 1 and more at their largest, so that one of 0 has seen nothing; but for a row
+// that has keys, all of whose scores are -inf: its query is not finite, and the softmax not defined.
+DSA_DEV float defined(float sum, int pos) { return sum == 0.f && pos >= 0 ? __int_as_float(0x7FC00000) : sum; }
 // 1 / sum; 0 for a row that saw nothing, and a NaN stays one
 DSA_DEV float inverse(float sum) { return sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum); }
 DSA_DEV float lse_of(float m, float l) { return l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l)); }
@@ -762,6 +765,7 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
     }
     const long long token = (long long)x.t.q0 + row;
     if (!SPLIT || x.pieces == 1) {
+      l = defined(l, pos);
       uint16_t* dst = P.out + token * P.out_ld + x.head * P.out_hd;
       const bool wide = ((uintptr_t)dst & 31) == 0;
       const float inv = inverse(l);
@@ -926,6 +930,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
       m = top;
     }
     const long long token = (long long)t.q0 + row;
+    l = defined(l, t.kv - t.rows + row);
     const float inv = inverse(l);
     *reinterpret_cast<uint2*>(P.out + token * P.out_ld + head * P.out_hd + 4 * chunk) =
         make_uint2(pack<BF16>(o[0] * inv, o[1] * inv), pack<BF16>(o[2] * inv, o[3] * inv));
