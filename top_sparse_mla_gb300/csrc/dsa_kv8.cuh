@@ -44,6 +44,7 @@ struct Header {
   long long share;   // steps of every CTA
   int row_units;     // PREFIX: units that rows_kernel's CTAs take whole, one after the other; 0 where they have shares
   int next_unit;     // how many were taken beside each CTA's first
+  unsigned long long planned;   // PREFIX: the call's number once its plan is there, and 0 in the end
 };
 
 enum { SHARED = 0, OWN = 1 };
@@ -90,6 +91,7 @@ struct Params {
   float* pieces;
   int* row_parts;   // parts of rows_kernel whose units are taken whole
   int n_groups, tile_shares;
+  unsigned long long call;   // another number for every call, never 0
   int most_shared;   // tokens of a group: its rows' positions go on from the last one, and stay as far below 2^31 as others
   uint32_t test_block;   // block of CTA 0 at which the copies stop (DSA_KV8_FLAG_TEST_WAIT_TIMEOUT)
   float scale_log2;   // softmax_scale * log2 e

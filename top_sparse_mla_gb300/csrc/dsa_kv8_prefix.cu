@@ -7,6 +7,8 @@
 // (dsa_kv8_rows.cuh, dsa_kv8_tiles.cuh) and leave each row's O, m and l of either part in the
 // workspace; a last kernel joins the two.
 
+#include <atomic>
+
 #include "device.cuh"
 #include "dsa_kv8_prefix.h"
 
@@ -98,6 +100,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
   const Part own = P.parts[P.n_groups + blockIdx.y];
   const Part shared = P.parts[own.lo > 0 ? own.group : P.n_groups + blockIdx.y];
   const int n_tiles = P.header->n_tiles;
+  // a graph's next launch has the same number
+  if (blockIdx.x + blockIdx.y + threadIdx.x == 0) P.header->planned = 0;
   const long long items = (long long)own.q_len * P.h_q * (D / 8);
   for (long long u = (long long)blockIdx.x * JOIN_THREADS + threadIdx.x; u < items; u += (long long)gridDim.x * JOIN_THREADS) {
     // the heads of a KV head side by side, as their rows are in a piece
@@ -245,6 +249,9 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   P.part_o = reinterpret_cast<float*>(ws + L.part_o);
   P.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   P.n_groups = n_groups;
+  static std::atomic<uint32_t> calls{0};
+  // the upper half: a workspace may have anything in it at first
+  P.call = 0x706C616Eull << 32 | calls.fetch_add(1, std::memory_order_relaxed);
   P.most_shared = (int)(MOST_TOKENS - p->n_tokens);
   P.own_plan = 0;
   P.small_rows = 8 * prefix_row_tiles(p);

@@ -290,6 +290,16 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
   }
   // ascending cu_q cannot give more tiles than the list has room for
   const int n_tiles = (int)min(all_tiles, (long long)P.max_tiles);
+  auto finish = [&]() {
+    if (PREFIX) __syncthreads();   // the whole plan in front of what says that it is there
+    if (tid != 0) return;
+    P.header->status = s_bad;
+    P.header->n_tiles = n_tiles;
+    P.header->share = share;
+    P.header->row_units = row_units;
+    P.header->next_unit = 0;
+    if (PREFIX) asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(&P.header->planned), "l"(P.call) : "memory");
+  };
   if (n_tiles > 0) {
     // the longest first (by cached tokens in blocks of 128, all above THREADS - 1 alike): a count
     // of each length, the places behind the longer ones, then the tiles.  The order among
@@ -368,13 +378,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
         cuts.ctas_of(u, by.x, by.y);
         P.unit_ctas[u] = by;
       }
-      if (tid == 0) {
-        P.header->status = s_bad;
-        P.header->n_tiles = n_tiles;
-        P.header->share = share;
-        P.header->row_units = row_units;
-        P.header->next_unit = 0;
-      }
+      finish();
       return;
     }
     auto length = [](const Tile& t) { return THREADS - 1 - min(max(t.hi - t.lo, 0) / 128, THREADS - 1); };
@@ -400,13 +404,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       P.tiles[atomicAdd(&s_place[length(t)], 1)] = t;
     }
   }
-  if (tid == 0) {
-    P.header->status = s_bad;
-    P.header->n_tiles = n_tiles;
-    P.header->share = share;
-    P.header->row_units = row_units;
-    P.header->next_unit = 0;
-  }
+  finish();
 }
 
 // ------------------------------------------------------------------------------ rows

@@ -139,6 +139,24 @@ DSA_DEV bool wait_unit(const Ctx& c, uint32_t u) {
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
+// PREFIX: the plan, and what was there before it, seen by the threads that meet this one behind this.  Only
+// griddepcontrol.wait does so by itself, and it would be for the end of rows_kernel.  The plan has run when
+// this kernel begins; it is the word's acquisition that orders reads behind the plan's writes.  (us, by that
+// wait and by the word: 64 requests behind 16k tokens 84.4 and 76.9, 240 verified 56.7 and 51.8.)
+DSA_DEV bool wait_planned(const Params& P, const Ctx& c) {
+  const unsigned long long start = clock64();
+  while (true) {
+    unsigned long long call;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(call) : "l"(&P.header->planned) : "memory");
+    if (call == P.call) return true;
+    if (clock64() - start > WAIT_LIMIT_CYCLES) {
+      atomicOr(c.status, DSA_STATUS_WAIT_TIMEOUT);
+      return false;
+    }
+    __nanosleep(50);
+  }
+}
+
 // For tests of the failure path: a wait that runs out, after an eighth of the limit.
 DSA_DEV bool wait_in_vain(const Ctx& c) {
   const unsigned long long start = clock64();
@@ -245,6 +263,8 @@ DSA_DEV void copies(const Params& P, const Ctx& c, int n_tiles) {
   const int page_mask = (1 << P.page_shift) - 1;
   uint32_t g = 0, u = 0;
   bool ok = true;
+  // the codes that were written before the plan, for copies of the asynchronous kind
+  if (PREFIX) asm volatile("fence.proxy.async.global;" ::: "memory");
   Unit x;
   for (; ok && unit<SPLIT, PREFIX>(P, u, n_tiles, x); ++u) {
     const int blocks = max(x.blocks[0], x.blocks[1]);
@@ -895,6 +915,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
     mbar_init(bar(c, B_DRAIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     c.misc[1] = c.misc[6] = c.misc[7] = 0;
+    if (PREFIX && !wait_planned(P, c)) c.misc[1] = 1;
   }
   if (warp == W_MMA) tmem_alloc(c.sb + SM::MISC, Tmem<D>::COLS);
   tc_fence_before();
@@ -902,10 +923,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tiles_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = (uint32_t)c.misc[0];
   // Launched as a programmatic dependent of rows_kernel, which waited for the plan.  PREFIX: rows_kernel's CTAs allow this
-  // kernel's only behind that wait, and it needs nothing else of theirs; what comes behind this kernel does.
+  // kernel's only behind that wait, so that these find the SMs taken until then, and it needs nothing else of theirs; what
+  // comes behind this kernel does.
   if (!PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
   else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join
-  const int n_tiles = P.header->n_tiles;
+  const int n_tiles = PREFIX && c.misc[1] ? 0 : P.header->n_tiles;
   bool met = false;
   if (warp < W_DQ) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
