@@ -23,8 +23,9 @@ constexpr int LAUNCH_REGS = 128;   // of a thread of the tiles' kernel
 namespace dsa_kv8 {
 
 // ------------------------------------------------------------------------------ join
-// CTAs (x, r) have the query rows of request r; a thread takes 8 dims of a row at a time.  The pieces of
-// a part are joined in their order, and then the parts.
+// A thread takes 8 dims of a row at a time.  The pieces of a part are joined in their order, and then the
+// parts.  By request: CTAs (x, r) have the rows of request r, as many of them as max_q_len asks for; else the
+// CTAs have those of the batch and each row looks for its request.  launch_prefix() chooses.
 constexpr int JOIN_THREADS = 256;
 
 constexpr int AT_ONCE = 4;   // pieces on their way together
@@ -61,7 +62,7 @@ template <int D>
 __device__ __forceinline__ void add_part(const Params& P, const Part& a, int n_tiles, int token, int head, int k, Sum& sum) {
   if (a.q_len * P.group > P.small_rows && P.tile_shares) {
     const int row = (token - a.q0) * P.group + head % P.group, tile = a.tile0 + row / TILE_ROWS, r = row % TILE_ROWS;
-    if (tile >= n_tiles) return;   // lists that do not ascend may give more tiles than there is room for
+    if ((unsigned)tile >= (unsigned)n_tiles) return;   // lists that do not ascend may give more tiles than there is room for
     const int2 by = P.unit_ctas[tile * P.h_kv + head / P.group];
     if (by.x != by.y) {
       for (int b0 = by.x; b0 <= by.y; b0 += AT_ONCE) {
@@ -94,20 +95,31 @@ __device__ __forceinline__ void add_part(const Params& P, const Part& a, int n_t
   sum.add(m, l, v);
 }
 
-template <int D>
+template <int D, bool BY_REQUEST>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Part own = P.parts[P.n_groups + blockIdx.y];
-  const Part shared = P.parts[own.lo > 0 ? own.group : P.n_groups + blockIdx.y];
-  const int n_tiles = P.header->n_tiles;
+  const int n_tiles = P.header->n_tiles, n = P.n_req - P.n_groups;
   // a graph's next launch has the same number
   if (blockIdx.x + blockIdx.y + threadIdx.x == 0) P.header->planned = 0;
-  const long long items = (long long)own.q_len * P.h_q * (D / 8);
+  int r = BY_REQUEST ? blockIdx.y : 0;
+  Part own = P.parts[P.n_groups + r], shared = P.parts[own.lo > 0 ? own.group : P.n_groups + r];
+  const long long items = (long long)(BY_REQUEST ? own.q_len : P.n_tokens) * P.h_q * (D / 8);
   for (long long u = (long long)blockIdx.x * JOIN_THREADS + threadIdx.x; u < items; u += (long long)gridDim.x * JOIN_THREADS) {
     // the heads of a KV head side by side, as their rows are in a piece
     const long long v = u / P.group, row = v / (D / 8);
-    const int k = (int)(v % (D / 8)) * 8, i = (int)(row / P.h_kv);
-    const int head = (int)(row - (long long)i * P.h_kv) * P.group + (int)(u - v * P.group), token = own.q0 + i;
+    const int k = (int)(v % (D / 8)) * 8, i = (int)(row / P.h_kv), token = BY_REQUEST ? own.q0 + i : i;
+    const int head = (int)(row - (long long)i * P.h_kv) * P.group + (int)(u - v * P.group);
+    if (!BY_REQUEST) {
+      int hi = n;   // the last request that begins at or before the token
+      r = 0;
+      while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (min(max(__ldg(P.cu_q + mid), 0), P.n_tokens) <= token) r = mid; else hi = mid;
+      }
+      own = P.parts[P.n_groups + r];
+      if (token < own.q0 || token >= own.q0 + own.q_len) continue;   // of no request, or of one that is skipped
+      shared = P.parts[own.lo > 0 ? own.group : P.n_groups + r];
+    }
     Sum s;
     s.m = M_INIT;
     s.l = 0.f;
@@ -197,9 +209,18 @@ static int launch_prefix(const dsa_kv8_params* p, const Params& P, cudaStream_t 
   if (rc == DSA_OK && P.has_tiles) rc = launch_tiles_of<true>(D, P, st);
   if (rc != DSA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  const long long items = (long long)p->max_q_len * p->h_q * (D / 8);
-  const long long most = 2LL * P.n_shares, x = (items + JOIN_THREADS - 1) / JOIN_THREADS;
-  cfg.gridDim = dim3((unsigned)(x < 1 ? 1 : x > most ? most : x), (unsigned)p->n_req);
+  // By request where that is at most twice the CTAs that the batch's rows need: the search takes 1 to 2.5 us (4 requests
+  // behind 2k 20.6 and 21.6, 64 behind 16k 76.0 and 78.7, 240 verified 51.4 and 52.9).  But 4096 requests of one query
+  // behind 256 tokens, 16/2 heads, take 5684 by request where max_q_len is n_tokens, and 182 without; 64 decoded
+  // requests beside a chunk of 2048 queries 266 and 197.
+  const long long most = 2LL * P.n_shares, per_query = (long long)p->h_q * (D / 8);
+  auto needed = [&](long long queries) { return (queries * per_query + JOIN_THREADS - 1) / JOIN_THREADS; };
+  auto grid = [&](long long queries) {
+    const long long x = needed(queries);
+    return x < 1 ? 1 : x > most ? most : x;
+  };
+  const bool by_request = grid(p->max_q_len) * p->n_req <= 2 * needed(p->n_tokens);
+  cfg.gridDim = by_request ? dim3((unsigned)grid(p->max_q_len), (unsigned)p->n_req) : dim3((unsigned)grid(p->n_tokens));
   cfg.blockDim = dim3(JOIN_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -207,7 +228,8 @@ static int launch_prefix(const dsa_kv8_params* p, const Params& P, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, P) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  const cudaError_t rc1 = by_request ? cudaLaunchKernelEx(&cfg, join_kernel<D, true>, P) : cudaLaunchKernelEx(&cfg, join_kernel<D, false>, P);
+  return rc1 == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace dsa_kv8
