@@ -31,4 +31,11 @@ inline int gb300_sms(int* sms) {
   return DSA_OK;
 }
 
+// SMs of the current device, of whatever capability: for sizes of workspaces.
+inline int current_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
 }  // namespace dsa

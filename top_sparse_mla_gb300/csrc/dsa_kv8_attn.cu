@@ -25,9 +25,18 @@
 // the result's own rounding hides it.  Against 64 bits bf16 outputs are off by 0.0017 of their norm,
 // with w in fp32 by the same; fp16 ones under a window of 640 by 0.00023, in fp32 by 0.00021.
 
+#include "device.cuh"
 #include "dsa_kv8_rows.cuh"
 
 namespace dsa_kv8 {
+
+static void set_clusters(Params& P, const dsa_kv8_params* p, int max_tiles, int sms) {
+  // cached tokens that a tile's rows may see
+  const long long seen = P.window > 0 ? (long long)P.window + TILE_ROWS / P.group + 1 + STEP : P.cap;
+  const long long pairs = (long long)max_tiles * p->h_kv;
+  P.cluster = P.has_tiles && 2 * pairs <= sms ? cluster_size(p->d, pairs, (int)((min(seen, (long long)P.cap) + 127) / 128)) : 0;
+  P.n_ctas = P.cluster ? (int)pairs * P.cluster : sms;
+}
 
 template <int D>
 static int launch_all(const dsa_kv8_params* p, const Params& P, bool wide, cudaStream_t st) {
@@ -62,7 +71,7 @@ int dsa_kv8_params_init(dsa_kv8_params* p, int32_t n_tokens, int32_t n_req, int3
 
 size_t dsa_kv8_attn_workspace_size(const dsa_kv8_params* p, int num_sms) {
   if (dsa_kv8::check(p) != DSA_OK) return 0;
-  if (num_sms <= 0 && dsa_kv8::current_sms(&num_sms) != DSA_OK) return 0;
+  if (num_sms <= 0 && dsa::current_sms(&num_sms) != DSA_OK) return 0;
   return dsa_kv8::layout(p, num_sms).bytes;
 }
 
@@ -76,7 +85,7 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   const Call c{q, q_ld, q_hd, k_pool, v_pool, k_scale, v_scale, block_table, table_ld, cu_q, kv_lens, out, out_ld, out_hd, lse, workspace};
   if (bad_call(c, p)) return DSA_ERR_INVALID_ARG;
   int sms = 0;
-  const int rc0 = gb300_sms(&sms);
+  const int rc0 = dsa::gb300_sms(&sms);
   if (rc0 != DSA_OK) return rc0;
   const Layout L = layout(p, sms);
   if (workspace_bytes < L.bytes) return DSA_ERR_WORKSPACE_TOO_SMALL;
@@ -85,7 +94,8 @@ int dsa_kv8_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const void* k_po
   if (p->n_tokens == 0 || p->n_req == 0)
     return cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
   const bool is_wide = wide(p, sms);
-  const Params P = params_of(c, p, L, sms, is_wide);
+  Params P = params_of(c, p, L, is_wide);
+  set_clusters(P, p, L.max_tiles, sms);
   const auto plan_smem = [](int n_req) { return (size_t)(n_req + 1) * 2 * sizeof(long long); };
   const size_t smem = plan_smem(p->n_req), most_smem = plan_smem(DSA_KV8_MAX_REQ);
   const int rc1 = P.own_plan ? launch(plan_kernel<FEW_THREADS>, 1, FEW_THREADS, smem, most_smem, st, P, false)

@@ -238,7 +238,7 @@ extern "C" {
 
 size_t dsa_kv8_prefix_workspace_size(const dsa_kv8_params* p, int32_t n_groups, int num_sms) {
   if (dsa_kv8::check_prefix(p, n_groups) != DSA_OK) return 0;
-  if (num_sms <= 0 && dsa_kv8::current_sms(&num_sms) != DSA_OK) return 0;
+  if (num_sms <= 0 && dsa::current_sms(&num_sms) != DSA_OK) return 0;
   return dsa_kv8::prefix_layout(p, n_groups, num_sms).bytes;
 }
 
@@ -262,7 +262,7 @@ int dsa_kv8_prefix_attn_fwd(const void* q, int64_t q_ld, int64_t q_hd, const voi
   cudaStream_t st = (cudaStream_t)stream;
   if (p->n_tokens == 0 || p->n_req == 0)
     return cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-  Params P = params_of(c, p, L.base, sms, false);
+  Params P = params_of(c, p, L.base, false);
   P.n_req = p->n_req + n_groups;
   P.parts = reinterpret_cast<Part*>(ws + L.parts);
   P.row_parts = reinterpret_cast<int*>(ws + L.row_parts);

@@ -1145,12 +1145,6 @@ static int launch_rows(const Params& P, bool wide, cudaStream_t st) {
 // positions stay below 2^31 with room for a step and a tile behind the last one
 constexpr long long MOST_TOKENS = (1LL << 31) - 1024;
 
-static int current_sms(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
-  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-}
-
 // The arguments of a call that both entry points have.
 struct Call {
   const void* q;
@@ -1180,25 +1174,7 @@ static bool bad_call(const Call& c, const dsa_kv8_params* p) {
                             !aligned(c.v_pool, 16) || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4));
 }
 
-// SMs of the current device, which has to be of compute capability 10.3
-static int gb300_sms(int* sms) {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return DSA_ERR_UNSUPPORTED_DEVICE;
-  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-}
-
-static void set_clusters(Params& P, const dsa_kv8_params* p, int max_tiles, int sms) {
-  // cached tokens that a tile's rows may see
-  const long long seen = P.window > 0 ? (long long)P.window + TILE_ROWS / P.group + 1 + STEP : P.cap;
-  const long long pairs = (long long)max_tiles * p->h_kv;
-  P.cluster = P.has_tiles && 2 * pairs <= sms ? cluster_size(p->d, pairs, (int)((min(seen, (long long)P.cap) + 127) / 128)) : 0;
-  P.n_ctas = P.cluster ? (int)pairs * P.cluster : sms;
-}
-
-static Params params_of(const Call& c, const dsa_kv8_params* p, const Layout& L, int sms, bool is_wide) {
+static Params params_of(const Call& c, const dsa_kv8_params* p, const Layout& L, bool is_wide) {
   Params P = {};
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   P.q = static_cast<const uint16_t*>(c.q);
@@ -1236,7 +1212,6 @@ static Params params_of(const Call& c, const dsa_kv8_params* p, const Layout& L,
   P.window = p->window < P.cap ? p->window : 0;
   P.fp16 = p->type == DSA_KV8_FP16;
   P.has_tiles = has_tiles(p);
-  set_clusters(P, p, L.max_tiles, sms);
   P.small_rows = 8 * row_tiles(p);
   P.n_shares = L.n_shares;
   const int warps = is_wide ? ROW_WARPS * ctas_per_sm(p->d, row_tiles(p)) : ROW_WARPS;

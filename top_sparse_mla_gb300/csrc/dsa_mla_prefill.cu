@@ -979,12 +979,6 @@ static Layout layout(const dsa_mla_params* p, int sms) {
   return L;
 }
 
-static int current_sms(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
-  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-}
-
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1069,7 +1063,7 @@ int dsa_mla_params_init(dsa_mla_params* p, int32_t n_tokens, int32_t n_keys, int
 
 size_t dsa_mla_prefill_workspace_size(const dsa_mla_params* p, int num_sms) {
   if (dsa_mla::check(p) != DSA_OK) return 0;
-  if (num_sms <= 0 && dsa_mla::current_sms(&num_sms) != DSA_OK) return 0;
+  if (num_sms <= 0 && dsa::current_sms(&num_sms) != DSA_OK) return 0;
   return dsa_mla::layout(p, num_sms).bytes;
 }
 
