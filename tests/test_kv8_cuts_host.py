@@ -20,14 +20,15 @@ extern "C" int plan(const unsigned* len, unsigned n_tiles, unsigned h_kv, unsign
   using namespace dsa_kv8;
   std::vector<unsigned> before(n_tiles + 1), front(n_tiles + 1), ctas(n_tiles);
   for (unsigned i = 0; i < n_tiles; ++i) before[i + 1] = before[i] + len[i];
-  const unsigned total = before[n_tiles] * h_kv, each = equal_blocks(total, n_ctas);
+  const unsigned total = before[n_tiles] * h_kv;
   unsigned longest = 0;
   for (unsigned i = 0; i < n_tiles; ++i) {
     ctas[i] = own_ctas(len[i], total, n_ctas);
     front[i + 1] = front[i] + ctas[i] * h_kv;
     longest = std::max(longest, (len[i] + ctas[i] - 1) / ctas[i]);
   }
-  const Cuts c{before.data(), front.data(), ctas.data(), n_tiles, h_kv, each, own_pieces(front[n_tiles], n_ctas, longest, each)};
+  const Cuts c{before.data(), front.data(), ctas.data(), n_tiles, h_kv, equal_costs(total, n_tiles * h_kv, n_ctas),
+               own_pieces(front[n_tiles], n_ctas, longest, equal_blocks(total, n_ctas))};
   for (unsigned b = 0; b <= n_ctas; ++b) cuts[b] = c.cut(b, units[b]);
   for (unsigned u = 0; u < n_tiles * h_kv; ++u) c.ctas_of(u, by[2 * u], by[2 * u + 1]);
   return c.own;
@@ -61,17 +62,21 @@ def _check(plan, lens, h_kv, n_ctas):
         starts += [starts[-1] + n * (i + 1) for i in range(h_kv)]
     total = starts[-1]
     assert cuts[0] == 0 and cuts[n_ctas] == total and all(a <= b for a, b in zip(cuts, cuts[1:])), what
-    owners = [[] for _ in by]
+    owners, begun = [[] for _ in by], [0] * n_ctas
     for b in range(n_ctas):
         # as a CTA walks: from the unit that its cut names on, up to the next cut
         u, a, e = units[b], cuts[b], cuts[b + 1]
         assert a == e or starts[u] <= a < starts[u + 1], what
         while u < len(by) and starts[u] < e:
             assert min(e, starts[u + 1]) > max(a, starts[u]), what
+            begun[b] += starts[u] >= a
             owners[u].append(b)
             u += 1
     for u, (first, last) in enumerate(by):
         assert owners[u] == list(range(first, last + 1)) and last < n_ctas, (what, u, first, last, owners[u])
+    # no CTA gets many units of its own while others have one: a unit costs it four blocks and more
+    cost = [4 * n + e - a for n, a, e in zip(begun, cuts, cuts[1:])]
+    assert own or max(cost) <= max(6, -(-(total + 4 * len(by)) // n_ctas)) + 4, (what, max(cost))
     return own
 
 

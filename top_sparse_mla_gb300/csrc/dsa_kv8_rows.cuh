@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       return t;
     };
     if (PREFIX && P.tile_shares) {
-      // no order, and every CTA an equal share of the blocks of all heads of all tiles
+      // no order, and every CTA an equal share of all units, or each unit CTAs of its own (dsa_kv8_cuts.h)
       for (int r = tid; r < n; r += THREADS) P.parts[r].tile0 = (int)s_tile[r];
       // (all blocks of all heads are below 2^30: the 64-bit divisions of this kernel's beginning take 600 cycles each)
       unsigned* s_before = reinterpret_cast<unsigned*>(s_tile + n + 1);   // blocks of a head in front of each tile, [n_tiles + 1]
@@ -343,8 +343,6 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       long long all_blocks = 0, all_ctas = 0;
       unsigned before = (unsigned)scan<THREADS>(sum, s_step_warp, all_blocks);
       const unsigned every = (unsigned)all_blocks, total = every * h_kv;
-      // Every CTA as many blocks, or each unit CTAs of its own (own_pieces())
-      const unsigned each = equal_blocks(total, n_ctas);
       if (tid == 0) s_longest = 0;
       __syncthreads();
       unsigned some_ctas = 0;
@@ -366,8 +364,8 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
       }
       if (tid == 0) s_front[n_tiles] = (unsigned)all_ctas;
       __syncthreads();
-      const Cuts cuts{s_before, s_front, s_ctas, (unsigned)n_tiles, h_kv, each,
-                      own_pieces((unsigned long long)all_ctas, n_ctas, (unsigned)s_longest, each)};
+      const Cuts cuts{s_before, s_front, s_ctas, (unsigned)n_tiles, h_kv, equal_costs(total, n_tiles * h_kv, n_ctas),
+                      own_pieces((unsigned long long)all_ctas, n_ctas, (unsigned)s_longest, equal_blocks(total, n_ctas))};
       for (unsigned b = tid; b <= n_ctas; b += THREADS) {
         unsigned u;
         P.tile_cuts[b] = cuts.cut(b, u);
