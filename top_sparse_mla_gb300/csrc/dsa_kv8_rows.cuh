@@ -1136,8 +1136,10 @@ template <int D, int NT, bool PREFIX>
 static int launch_rows(const Params& P, bool wide, cudaStream_t st) {
   constexpr int W = ROW_WARPS, WW = D == 128 ? W * ctas_per_sm(D, NT) : W;
   constexpr size_t smem = sizeof(RowSmem<D, NT, W>), wide_smem = sizeof(RowSmem<D, NT, WW>);
-  return wide ? launch(rows_kernel<D, NT, WW, PREFIX>, P.n_shares, 32 * WW, wide_smem, wide_smem, st, P, true)
-              : launch(rows_kernel<D, NT, W, PREFIX>, P.n_shares, 32 * W, smem, smem, st, P, true);
+  if constexpr (!PREFIX) {   // the call for shared prefixes has none of these
+    if (wide) return launch(rows_kernel<D, NT, WW, false>, P.n_shares, 32 * WW, wide_smem, wide_smem, st, P, true);
+  }
+  return launch(rows_kernel<D, NT, W, PREFIX>, P.n_shares, 32 * W, smem, smem, st, P, true);
 }
 
 // positions stay below 2^31 with room for a step and a tile behind the last one
