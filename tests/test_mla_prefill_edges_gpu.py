@@ -31,3 +31,16 @@ def test_a_query_whose_every_score_is_minus_infinity_spoils_its_row(lens, rows, 
     empty = torch.isneginf(want_l)
     assert out[~keep & ~empty].isnan().all() and lse[~keep & ~empty].isnan().all()
     assert (out[~keep & empty] == 0).all() and torch.isneginf(lse[~keep & empty]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("how", [SPLIT, WHOLE], ids=["split", "whole"])
+def test_a_row_with_one_key_has_its_value_as_it_is(how, dtype):
+    # its weight is 1, whatever its score
+    lens = [(1, 1)] * 40 + [(3, 3), (130, 130), (300, 300), (2, 1), (1, 700)]
+    c = Case(52, lens, h=3, dtype=dtype)
+    out, lse = _check(c, **how)
+    v = c.up[:, :, 128:].cuda()
+    for r, (ql, kv) in enumerate(lens[:-1]):
+        row, key = int(c.cu[r]) + ql - kv, int(c.ck[r])
+        assert torch.equal(out[row], v[key]), r

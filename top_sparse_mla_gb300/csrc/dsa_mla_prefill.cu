@@ -35,10 +35,10 @@
 // Every wait is bounded: where one runs out the call's status gets DSA_STATUS_WAIT_TIMEOUT
 // and the CTA's roles stop, drain the tensor core and free its memory.
 //
-// Scores become u = S * (softmax_scale * log2 e) - m and weights 2^u, with m an integer that was
-// the row's maximum, rounded down, when it was last set.  It is set anew, and O rescaled by a
-// power of two, exactly, when a weight would pass 2^15, so that each fits fp16: rare behind the
-// first block.
+// Scores become u = S * (softmax_scale * log2 e) - m and weights 2^u, with m the maximum of the row's first
+// scores, so that a row with one key has a weight of 1, which nothing rounds, and its value as it is.  m is
+// raised, by whole numbers, and O rescaled by a power of two, exactly, when a weight would pass 2^15, so
+// that each fits fp16: rare behind the first block.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -715,7 +715,7 @@ DSA_DEV void softmax(const Params& P, const Ctx& c, uint32_t tmem, int n_tiles, 
       if (__any_sync(0xFFFFFFFFu, fresh || top > MOST)) {
         const bool up = top > (fresh ? -INFINITY : LAG);
         // by delta, not by m's rounded step: from 2^23 on m + delta is rounded
-        const float delta = up ? floorf(top) : 0.f;
+        const float delta = up ? (fresh ? top : floorf(top)) : 0.f;
         const float f = (up && !fresh) ? ex2(-delta) : 1.0f;
         if (up) fresh = false;
         m += delta;
