@@ -392,7 +392,10 @@ DSA_DEV void dequant(const Params& P, const Ctx& c, int n_tiles) {
             if (!((mask >> (row >> 4)) & 1u) || (kv == 1 && (j < seen_lo || j >= x.t.hi))) r[p] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        arrive_w(c, B_RAWFREE + kv);   // the codes are in registers
+        // The codes are in registers once this fence is passed: nothing else keeps a load in front of the copy that comes next
+        // to its place, which is of another kind (of proxy) than loads and stores.
+        fence_async_smem();
+        arrive_w(c, B_RAWFREE + kv);
         if (!wait_w(c, (kv ? B_VFREE : B_KFREE) + buf, ((g >> 1) & 1) ^ 1)) return;
         const uint32_t to = store_at + (kv ? SM::V : SM::K) + buf * SM::OPERAND;
 #pragma unroll
