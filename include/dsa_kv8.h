@@ -45,6 +45,8 @@
  *   out[t][h] = sum_j softmax_j(softmax_scale * q[t][h].k_j) v_j
  *   lse[t][h] = natural-log sum-exp of the scaled scores (-inf, and out = 0, for a row
  *               that sees nothing)
+ * A query that is not finite makes its own row NaN, or, where every score that it sees is
+ * -infinity, 0 with an lse of -inf; no other row.
  * A table entry that is negative or >= n_pages holds nothing: its positions are not seen.
  * Rows of q and out that belong to no request are neither read nor written.  Codes of
  * rows that some query row of the request sees are finite, with positive finite scales

@@ -17,6 +17,11 @@
  *   prefix_lens  int32 [n_groups] (negative: 0)
  *   n_groups     0 (neither array is read) to DSA_KV8_MAX_GROUPS; n_req + n_groups <= DSA_KV8_MAX_REQ
  *   window has to be 0
+ * What the call saves is reading, (n - 1) times a prefix for a group of n requests; it costs
+ * two kernels more and a pass over O in fp32.  On a GB300 it is the faster one for groups of
+ * eight and more from about 250 MB of codes saved in a call on (16 requests behind 8 k tokens
+ * or 64 behind 2 k, 8 KV heads of 128), for groups of four from about 1 GB; for pairs, for
+ * prompts of some hundred tokens and for chunks of 128 queries and more, dsa_kv8_attn_fwd is.
  * All other arguments, the status word of the workspace, what is left unwritten, and the rules
  * for streams and graphs are those of dsa_kv8_attn_fwd.  Beside its error, O and the sums of
  * the two parts of a row, the shared tokens and its own, are joined in fp32.

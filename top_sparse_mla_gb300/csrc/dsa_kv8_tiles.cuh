@@ -534,8 +534,8 @@ DSA_DEV bool sees_any(const Params& P, const Unit& x, int blocks, int pos) {
 // neighbours of a row: a lane for a row touches 32 lines with every load, which took a
 // 2123-token prefill 109 us in place of 104.
 //
-// A query that is not finite makes its row NaN, also by way of missing pages (0 * NaN); where the
-// row sees nothing it has to be 0, and the query is taken as 0.
+// A query that is not finite makes its row NaN (or 0, by scores of -infinity alone), also by way of
+// missing pages (0 * NaN); where the row sees nothing it has to be 0, and the query is taken as 0.
 template <int D, bool FP16>
 DSA_DEV float queries(const Params& P, const Unit& x, int blocks, int pos, const uint16_t* mine, uint32_t tile, int row0) {
   constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;   // lanes of a row, rows of a load; LANES loads
